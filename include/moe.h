@@ -16,6 +16,12 @@
  *   moe_grouped_gemm_fp8_swiglu (up-projection with the step above in its epilogue) -> FP8 + 1x128 scales
  *   moe_unpermute_combine  topk_weights-weighted sum back to token order
  *
+ * before it, moe_router_topk (router logits -> topk_ids and topk_weights);
+ * beside it, moe_gemm_fp8 (the dense product of an expert that every token
+ * uses, or of any projection; arbitrary fp32 block scales); and for training
+ * the gradients moe_unpermute_combine_bwd, moe_router_topk_bwd, and
+ * moe_quant_act_t, which prepares the operands of moe_gemm_fp8's weight gradient;
+ *
  * plus weight-preparation calls (moe_quant_weight_fp8 / _int4 / _fp4 / _int8,
  * moe_pack_weight_fp8 / _int4 / _fp4 / _bf16) that turn bf16 expert weights
  * into the formats the GEMMs read, and moe_quant_act_int8 (the INT8 variant's
@@ -507,6 +513,124 @@ moe_status moe_unpermute_combine(const uint16_t* Y, int64_t y_rows,
                                  const float* topk_weights,
                                  int T, int k, int N,
                                  uint16_t* Z, void* stream);
+
+/* moe_unpermute_combine_bwd: the gradient of moe_unpermute_combine.
+ *     dweights[t, r] = sum_n dZ[t, n] * Y[output_index[t, r], n]     (fp32; 0 for a skipped slot)
+ *     dY[p, n]       = bf16_rne( sum over the slots (t, r) that name row p, in route order
+ *                                t*k + r, of topk_weights[t, r] * dZ[t, n] )
+ *   Slots with output_index < 0 or >= y_rows are skipped.  Rows of dY that no
+ *   slot names (padding) are never written.  moe_route_pack gives each route a
+ *   row of its own; rows named by several slots get the whole sum (in fp32, one
+ *   rounding), more slowly.
+ *     dZ [T, N], Y and dY [y_rows, N] bf16 (16-byte aligned, N % 8 == 0);
+ *     output_index [T, k] int32; topk_weights and dweights [T, k] fp32.
+ *   dY may be NULL (topk_weights is then not read and may be NULL too), and so
+ *   may dweights (Y then), but not both.  Outputs must not overlap inputs.
+ *   workspace: at least moe_unpermute_combine_bwd_workspace_bytes(T, k, y_rows)
+ *   bytes, 8-byte aligned (may be NULL when that is 0, or when dY is); calls
+ *   that overlap in time must not share it.  T == 0 is a no-op. */
+int64_t moe_unpermute_combine_bwd_workspace_bytes(int T, int k, int64_t y_rows);
+moe_status moe_unpermute_combine_bwd(const uint16_t* dZ, const uint16_t* Y, int64_t y_rows,
+                                     const int32_t* output_index, const float* topk_weights,
+                                     int T, int k, int N,
+                                     uint16_t* dY, float* dweights,
+                                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Element types of arguments that come in more than one. */
+enum { MOE_F32 = 0, MOE_BF16 = 1 };
+
+/* moe_router_topk: the router's choice, from the gate projection's logits to
+ * the topk_ids and topk_weights that moe_route_pack and moe_unpermute_combine
+ * take.  Per token (row x of E logits):
+ *   score  MOE_SCORE_SOFTMAX  s_e = exp(x_e) / sum_e' exp(x_e')
+ *          MOE_SCORE_SIGMOID  s_e = 1 / (1 + exp(-x_e))
+ *   key    s_e + bias[e], or x_e itself when bias is NULL (the scores' order).
+ *          The bias (a load-balance term) decides the choice only, not the
+ *          weights.
+ *   groups n_group > 1: the experts form n_group groups of E/n_group consecutive
+ *          ones; the topk_group groups with the largest group scores are kept
+ *          (ties: the lowest group).  Group score: the largest key of the group
+ *          (group_top 1), or the sum of its two largest of s_e (+ bias[e])
+ *          (group_top 2; of a group with one expert available, that one's).
+ *   slots  the k largest keys among the kept groups, descending, ties to the
+ *          lowest expert; topk_ids[t, r] = expert of slot r.
+ *   weight renormalize: scale * s_r / (sum over the row's slots of s), else scale * s_r.
+ *   Keys and group scores are ordered as their 64-bit values; weights are fp32,
+ *   a few ulps from the exact value, without underflow in the renormalised form.
+ *   A logit of -inf or NaN (or a key of -inf or NaN) takes the expert out for
+ *   that token; if fewer than k are available, the slots left over get
+ *   topk_ids -1 (which moe_route_pack skips) and weight 0.  Of logits of +inf
+ *   softmax gives each an equal share.
+ *     logits [T, E], fp32 or bf16 (logits_type), rows logits_ld elements apart
+ *     (>= E); bias [E] fp32 or NULL; topk_ids [T, k] int32 and topk_weights
+ *     [T, k] fp32, 4-byte aligned.
+ *   1 <= E <= 1024, 1 <= k <= 64, n_group <= 64 dividing E,
+ *   k <= topk_group * (E / n_group), scale finite.  T == 0 is a no-op. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+moe_status moe_router_topk(const void* logits, int logits_type, int64_t logits_ld, const float* bias,
+                           int T, int E, int k, int score, int n_group, int topk_group, int group_top,
+                           int renormalize, float scale,
+                           int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* moe_router_topk_bwd: the gradient of moe_router_topk's weights with respect
+ * to the logits, for the choice it made (the choice itself and the bias have
+ * none).  With g = dweights, w and s the weight and score of a slot:
+ *   renormalize           dx_r = w_r * (g_r - sum_j g_j w_j / scale), times (1 - s_r) for sigmoid scores
+ *   sigmoid as it is      dx_r = scale * g_r * s_r * (1 - s_r)
+ *   softmax as it is      dx_e = scale * s_e * ([e selected] g_e - sum_j g_j s_j), for every expert
+ *   and 0 for every other expert of the row: dlogits is written whole.  Slots
+ *   with topk_ids outside [0, E), or whose logit is -inf or NaN, count for
+ *   nothing; an expert named by several slots gets the sum over them.
+ *     logits and dlogits [T, E] of the type logits_type, rows logits_ld and
+ *     dlogits_ld apart; topk_ids [T, k] int32; dweights [T, k] fp32.  Limits as
+ *   for moe_router_topk; dlogits must not overlap the inputs. */
+moe_status moe_router_topk_bwd(const void* logits, int logits_type, int64_t logits_ld,
+                               const int32_t* topk_ids, const float* dweights,
+                               int T, int E, int k, int score, int renormalize, float scale,
+                               void* dlogits, int64_t dlogits_ld, void* stream);
+
+/* moe_gemm_fp8: dense FP8 product, "NT" (both operands K-contiguous), with an
+ * fp32 scale per block of 128 (the block-scaled recipe of moe_grouped_gemm_fp8
+ * for one weight matrix, and for scales that need not be powers of two, as
+ * checkpoints quantised with amax / 448 hold them).
+ *     D[m, n] = C[m, n] + sum_kb (SFA[m, kb] * SFW[n / gran_n, kb]) *
+ *                         sum_{k in kb} dec(A[m, k]) * dec(W[n, k])
+ *   each block's sum, the scales' product and the accumulation in fp32.
+ *     A [M, K] E4M3FN, rows lda bytes apart; SFA [M, K/128] fp32.
+ *     W [N, K] E4M3FN, rows ldw bytes apart; SFW [ceil(N/gran_n), K/128] fp32,
+ *       gran_n 128 (128x128 blocks) or 1 (1x128, like A's).
+ *     D [M, N] of type out_type (MOE_BF16, rounded to nearest even, or MOE_F32),
+ *       rows ldd elements apart; nothing past column N is written.
+ *     C [M, N] fp32, rows ldc elements apart, or NULL for none; needs
+ *       out_type MOE_F32.  C may be D itself (with ldc = ldd).
+ *   Forward: A activations, W weights.  Input gradient: A the output gradient
+ *   (moe_quant_act), W the transposed weight.  Weight gradient [N, K]: A and W
+ *   the output gradient and the input as moe_quant_act_t writes them, gran_n 1.
+ *   Requires K % 128 == 0, lda and ldw multiples of 16, >= K and < 2^23; A and W
+ *   16-byte aligned, D aligned to its type; M and N < 2^30.  M == 0 is a no-op.
+ *   D must not overlap A, W or the scales.
+ *   workspace: at least moe_gemm_fp8_workspace_bytes(M, N, K) bytes, 16-byte
+ *   aligned (may be NULL when that is 0; it is not 0 only where few output tiles
+ *   make it pay to split K); calls that overlap in time must not share it.
+ *   Results are deterministic. */
+int64_t moe_gemm_fp8_workspace_bytes(int M, int N, int K);
+moe_status moe_gemm_fp8(const uint8_t* A, int64_t lda, const float* SFA,
+                        const uint8_t* W, int64_t ldw, const float* SFW, int gran_n,
+                        void* D, int out_type, int64_t ldd,
+                        const float* C, int64_t ldc, int M, int N, int K,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/* moe_quant_act_t: transposing 1x128 FP8 quantisation along the rows (tokens)
+ * of x, for products that contract over them (moe_gemm_fp8's weight gradient).
+ *   x [M, K] bf16, rows ldx elements apart.  With Mp = M rounded up to 128:
+ *   qt [K, Mp] E4M3FN codes and sft [K, Mp/128] fp32: row k of qt is column k of
+ *   x, quantised by the rule of moe_quant_act (power-of-two scale per 128
+ *   consecutive m), rows of x past M counting as zeros.
+ *   Requires K % 8 == 0, ldx % 8 == 0 and >= K, x and qt 16-byte aligned, sft
+ *   4-byte aligned; the outputs must not overlap x.  M == 0 is a no-op. */
+moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx,
+                           uint8_t* qt, float* sft, void* stream);
 
 /* moe_stream_read: a measurement helper, not a step of the method.  Reads the
  * `bytes` bytes at `buf` once with 16-byte nontemporal loads (eight in

@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 LAYOUT_CONTIGUOUS = 0
 LAYOUT_MASKED = 1
 WEIGHTS_PACKED = 0x10  # flag for moe_grouped_gemm_fp8's layout: W in moe_pack_weight_fp8 order
+F32, BF16 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
 DEV_ID_RANGE = 1
 DEV_CAPACITY = 2
 
@@ -66,6 +68,18 @@ SIGNATURES = {
     "moe_grouped_gemm_int8": (_c_i32, [ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                        ctypes.c_int, _c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
     "moe_unpermute_combine": (_c_i32, [_vp, _c_i64, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp]),
+    "moe_unpermute_combine_bwd_workspace_bytes": (_c_i64, [ctypes.c_int, ctypes.c_int, _c_i64]),
+    "moe_unpermute_combine_bwd": (_c_i32, [_vp, _vp, _c_i64, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                           _vp, _vp, _vp, _c_i64, _vp]),
+    "moe_router_topk": (_c_i32, [_vp, ctypes.c_int, _c_i64, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                 ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                 ctypes.c_float, _vp, _vp, _vp]),
+    "moe_router_topk_bwd": (_c_i32, [_vp, ctypes.c_int, _c_i64, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                     ctypes.c_int, ctypes.c_int, ctypes.c_float, _vp, _c_i64, _vp]),
+    "moe_gemm_fp8_workspace_bytes": (_c_i64, [ctypes.c_int] * 3),
+    "moe_gemm_fp8": (_c_i32, [_vp, _c_i64, _vp, _vp, _c_i64, _vp, ctypes.c_int, _vp, ctypes.c_int, _c_i64,
+                              _vp, _c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _c_i64, _vp]),
+    "moe_quant_act_t": (_c_i32, [_vp, _c_i64, ctypes.c_int, _c_i64, _vp, _vp, _vp]),
     "moe_stream_read_words": (ctypes.c_int, []),
     "moe_stream_read": (_c_i32, [_vp, _c_i64, _vp, _vp]),
 }
@@ -122,6 +136,29 @@ def _dev(t, name, dtype=None, ndim=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+
+
+def _rows(t, name, dtypes):
+    """A 2-D GPU tensor whose rows are contiguous; returns its row stride in elements."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _one_device(fn, stream, *tensors):
+    """The tensors lie on one device, the stream's (or the current one): a kernel is launched there."""
+    dev = torch.cuda.current_device() if stream is None else stream.device.index
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the stream is not on the current device")
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{fn}: a tensor is on {t.device}, the call on cuda:{dev}")
 
 
 def _row_bytes(t) -> int:
@@ -445,6 +482,122 @@ def moe_unpermute_combine(Y, output_index, topk_weights, Z, stream=None):
         raise ValueError("moe_unpermute_combine: shape mismatch")
     _check(load().moe_unpermute_combine(_ptr(Y), Y.shape[0], _ptr(output_index), _ptr(topk_weights), T, k, N,
                                         _ptr(Z), _stream(stream)), "moe_unpermute_combine")
+
+
+def moe_unpermute_combine_bwd_workspace_bytes(T: int, k: int, y_rows: int) -> int:
+    return int(load().moe_unpermute_combine_bwd_workspace_bytes(T, k, y_rows))
+
+
+def moe_unpermute_combine_bwd(dZ, Y, output_index, topk_weights, dY, dweights, workspace=None, stream=None):
+    """dZ bf16 [T, N] -> dY bf16 [y_rows, N] (rows that a slot names) and dweights float32 [T, k].  Either output may
+    be None: without dY topk_weights may be None, without dweights Y may be None."""
+    _dev(dZ, "dZ", torch.bfloat16, 2), _dev(Y, "Y", torch.bfloat16, 2)
+    _dev(output_index, "output_index", torch.int32, 2), _dev(topk_weights, "topk_weights", torch.float32, 2)
+    _dev(dY, "dY", torch.bfloat16, 2), _dev(dweights, "dweights", torch.float32, 2), _dev(workspace, "workspace")
+    T, N = dZ.shape
+    k = output_index.shape[1]
+    if dY is None and dweights is None:
+        raise ValueError("moe_unpermute_combine_bwd: dY and dweights are both None")
+    if (dweights is not None and Y is None) or (dY is not None and topk_weights is None):
+        raise ValueError("moe_unpermute_combine_bwd: dweights needs Y, dY needs topk_weights")
+    y_rows = (Y if Y is not None else dY).shape[0]
+    for name, t, shape in (("output_index", output_index, (T, k)), ("topk_weights", topk_weights, (T, k)),
+                           ("dweights", dweights, (T, k)), ("Y", Y, (y_rows, N)), ("dY", dY, (y_rows, N))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"moe_unpermute_combine_bwd: {name} is {tuple(t.shape)}, needs {shape}")
+    _one_device("moe_unpermute_combine_bwd", stream, dZ, Y, output_index, topk_weights, dY, dweights, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().moe_unpermute_combine_bwd(_ptr(dZ), _ptr(Y), y_rows, _ptr(output_index), _ptr(topk_weights), T, k, N,
+                                            _ptr(dY), _ptr(dweights), _ptr(workspace), ws_bytes, _stream(stream)),
+           "moe_unpermute_combine_bwd")
+
+
+def _score(fn, score):
+    if score not in SCORES:
+        raise ValueError(f"{fn}: score must be one of {sorted(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def moe_router_topk(logits, topk_ids, topk_weights, score: str = "softmax", bias=None, n_group: int = 1,
+                    topk_group: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                    stream=None):
+    """logits float32 or bf16 [T, E] (rows may be strided) -> topk_ids int32 and topk_weights float32 [T, k]; bias
+    float32 [E] (in the choice only).  See include/moe.h."""
+    fn = "moe_router_topk"
+    ld = _rows(logits, "logits", (torch.float32, torch.bfloat16))
+    _dev(topk_ids, "topk_ids", torch.int32, 2), _dev(topk_weights, "topk_weights", torch.float32, 2)
+    _dev(bias, "bias", torch.float32, 1)
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    if topk_ids.shape[0] != T or tuple(topk_weights.shape) != (T, k) or (bias is not None and bias.shape[0] != E):
+        raise ValueError(f"{fn}: shape mismatch")
+    sc = _score(fn, score)
+    _one_device(fn, stream, logits, topk_ids, topk_weights, bias)
+    _check(load().moe_router_topk(_ptr(logits), BF16 if logits.dtype == torch.bfloat16 else F32, ld, _ptr(bias), T, E,
+                                  k, sc, n_group, topk_group, group_top, int(renormalize), scale, _ptr(topk_ids),
+                                  _ptr(topk_weights), _stream(stream)), fn)
+
+
+def moe_router_topk_bwd(logits, topk_ids, dweights, dlogits, score: str = "softmax", renormalize: bool = True,
+                        scale: float = 1.0, stream=None):
+    """dweights float32 [T, k] -> dlogits [T, E], of logits' type (rows may be strided), for the choice topk_ids."""
+    fn = "moe_router_topk_bwd"
+    ld = _rows(logits, "logits", (torch.float32, torch.bfloat16))
+    ldd = _rows(dlogits, "dlogits", (logits.dtype,))
+    _dev(topk_ids, "topk_ids", torch.int32, 2), _dev(dweights, "dweights", torch.float32, 2)
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    if tuple(dlogits.shape) != (T, E) or topk_ids.shape[0] != T or tuple(dweights.shape) != (T, k):
+        raise ValueError(f"{fn}: shape mismatch")
+    sc = _score(fn, score)
+    _one_device(fn, stream, logits, topk_ids, dweights, dlogits)
+    _check(load().moe_router_topk_bwd(_ptr(logits), BF16 if logits.dtype == torch.bfloat16 else F32, ld,
+                                      _ptr(topk_ids), _ptr(dweights), T, E, k, sc, int(renormalize), scale,
+                                      _ptr(dlogits), ldd, _stream(stream)), fn)
+
+
+def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().moe_gemm_fp8_workspace_bytes(M, N, K))
+
+
+def moe_gemm_fp8(A, SFA, W, SFW, D, C=None, workspace=None, stream=None):
+    """D = C + A W^T of E4M3 codes: A uint8 [M, K] with SFA float32 [M, K/128], W uint8 [N, K] with SFW float32
+    [ceil(N/128), K/128] or [N, K/128]; D bf16 or float32 [M, N], C float32 [M, N] (float32 D only; may be D).  Rows of A, W, D
+    and C may be strided.  workspace: moe_gemm_fp8_workspace_bytes(M, N, K) bytes."""
+    fn = "moe_gemm_fp8"
+    lda, ldw = _rows(A, "A", (torch.uint8,)), _rows(W, "W", (torch.uint8,))
+    ldd = _rows(D, "D", (torch.bfloat16, torch.float32))
+    ldc = 0 if C is None else _rows(C, "C", (torch.float32,))
+    _dev(SFA, "SFA", torch.float32, 2), _dev(SFW, "SFW", torch.float32, 2), _dev(workspace, "workspace")
+    M, K = A.shape
+    N = W.shape[0]
+    if W.shape[1] != K or tuple(D.shape) != (M, N) or (C is not None and tuple(C.shape) != (M, N)):
+        raise ValueError(f"{fn}: A is {tuple(A.shape)}, W {tuple(W.shape)}, D {tuple(D.shape)}"
+                         + ("" if C is None else f", C {tuple(C.shape)}"))
+    nb = (N + 127) // 128
+    if tuple(SFA.shape) != (M, K // 128) or tuple(SFW.shape) not in ((nb, K // 128), (N, K // 128)):
+        raise ValueError(f"{fn}: SFA is {tuple(SFA.shape)} (needs {(M, K // 128)}), SFW {tuple(SFW.shape)} "
+                         f"(needs {(nb, K // 128)} or {(N, K // 128)})")
+    gran = 128 if SFW.shape[0] == nb else 1
+    _one_device(fn, stream, A, SFA, W, SFW, D, C, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().moe_gemm_fp8(_ptr(A), lda, _ptr(SFA), _ptr(W), ldw, _ptr(SFW), gran, _ptr(D),
+                               BF16 if D.dtype == torch.bfloat16 else F32, ldd, _ptr(C), ldc, M, N, K,
+                               _ptr(workspace), ws_bytes, _stream(stream)), fn)
+
+
+def moe_quant_act_t(x, q, sf, stream=None):
+    """x bf16 [M, K] (rows may be strided) -> q uint8 [K, Mp] (E4M3 codes of the transposed x) and sf float32
+    [K, Mp/128], Mp = M rounded up to a multiple of 128."""
+    fn = "moe_quant_act_t"
+    ldx = _rows(x, "x", (torch.bfloat16,))
+    _dev(q, "q", torch.uint8, 2), _dev(sf, "sf", torch.float32, 2)
+    M, K = x.shape
+    mb = (M + 127) // 128
+    if tuple(q.shape) != (K, 128 * mb) or tuple(sf.shape) != (K, mb):
+        raise ValueError(f"{fn}: q is {tuple(q.shape)}, sf {tuple(sf.shape)}, need {(K, 128 * mb)} and {(K, mb)}")
+    _one_device(fn, stream, x, q, sf)
+    _check(load().moe_quant_act_t(_ptr(x), M, K, ldx, _ptr(q), _ptr(sf), _stream(stream)), fn)
 
 
 def moe_stream_read_words() -> int:

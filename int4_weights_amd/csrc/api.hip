@@ -2,6 +2,7 @@
 // Every entry point validates its arguments on the host, returns a status
 // without launching anything on failure (with a reason in moe_last_error()),
 // and otherwise enqueues its kernels on the caller's stream.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -627,6 +628,198 @@ moe_status moe_unpermute_combine(const uint16_t* Y, int64_t y_rows, const int32_
     return fail(MOE_ERR_ALIGN, "moe_unpermute_combine: Y and Z must be 16-byte aligned");
   return hip_status(launch_combine(Y, y_rows, output_index, topk_weights, T, k, N, Z, (hipStream_t)stream),
                     "moe_unpermute_combine");
+}
+
+int64_t moe_unpermute_combine_bwd_workspace_bytes(int T, int k, int64_t y_rows) {
+  if (T < 0 || k < 1 || k > MOE_MAX_TOPK || y_rows < 0 || y_rows > 0x7fffffff || (int64_t)T * k > 0x7fffffff)
+    return -1;
+  return combine_bwd_workspace_bytes((int64_t)T * k, y_rows);
+}
+
+moe_status moe_unpermute_combine_bwd(const uint16_t* dZ, const uint16_t* Y, int64_t y_rows,
+                                     const int32_t* output_index, const float* topk_weights, int T, int k, int N,
+                                     uint16_t* dY, float* dweights, void* workspace, int64_t workspace_bytes,
+                                     void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_unpermute_combine_bwd";
+  if (T < 0 || k < 1 || k > MOE_MAX_TOPK || N <= 0 || y_rows < 0 || y_rows > 0x7fffffff)
+    return fail(MOE_ERR_SHAPE, "%s: T=%d k=%d N=%d y_rows=%lld", fn, T, k, N, (long long)y_rows);
+  if ((int64_t)T * k > 0x7fffffff) return fail(MOE_ERR_SHAPE, "%s: T*k too large", fn);
+  if (N % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d must be a multiple of 8", fn, N);
+  if (!dY && !dweights) return fail(MOE_ERR_NULL, "%s: dY and dweights are both null", fn);
+  if (T == 0) return MOE_OK;
+  if (!dZ || !output_index || (dY && !topk_weights) || (dweights && !Y && y_rows > 0))
+    return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(dZ, 16) || !aligned(Y, 16) || !aligned(dY, 16) || !aligned(output_index, 4) ||
+      !aligned(topk_weights, 4) || !aligned(dweights, 4))
+    return fail(MOE_ERR_ALIGN, "%s: dZ, Y and dY must be 16-byte aligned, the tables 4-byte", fn);
+  const int64_t need = dY ? combine_bwd_workspace_bytes((int64_t)T * k, y_rows) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 8)))
+    return fail(MOE_ERR_WORKSPACE, "%s: needs %lld workspace bytes (8-byte aligned), got %lld", fn, (long long)need,
+                (long long)workspace_bytes);
+  CombineBwdArgs a{};
+  a.dZ = dZ;
+  a.Y = Y;
+  a.y_rows = y_rows;
+  a.oi = output_index;
+  a.w = topk_weights;
+  a.T = T;
+  a.k = k;
+  a.N = N;
+  a.dY = dY;
+  a.dw = dweights;
+  a.who = need > 0 ? (int2*)workspace : nullptr;
+  return hip_status(launch_combine_bwd(a, (hipStream_t)stream), fn);
+}
+
+// Checks shared by the router and its gradient.
+static moe_status check_router(const char* fn, const void* logits, int type, int64_t ld, int T, int E, int k,
+                               int score, float scale) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || k > E)
+    return fail(MOE_ERR_SHAPE, "%s: T=%d E=%d k=%d (need T>=0, 1<=E<=%d, 1<=k<=min(E, %d))", fn, T, E, k,
+                MOE_MAX_EXPERTS, MOE_MAX_TOPK);
+  if ((int64_t)T * k > 0x7fffffff) return fail(MOE_ERR_SHAPE, "%s: T*k too large", fn);
+  if (type != MOE_F32 && type != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: unknown element type %d", fn, type);
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown score function %d", fn, score);
+  if (!isfinite(scale)) return fail(MOE_ERR_UNSUPPORTED, "%s: scale is not finite", fn);
+  if (ld < E) return fail(MOE_ERR_SHAPE, "%s: rows of %d logits cannot be %lld apart", fn, E, (long long)ld);
+  if (!aligned(logits, type == MOE_F32 ? 4 : 2)) return fail(MOE_ERR_ALIGN, "%s: logits misaligned", fn);
+  return MOE_OK;
+}
+
+moe_status moe_router_topk(const void* logits, int logits_type, int64_t logits_ld, const float* bias, int T, int E,
+                           int k, int score, int n_group, int topk_group, int group_top, int renormalize,
+                           float scale, int32_t* topk_ids, float* topk_weights, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_router_topk";
+  moe_status st = check_router(fn, logits, logits_type, logits_ld, T, E, k, score, scale);
+  if (st) return st;
+  if (n_group < 1 || n_group > 64 || E % n_group || topk_group < 1 || topk_group > n_group)
+    return fail(MOE_ERR_SHAPE, "%s: n_group=%d (1..64, dividing E=%d) topk_group=%d (1..n_group)", fn, n_group, E,
+                topk_group);
+  if (group_top != 1 && group_top != 2) return fail(MOE_ERR_UNSUPPORTED, "%s: group_top=%d must be 1 or 2", fn, group_top);
+  if (k > topk_group * (E / n_group))
+    return fail(MOE_ERR_SHAPE, "%s: k=%d exceeds the %d experts of the kept groups", fn, k, topk_group * (E / n_group));
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_weights) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+    return fail(MOE_ERR_ALIGN, "%s: bias, topk_ids and topk_weights must be 4-byte aligned", fn);
+  RouterArgs a{};
+  a.logits = logits;
+  a.bf16 = logits_type == MOE_BF16;
+  a.ld = logits_ld;
+  a.bias = bias;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.score = score;
+  a.G = n_group;
+  a.TG = topk_group;
+  a.gtop = group_top;
+  a.norm = renormalize != 0;
+  a.scale = scale;
+  a.ids = topk_ids;
+  a.w = topk_weights;
+  return hip_status(launch_router_topk(a, (hipStream_t)stream), fn);
+}
+
+moe_status moe_router_topk_bwd(const void* logits, int logits_type, int64_t logits_ld, const int32_t* topk_ids,
+                               const float* dweights, int T, int E, int k, int score, int renormalize, float scale,
+                               void* dlogits, int64_t dlogits_ld, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_router_topk_bwd";
+  moe_status st = check_router(fn, logits, logits_type, logits_ld, T, E, k, score, scale);
+  if (st) return st;
+  if (dlogits_ld < E) return fail(MOE_ERR_SHAPE, "%s: rows of %d dlogits cannot be %lld apart", fn, E, (long long)dlogits_ld);
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !dweights || !dlogits) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(dlogits, logits_type == MOE_F32 ? 4 : 2) || !aligned(topk_ids, 4) || !aligned(dweights, 4))
+    return fail(MOE_ERR_ALIGN, "%s: dlogits, topk_ids or dweights misaligned", fn);
+  RouterBwdArgs a{};
+  a.logits = logits;
+  a.bf16 = logits_type == MOE_BF16;
+  a.ld = logits_ld;
+  a.ids = topk_ids;
+  a.dw = dweights;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.score = score;
+  a.norm = renormalize != 0;
+  a.scale = scale;
+  a.dlogits = dlogits;
+  a.ldd = dlogits_ld;
+  return hip_status(launch_router_topk_bwd(a, (hipStream_t)stream), fn);
+}
+
+int64_t moe_gemm_fp8_workspace_bytes(int M, int N, int K) {
+  if (M < 0 || M >= (1 << 30) || N < 1 || N >= (1 << 30) || K < 1 || K % 128) return -1;
+  return dense_workspace_bytes(M, N, K);
+}
+
+moe_status moe_gemm_fp8(const uint8_t* A, int64_t lda, const float* SFA, const uint8_t* W, int64_t ldw,
+                        const float* SFW, int gran_n, void* D, int out_type, int64_t ldd, const float* C,
+                        int64_t ldc, int M, int N, int K, void* workspace, int64_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_gemm_fp8";
+  if (M < 0 || M >= (1 << 30) || N < 1 || N >= (1 << 30) || K < 1)
+    return fail(MOE_ERR_SHAPE, "%s: M=%d N=%d K=%d", fn, M, N, K);
+  if (K % 128) return fail(MOE_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 128", fn, K);
+  if (gran_n != 1 && gran_n != 128) return fail(MOE_ERR_UNSUPPORTED, "%s: gran_n=%d must be 1 or 128", fn, gran_n);
+  if (out_type != MOE_F32 && out_type != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown element type %d", fn, out_type);
+  if (C && out_type != MOE_F32) return fail(MOE_ERR_UNSUPPORTED, "%s: an addend needs fp32 output", fn);
+  if (lda < K || ldw < K || ldd < N || (C && ldc < N))
+    return fail(MOE_ERR_SHAPE, "%s: a row stride is shorter than its row", fn);
+  if (lda >= (1 << 23) || ldw >= (1 << 23))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: lda and ldw must be below 2^23 bytes", fn);
+  // tiles are numbered in 32 bits
+  if (((int64_t)(M + 15) / 16) * ((N + 15) / 16) > 0x7fffffff)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d x N=%d is too large", fn, M, N);
+  if (M == 0) return MOE_OK;
+  if (!A || !SFA || !W || !SFW || !D) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(A, 16) || !aligned(W, 16) || lda % 16 || ldw % 16 || !aligned(SFA, 4) || !aligned(SFW, 4) ||
+      !aligned(D, out_type == MOE_F32 ? 4 : 2) || !aligned(C, 4))
+    return fail(MOE_ERR_ALIGN, "%s: A and W (and lda, ldw) must be 16-byte aligned, the others to their type", fn);
+  if (C == D && ldc != ldd) return fail(MOE_ERR_SHAPE, "%s: C is D but ldc is not ldd", fn);
+  const int64_t need = dense_workspace_bytes(M, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(MOE_ERR_WORKSPACE, "%s: needs %lld workspace bytes (16-byte aligned), got %lld", fn, (long long)need,
+                (long long)workspace_bytes);
+  DenseArgs a{};
+  a.A = A;
+  a.lda = lda;
+  a.SFA = SFA;
+  a.W = W;
+  a.ldw = ldw;
+  a.SFW = SFW;
+  a.gran_n = gran_n;
+  a.D = D;
+  a.ldd = ldd;
+  a.f32 = out_type == MOE_F32;
+  a.C = C;
+  a.ldc = ldc;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.ws = need > 0 ? (float*)workspace : nullptr;
+  return hip_status(launch_gemm_dense(a, (hipStream_t)stream), fn);
+}
+
+moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx, uint8_t* qt, float* sft, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_quant_act_t";
+  if (M < 0 || K <= 0 || ldx < K) return fail(MOE_ERR_SHAPE, "%s: M=%lld K=%d ldx=%lld", fn, (long long)M, K, (long long)ldx);
+  if (K % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 8", fn, K);
+  // one workgroup per 128 rows x 64 columns
+  if (M > (1ll << 40) || ((M + 127) / 128) * ((K + 63) / 64) > 0x7fffffff)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: M=%lld x K=%d is too large", fn, (long long)M, K);
+  if (M == 0) return MOE_OK;
+  if (!x || !qt || !sft) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (!aligned(x, 16) || ldx % 8 || !aligned(qt, 16) || !aligned(sft, 4))
+    return fail(MOE_ERR_ALIGN, "%s: x (and its rows) and qt must be 16-byte aligned, sft 4-byte aligned", fn);
+  return hip_status(launch_quant_act_t(x, M, K, ldx, qt, sft, (hipStream_t)stream), fn);
 }
 
 int moe_stream_read_words(void) { return stream_read_grid(); }

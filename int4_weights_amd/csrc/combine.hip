@@ -8,6 +8,18 @@
 // routed row is read once and every output row written once, so both go
 // nontemporal (streamed past the caches; about 13% faster on the Qwen3-shaped
 // combine than cached accesses).
+//
+// moe_unpermute_combine_bwd: its gradient, dY[output_index[t,r]] = p[t,r] * dZ[t]
+// and dp[t,r] = <dZ[t], Y[output_index[t,r]]>.
+// One workgroup per token: the token's dZ row is read once per batch of 8
+// slots, every named row of Y is streamed once and its gradient row written
+// once (nontemporal).  HBM-bound.
+// A row is normally named by one slot (moe_route_pack gives every route a row
+// of its own).  A row named by several slots gets the sum over them in route
+// order: its lowest slot writes it, in fp32 until the one rounding.  Who names a row is
+// found by a scan of output_index in each workgroup (up to 4096 routes, no
+// workspace), or beforehand with one integer count and minimum per row in the
+// workspace (order-free, so results do not depend on timing).
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -65,6 +77,186 @@ hipError_t launch_combine(const uint16_t* Y, int64_t y_rows, const int32_t* oi, 
   const int64_t cap = (int64_t)device_info().cus * 32;
   if (grid > cap) grid = cap;
   combine_kernel<<<(unsigned)grid, 256, 0, s>>>(Y, y_rows, oi, w, T, k, N, Z);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------- backward --
+// workspace of the large path: per row of Y the number of slots naming it and the lowest of them
+__global__ __launch_bounds__(256) void combine_bwd_clear_kernel(int2* __restrict__ who, int64_t y_rows) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < y_rows; i += (int64_t)gridDim.x * 256)
+    who[i] = int2{0, 0x7fffffff};
+}
+__global__ __launch_bounds__(256) void combine_bwd_claim_kernel(const int32_t* __restrict__ oi, int64_t R,
+                                                                int64_t y_rows, int2* __restrict__ who) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < R; i += (int64_t)gridDim.x * 256) {
+    const int p = oi[i];
+    if (p >= 0 && p < y_rows) {
+      atomicAdd(&who[p].x, 1);
+      atomicMin(&who[p].y, (int)i);
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack8(const v4i r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_to_f32((uint32_t)r[i] & 0xffffu);
+    f[2 * i + 1] = bf16_to_f32((uint32_t)r[i] >> 16);
+  }
+}
+__device__ __forceinline__ v4i pack8(const float (&f)[8]) {
+  v4i o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (int)(f32_to_bf16_rne(f[2 * i]) | (f32_to_bf16_rne(f[2 * i + 1]) << 16));
+  return o;
+}
+
+// dY of a row named by `cnt` slots, the lowest of them `own`: the whole workgroup sums them in route order.
+__device__ inline void shared_row(const CombineBwdArgs& a, int p, int64_t own, int cnt) {
+  const int64_t R = (int64_t)a.T * a.k;
+  for (int c = threadIdx.x; c < a.N / 8; c += blockDim.x) {
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    int left = cnt;
+    for (int64_t i = own; i < R && left > 0; ++i) {
+      if (a.oi[i] != p) continue;
+      --left;
+      float dz[8];
+      unpack8(*(const v4i*)(a.dZ + i / a.k * a.N + 8 * c), dz);
+      const float w = a.w[i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = __builtin_fmaf(w, dz[j], acc[j]);
+    }
+    *(v4i*)(a.dY + (int64_t)p * a.N + 8 * c) = pack8(acc);
+  }
+}
+
+__global__ __launch_bounds__(256) void combine_bwd_kernel(const CombineBwdArgs a) {
+  constexpr int B = 8;  // slots per batch
+  __shared__ int s_cnt[B], s_own[B];
+  __shared__ float s_sum[4][B];
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
+  const int chunks = a.N / 8;
+  const int64_t R = (int64_t)a.T * a.k;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (int r0 = 0; r0 < a.k; r0 += B) {
+      const int64_t i0 = (int64_t)t * a.k + r0;
+      int p[B];
+      float w[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        p[j] = r0 + j < a.k ? a.oi[i0 + j] : -1;
+        if (p[j] >= a.y_rows) p[j] = -1;
+        w[j] = r0 + j < a.k && a.dY ? a.w[i0 + j] : 0.0f;
+      }
+      bool write[B], shared = false;
+      if (a.dY) {
+        if (a.who) {
+#pragma unroll
+          for (int j = 0; j < B; ++j) {
+            write[j] = p[j] >= 0;
+            if (p[j] >= 0 && a.who[p[j]].x != 1) {
+              write[j] = false;
+              shared = true;
+            }
+          }
+        } else {
+          if (tid < B) {
+            s_cnt[tid] = 0;
+            s_own[tid] = 0x7fffffff;
+          }
+          __syncthreads();
+          for (int i = tid; i < (int)R; i += 256) {
+            const int o = a.oi[i];
+#pragma unroll
+            for (int j = 0; j < B; ++j)
+              if (o == p[j] && o >= 0) {
+                atomicAdd(&s_cnt[j], 1);
+                atomicMin(&s_own[j], i);
+              }
+          }
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < B; ++j) {
+            write[j] = p[j] >= 0 && s_cnt[j] == 1;
+            shared = shared || (p[j] >= 0 && s_cnt[j] != 1);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < B; ++j) write[j] = false;
+      }
+
+      float dot[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) dot[j] = 0.0f;
+      for (int c = tid; c < chunks; c += 256) {
+        float dz[8];
+        unpack8(*(const v4i*)(a.dZ + (int64_t)t * a.N + 8 * c), dz);
+        if (a.dw) {
+          v4i y[B];
+#pragma unroll
+          for (int j = 0; j < B; ++j)
+            y[j] = p[j] >= 0 ? __builtin_nontemporal_load((const v4i*)(a.Y + (int64_t)p[j] * a.N + 8 * c))
+                             : v4i{0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < B; ++j) {
+            float f[8];
+            unpack8(y[j], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(f[i], dz[i], dot[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          if (!write[j]) continue;
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = w[j] * dz[i];
+          __builtin_nontemporal_store(pack8(o), (v4i*)(a.dY + (int64_t)p[j] * a.N + 8 * c));
+        }
+      }
+      if (shared) {
+        for (int j = 0; j < B; ++j) {
+          const int pj = r0 + j < a.k ? a.oi[i0 + j] : -1;
+          if (pj < 0 || pj >= a.y_rows) continue;
+          const int cnt = a.who ? a.who[pj].x : s_cnt[j];
+          const int own = a.who ? a.who[pj].y : s_own[j];
+          if (cnt > 1 && own == i0 + j) shared_row(a, pj, own, cnt);
+        }
+      }
+      if (a.dw) {
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+#pragma unroll
+          for (int off = 32; off; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
+          if (lane == 0) s_sum[wv][j] = dot[j];
+        }
+        __syncthreads();
+        if (tid < B && r0 + tid < a.k)
+          a.dw[i0 + tid] = (s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]);
+      }
+      __syncthreads();  // s_cnt, s_own and s_sum are reused
+    }
+  }
+}
+
+int64_t combine_bwd_workspace_bytes(int64_t R, int64_t y_rows) { return R <= kRouteSmallMax ? 0 : 8 * y_rows; }
+
+hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t s) {
+  const int64_t cap = (int64_t)device_info().cus * 32;
+  if (a.who) {
+    const int64_t R = (int64_t)a.T * a.k;
+    const int64_t gr = (a.y_rows + 255) / 256, gc = (R + 255) / 256;
+    combine_bwd_clear_kernel<<<(unsigned)(gr < cap ? gr : cap), 256, 0, s>>>(a.who, a.y_rows);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    combine_bwd_claim_kernel<<<(unsigned)(gc < cap ? gc : cap), 256, 0, s>>>(a.oi, R, a.y_rows, a.who);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  combine_bwd_kernel<<<(unsigned)(a.T < cap ? a.T : cap), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

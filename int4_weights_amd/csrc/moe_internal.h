@@ -101,4 +101,70 @@ hipError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* out, hip
 hipError_t launch_combine(const uint16_t* Y, int64_t y_rows, const int32_t* oi, const float* w, int T, int k,
                           int N, uint16_t* Z, hipStream_t s);
 
+struct CombineBwdArgs {
+  const uint16_t* dZ;    // bf16 [T, N]
+  const uint16_t* Y;     // bf16 [y_rows, N] (nullptr when dw is)
+  int64_t y_rows;
+  const int32_t* oi;     // [T, k]
+  const float* w;        // [T, k]
+  int T, k, N;
+  uint16_t* dY;          // bf16 [y_rows, N] or nullptr
+  float* dw;             // [T, k] or nullptr
+  int2* who;             // large path: {slots naming the row, lowest of them} [y_rows]
+};
+int64_t combine_bwd_workspace_bytes(int64_t R, int64_t y_rows);
+hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t s);
+
+struct RouterArgs {
+  const void* logits;    // fp32 or bf16 [T, E], rows ld apart
+  int bf16;
+  int64_t ld;
+  const float* bias;     // [E] or nullptr
+  int T, E, k;
+  int score;             // 0 softmax, 1 sigmoid
+  int G, TG, gtop;       // groups, groups kept, keys summed per group (1 or 2)
+  int norm;
+  float scale;
+  int32_t* ids;          // [T, k]
+  float* w;              // [T, k]
+};
+hipError_t launch_router_topk(const RouterArgs& a, hipStream_t s);
+
+struct RouterBwdArgs {
+  const void* logits;    // fp32 or bf16 [T, E], rows ld apart
+  int bf16;
+  int64_t ld;
+  const int32_t* ids;    // [T, k]
+  const float* dw;       // [T, k]
+  int T, E, k;
+  int score, norm;
+  float scale;
+  void* dlogits;         // as logits, rows ldd apart
+  int64_t ldd;
+};
+hipError_t launch_router_topk_bwd(const RouterBwdArgs& a, hipStream_t s);
+
+hipError_t launch_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx, uint8_t* q, float* sf,
+                              hipStream_t s);
+
+struct DenseArgs {
+  const uint8_t* A;      // E4M3 [M, K], rows lda apart
+  int64_t lda;
+  const float* SFA;      // [M, K/128]
+  const uint8_t* W;      // E4M3 [N, K], rows ldw apart
+  int64_t ldw;
+  const float* SFW;      // [ceil(N / gran_n), K/128]
+  int gran_n;            // 1 or 128
+  void* D;               // bf16 or fp32 [M, N], rows ldd apart
+  int64_t ldd;
+  int f32;               // D is fp32
+  const float* C;        // addend [M, N], rows ldc apart, or nullptr
+  int64_t ldc;
+  int M, N, K;
+  float* ws;             // split K: partial sums [splits, M, N]
+  int splits;
+};
+int64_t dense_workspace_bytes(int M, int N, int K);
+hipError_t launch_gemm_dense(const DenseArgs& a, hipStream_t s);
+
 }  // namespace moe

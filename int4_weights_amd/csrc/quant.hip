@@ -365,4 +365,75 @@ hipError_t launch_quant_weight_int4(const uint16_t* w, int E, int N, int K, uint
   return hipGetLastError();
 }
 
+// ------------------------------------------------------ transposing quantiser --
+// moe_quant_act_t: x [M, K] bf16 -> codes qt [K, Mp] and scales sft [K, Mp/128], Mp = M rounded up to 128: the
+// 1x128 rule of moe_quant_act along the rows of x (the tokens), for the weight gradient's product, which
+// contracts over them.  Rows past M count as zeros.
+// One workgroup per 128 rows x 64 columns.  A lane holds 4 consecutive rows of 8 columns (16-byte loads), so
+// each column's 4 codes are one dword of the transposed tile; column maxima meet over the lanes that share
+// columns, then over the 4 waves.  The tile goes through LDS (rows of 132 bytes: the 64 dwords a wave writes at once
+// fall on 64 banks) and leaves as whole 128-byte rows.  HBM-bound: 2 bytes read and 1 written per value.
+constexpr int kQtCols = 64, kQtStride = 132;
+
+__global__ __launch_bounds__(256) void quant_act_t_kernel(const uint16_t* __restrict__ x, int64_t M, int K,
+                                                          int64_t ldx, uint8_t* __restrict__ q,
+                                                          float* __restrict__ sf, int64_t mb, int kb) {
+  __shared__ float s_max[4][kQtCols];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t[kQtCols * kQtStride];
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
+  const int64_t mblk = blockIdx.x / kb, m0 = mblk * 128;
+  const int k0 = (int)(blockIdx.x % kb) * kQtCols;
+  const int c8 = tid & 7, a = tid >> 3;  // columns k0 + 8 c8 .., rows m0 + 4 a ..
+  const bool col_on = k0 + 8 * c8 < K;
+  float f[4][8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int64_t m = m0 + 4 * a + r;
+    v4i v = {0, 0, 0, 0};
+    if (col_on && m < M) v = *(const v4i*)(x + m * ldx + k0 + 8 * c8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[r][2 * i] = bf16_to_f32((uint32_t)v[i] & 0xffffu);
+      f[r][2 * i + 1] = bf16_to_f32((uint32_t)v[i] >> 16);
+    }
+  }
+  float mx[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    mx[c] = fmaxf(fmaxf(fabsf(f[0][c]), fabsf(f[1][c])), fmaxf(fabsf(f[2][c]), fabsf(f[3][c])));
+#pragma unroll
+    for (int off = 8; off < 64; off <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor(mx[c], off, 64));
+    if (lane < 8) s_max[wv][8 * c8 + c] = mx[c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int col = 8 * c8 + c;
+    const int e = pow2_exponent(fmaxf(fmaxf(s_max[0][col], s_max[1][col]), fmaxf(s_max[2][col], s_max[3][col])));
+    int o = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_ldexpf(f[0][c], -e),
+                                           __builtin_amdgcn_ldexpf(f[1][c], -e), 0, false);
+    o = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_ldexpf(f[2][c], -e), __builtin_amdgcn_ldexpf(f[3][c], -e),
+                                       o, true);
+    *(int*)(s_t + col * kQtStride + 4 * a) = o;
+    if (a == 0 && col_on) sf[(int64_t)(k0 + col) * mb + mblk] = pow2f(e);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = tid + 256 * i, col = u >> 3, part = u & 7;
+    if (k0 + col < K) {
+      const int* src = (const int*)(s_t + col * kQtStride + 16 * part);
+      *(v4i*)(q + (int64_t)(k0 + col) * (128 * mb) + m0 + 16 * part) = v4i{src[0], src[1], src[2], src[3]};
+    }
+  }
+}
+
+hipError_t launch_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx, uint8_t* q, float* sf,
+                              hipStream_t s) {
+  const int64_t mb = (M + 127) / 128;
+  const int kb = (K + kQtCols - 1) / kQtCols;
+  quant_act_t_kernel<<<(unsigned)(mb * kb), 256, 0, s>>>(x, M, K, ldx, q, sf, mb, kb);
+  return hipGetLastError();
+}
+
 }  // namespace moe

@@ -1,0 +1,523 @@
+// router.hip -- moe_router_topk and its gradient: the router between the gate
+// projection's logits and moe_route_pack's topk_ids / topk_weights.
+//
+// Forward, per token (row of E logits x):
+//   score   s_e = 1 / (1 + exp(-x_e)) or exp(x_e - m) / sum exp(x - m)
+//   key     x_e without a bias (every score is increasing in x), else s_e + b_e
+//   groups  G groups of E/G consecutive experts, the best topk_group of them by
+//           their largest key, or by the sum of their two largest keys
+//   slots   the k largest keys of the kept groups, ties to the lowest expert
+//   weight  scale * s, or scale * s / (sum of the selected s)
+// One wave per token, the row in registers: lane group g holds expert group g
+// (G rounded up to a power of two divides the wave), each lane VPL consecutive
+// experts, so a lane's order is the experts' order and a tie goes to the lowest
+// lane, then its lowest register.
+//
+// Exact choice from 32-bit keys.  Experts are ordered by key in 64 bits
+// (scores of two experts can lie closer together than fp32 resolves, and a
+// different order is a different result), but nearly every row is decided by
+// fp32 keys: they carry a bound es + 2^-23 |key| on their error (es: 2^-20 for
+// sigmoid scores, 2^-18 times the largest probability for softmax ones; the
+// evaluation below stays within half of that), and a row whose neighbouring
+// winners, or the groups around the last kept one, are closer than the bounds
+// allow is selected again with fp64 scores.  Without a bias the keys are the
+// logits themselves and need no such check.
+//
+// A logit of -inf or NaN marks an expert that this token may not use; slots
+// left over get id -1 and weight 0, which moe_route_pack skips.
+#include "moe_device.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kNone = (int)0x80000000;  // key of an expert that cannot be chosen
+
+// exp(x) for x <= 0 (and any x below overflow) to about two fp32 ulps: the product x * log2(e) is carried as
+// hi + lo, the hardware exp2 takes hi, and lo enters to first order.  0 at -inf.
+__device__ __forceinline__ float exp_f32(float x) {
+  constexpr float kLog2e = 1.44269504088896341f, kLog2eLo = 1.92596299e-08f, kLn2 = 0.693147180559945309f;
+  const float hi = x * kLog2e;
+  const float lo = __builtin_fmaf(x, kLog2e, -hi) + x * kLog2eLo;
+  const float r = __builtin_amdgcn_exp2f(hi);
+  return fabsf(hi) < 200.0f ? r * __builtin_fmaf(lo, kLn2, 1.0f) : r;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
+
+// signed integer in the order of the float (x + 0 turns -0 into +0: equal floats have equal keys)
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x + 0.0f);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, 0xF, 0xF, false);
+}
+
+// Maximum over the wave, in every lane (as a scalar): five steps inside the rows of 16 lanes, two across them.
+__device__ __forceinline__ int wave_max_i32(int v) {
+  v = max(v, dpp<0xB1>(v, v));
+  v = max(v, dpp<0x4E>(v, v));
+  v = max(v, dpp<0x141>(v, v));
+  v = max(v, dpp<0x140>(v, v));
+  v = max(v, dpp<0x142>(v, v));  // lane 15 of a row to the next row
+  v = max(v, dpp<0x143>(v, v));  // lane 31 to rows 2 and 3
+  return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ float wave_max_f32(float v) { return unordered(wave_max_i32(ordered(v))); }
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+__device__ __forceinline__ float readlane_f32(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p) {
+  if constexpr (sizeof(T) == 2)
+    return bf16_to_f32(*p);
+  else
+    return *p;
+}
+
+// Orders one wave's LDS accesses: what a lane wrote before it, every lane of the wave reads after it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Where this lane's experts are: expert base + j for j < n.
+struct LaneExperts {
+  int base, n, lpg;  // lpg: lanes per group
+};
+__device__ __forceinline__ LaneExperts lane_experts(int E, int G, int lane) {
+  const int S = E / G;
+  const int lg = G > 1 ? 32 - __builtin_clz(G - 1) : 0;  // log2 of G rounded up
+  const int lpg = 64 >> lg;
+  const int cnt = (S + lpg - 1) / lpg;
+  const int g = lane >> (6 - lg), l = lane & (lpg - 1);
+  LaneExperts r;
+  r.lpg = lpg;
+  r.base = g * S + l * cnt;
+  r.n = g < G ? max(0, min(cnt, S - l * cnt)) : 0;
+  return r;
+}
+
+struct Pick {
+  int id;   // lane r < k: the expert of slot r, -1 if none
+  float x;  // and its logit
+};
+
+// Two largest of the group's keys, in all its lanes.
+template <typename F>
+__device__ __forceinline__ void group_top2(F& a1, F& a2, int lpg) {
+  for (int off = 1; off < lpg; off <<= 1) {
+    const F b1 = __shfl_xor(a1, off, 64), b2 = __shfl_xor(a2, off, 64);
+    const F lo = a1 < b1 ? a1 : b1;
+    const F m2 = a2 > b2 ? a2 : b2;
+    a1 = a1 > b1 ? a1 : b1;
+    a2 = lo > m2 ? lo : m2;
+  }
+}
+
+// The choice in 64 bits (every lane of the wave calls it).
+template <int VPL>
+__device__ __forceinline__ Pick select_f64(const RouterArgs& a, const float (&x)[VPL], const float (&b)[VPL],
+                                           const LaneExperts& le, int lane) {
+  const double ninf = -__builtin_huge_val();
+  double key[VPL];
+  double den = 1.0, m = 0.0;
+  if (a.score == 0) {
+    float mf = -__builtin_huge_valf();
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) mf = fmaxf(mf, x[j]);
+    m = (double)wave_max_f32(mf);
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (x[j] > -__builtin_huge_valf()) s += (double)x[j] == m ? 1.0 : exp((double)x[j] - m);
+    den = wave_sum_f64(s);
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const double xd = (double)x[j];
+    double s;
+    if (a.score == 0)
+      s = (xd == m ? 1.0 : exp(xd - m)) / den;
+    else
+      s = 1.0 / (1.0 + exp(-xd));
+    key[j] = a.bias ? s + (double)b[j] : s;
+    if (!(x[j] > -__builtin_huge_valf()) || !(key[j] > ninf)) key[j] = ninf;
+  }
+  bool kept = true;
+  if (a.G > 1) {
+    double a1 = ninf, a2 = ninf;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      // by logit where there is no bias and only the largest counts: the order of the scores
+      const double v = !a.bias && a.gtop == 1 ? (key[j] > ninf ? (double)x[j] : ninf) : key[j];
+      const double lo = v < a1 ? v : a1;
+      a1 = v > a1 ? v : a1;
+      a2 = lo > a2 ? lo : a2;
+    }
+    group_top2(a1, a2, le.lpg);
+    const double gs = a.gtop == 1 || !(a2 > ninf) ? a1 : a1 + a2;
+    const int g = lane / le.lpg;
+    int better = 0;
+    for (int o = 0; o < a.G; ++o) {
+      const double go = __shfl(gs, o * le.lpg, 64);
+      better += go > gs || (go == gs && o < g);
+    }
+    kept = better < a.TG;
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    if (!a.bias) key[j] = key[j] > ninf ? (double)x[j] : ninf;
+    if (!kept) key[j] = ninf;
+  }
+  Pick p{-1, 0.0f};
+  for (int r = 0; r < a.k; ++r) {
+    double best = ninf;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) best = key[j] > best ? key[j] : best;
+    double m2 = best;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double o = __shfl_xor(m2, off, 64);
+      m2 = o > m2 ? o : m2;
+    }
+    if (!(m2 > ninf)) break;
+    const uint64_t who = __ballot(best == m2);
+    const int wl = __builtin_ctzll(who);
+    int e = -1;
+    float xs = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (e < 0 && key[j] == m2) {
+        e = le.base + j;
+        xs = x[j];
+        if (lane == wl) key[j] = ninf;
+      }
+    const int ew = __builtin_amdgcn_readlane(e, wl);
+    const float xw = readlane_f32(xs, wl);
+    if (lane == r) {
+      p.id = ew;
+      p.x = xw;
+    }
+  }
+  return p;
+}
+
+// The weights of the selected slots (lane r: slot r; lanes >= k and empty slots hold on = false).
+__device__ __forceinline__ float slot_weight(int score, int norm, float scale, bool on, float x, float row_m,
+                                             float row_den) {
+  if (norm) {
+    const float m = wave_max_f32(on ? x : -__builtin_huge_valf());
+    float q;
+    if (score == 0)
+      q = x == m ? 1.0f : exp_f32(x - m);
+    else  // s / s_max without underflow: exp(min(x, 0)) / (1 + exp(-|x|)) is the sigmoid for either sign
+      q = exp_f32(fminf(x, 0.0f) - fminf(m, 0.0f)) / (1.0f + exp_f32(-fabsf(x)));
+    q = on ? q : 0.0f;
+    const float sum = wave_sum_f32(q);
+    return on ? scale * (q / sum) : 0.0f;
+  }
+  float s;
+  if (score == 0)
+    s = (x == row_m ? 1.0f : exp_f32(x - row_m)) / row_den;
+  else
+    s = exp_f32(fminf(x, 0.0f)) / (1.0f + exp_f32(-fabsf(x)));
+  return on ? scale * s : 0.0f;
+}
+
+}  // namespace
+
+template <typename T, int VPL>
+__global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
+  const int lane = lane_id();
+  const float ninf = -__builtin_huge_valf();
+  const LaneExperts le = lane_experts(a.E, a.G, lane);
+  const bool by_score = a.bias || (a.G > 1 && a.gtop == 2);
+  for (int t = blockIdx.x * 4 + uniform(threadIdx.x >> 6); t < a.T; t += gridDim.x * 4) {
+    const T* row = (const T*)a.logits + (int64_t)t * a.ld + le.base;
+    float x[VPL], b[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      x[j] = j < le.n ? load_logit(row + j) : ninf;
+      b[j] = a.bias && j < le.n ? a.bias[le.base + j] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) x[j] = x[j] > ninf ? x[j] : ninf;  // NaN is -inf
+
+    float row_m = 0.0f, row_den = 1.0f, ex[VPL];
+    if (a.score == 0 && (by_score || !a.norm)) {
+      float mf = ninf;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) mf = fmaxf(mf, x[j]);
+      row_m = wave_max_f32(mf);
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        ex[j] = x[j] > ninf ? (x[j] == row_m ? 1.0f : exp_f32(x[j] - row_m)) : 0.0f;
+        s += ex[j];
+      }
+      s = wave_sum_f32(s);
+      row_den = s > 0.0f ? s : 1.0f;  // 0 only where no expert is available
+    }
+
+    float key[VPL];
+    float es = 0.0f;
+    if (by_score) {
+      const float inv = 1.0f / row_den;
+      es = a.score == 0 ? 0x1p-18f * inv : 0x1p-20f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const float s = a.score == 0 ? ex[j] * inv : sigmoid_f32(x[j]);
+        key[j] = s + b[j];
+        if (!(x[j] > ninf) || !(key[j] > ninf)) key[j] = ninf;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) key[j] = x[j];
+    }
+
+    bool unsure = false, kept = true;
+    if (a.G > 1) {
+      float a1 = ninf, a2 = ninf;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const float v = key[j], lo = fminf(v, a1);
+        a1 = fmaxf(v, a1);
+        a2 = fmaxf(lo, a2);
+      }
+      group_top2(a1, a2, le.lpg);
+      const bool two = a.gtop == 2 && a2 > ninf;
+      const float gs = two ? a1 + a2 : a1;
+      const int g = lane / le.lpg;
+      if (by_score) {
+        // 0 for a group without available experts (its infinite key says nothing about precision)
+        const float eg = a1 > ninf ? 2.0f * es + 0x1p-22f * (fabsf(a1) + (two ? fabsf(a2) : 0.0f)) : 0.0f;
+        const float lo = gs - eg, hi = gs + eg;
+        int above = 0, maybe = -1;  // groups surely above this one; possibly above (this one itself counts once)
+        for (int o = 0; o < a.G; ++o) {
+          above += readlane_f32(lo, o * le.lpg) > hi;
+          maybe += !(readlane_f32(hi, o * le.lpg) < lo);
+        }
+        kept = above < a.TG;
+        unsure = kept && maybe >= a.TG && gs > ninf;
+      } else {
+        int better = 0;
+        for (int o = 0; o < a.G; ++o) {
+          const float go = readlane_f32(gs, o * le.lpg);
+          better += go > gs || (go == gs && o < g);
+        }
+        kept = better < a.TG;
+      }
+    }
+
+    Pick p{-1, 0.0f};
+    if (!__any(unsure)) {
+      int ik[VPL];
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        // without a bias the experts' order is the logits'
+        const float v = a.bias ? key[j] : x[j];
+        ik[j] = kept && key[j] > ninf ? ordered(v) : kNone;
+      }
+      const int rounds = a.bias ? a.k + 1 : a.k;  // with a bias, the best loser has to be clearly below too
+      float prev = 0.0f;
+      bool close = false;
+      for (int r = 0; r < rounds; ++r) {
+        int best = ik[0];
+#pragma unroll
+        for (int j = 1; j < VPL; ++j) best = max(best, ik[j]);
+        const int mk = wave_max_i32(best);
+        if (mk == kNone) break;
+        if (a.bias) {
+          const float v = unordered(mk);
+          if (r > 0 && !(prev - v > 2.0f * es + 0x1p-23f * (fabsf(prev) + fabsf(v)))) {
+            close = true;
+            break;
+          }
+          prev = v;
+          if (r == a.k) break;
+        }
+        const int wl = __builtin_ctzll(__ballot(best == mk));
+        int e = -1;
+        float xs = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+          if (e < 0 && ik[j] == mk) {
+            e = le.base + j;
+            xs = x[j];
+            if (lane == wl) ik[j] = kNone;
+          }
+        const int ew = __builtin_amdgcn_readlane(e, wl);
+        const float xw = readlane_f32(xs, wl);
+        if (lane == r) {
+          p.id = ew;
+          p.x = xw;
+        }
+      }
+      unsure = close;
+    }
+    if (__any(unsure)) p = select_f64<VPL>(a, x, b, le, lane);
+
+    const bool on = p.id >= 0;
+    const float w = slot_weight(a.score, a.norm, a.scale, on, p.x, row_m, row_den);
+    if (lane < a.k) {
+      a.ids[(int64_t)t * a.k + lane] = p.id;
+      a.w[(int64_t)t * a.k + lane] = w;
+    }
+  }
+}
+
+// Gradient, per token, with g_r = d weight_r, w_r the weight and s_r the score of slot r:
+//   renormalised:       d x_r = w_r (g_r - sum_j g_j w_j / scale), times 1 - s_r for sigmoid scores
+//   sigmoid as it is:   d x_r = scale g_r s_r (1 - s_r)
+//   softmax as it is:   d x_e = scale p_e ([e selected] g_e - sum_j g_j p_j), for every expert
+// One wave per token; slots in lanes, the row assembled in LDS so that it is written once, whole.  An expert
+// named by two slots gets the sum over them, in slot order.
+template <typename T, int VPL>
+__global__ __launch_bounds__(256) void router_topk_bwd_kernel(const RouterBwdArgs a) {
+  __shared__ float s_row[4][64 * VPL];
+  const int lane = lane_id(), wv = uniform(threadIdx.x >> 6);
+  const float ninf = -__builtin_huge_valf();
+  float* srow = s_row[wv];
+  const bool dense = a.score == 0 && !a.norm;
+  const int base = lane * VPL;
+  for (int t = blockIdx.x * 4 + wv; t < a.T; t += gridDim.x * 4) {
+    const T* row = (const T*)a.logits + (int64_t)t * a.ld;
+    int id = -1;
+    float g = 0.0f, x = ninf;
+    if (lane < a.k) {
+      id = a.ids[(int64_t)t * a.k + lane];
+      if (id < 0 || id >= a.E) id = -1;
+      if (id >= 0) {
+        x = load_logit(row + id);
+        g = a.dw[(int64_t)t * a.k + lane];
+      }
+    }
+    const bool on = x > ninf;  // an empty slot, or an expert that was not available: no gradient
+    g = on ? g : 0.0f;
+    float row_m = 0.0f, row_den = 1.0f, ex[VPL];
+    if (dense) {
+      float mf = ninf;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const float v = base + j < a.E ? load_logit(row + base + j) : ninf;
+        ex[j] = v > ninf ? v : ninf;
+        mf = fmaxf(mf, ex[j]);
+      }
+      row_m = wave_max_f32(mf);
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        ex[j] = ex[j] > ninf ? (ex[j] == row_m ? 1.0f : exp_f32(ex[j] - row_m)) : 0.0f;
+        s += ex[j];
+      }
+      s = wave_sum_f32(s);
+      row_den = s > 0.0f ? s : 1.0f;  // 0 only where no expert is available
+    }
+    const float w = slot_weight(a.score, a.norm, 1.0f, on, x, row_m, row_den);
+    const float sg = a.scale * g;
+    float d, mean = 0.0f;
+    if (a.norm || dense) mean = wave_sum_f32(sg * w);
+    if (a.norm)
+      d = w * (sg - mean);
+    else
+      d = sg * w;  // dense: the -p_e * mean part is added to every expert below
+    if (a.score != 0) {
+      const float ax = fabsf(x);  // 1 - s = exp(min(-x, 0)) / (1 + exp(-|x|))
+      d *= exp_f32(fminf(-x, 0.0f)) / (1.0f + exp_f32(-ax));
+    }
+    d = on ? d : 0.0f;
+    // slots of the same expert: the first one carries the sum
+    bool first = on;
+    float sum = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+      const int ij = __builtin_amdgcn_readlane(id, j);
+      const float dj = readlane_f32(d, j);
+      if (ij == id) {
+        sum += dj;
+        if (j < lane) first = false;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) srow[base + j] = 0.0f;
+    wave_fence();
+    if (first) srow[id] = sum;
+    wave_fence();
+    T* out = (T*)a.dlogits + (int64_t)t * a.ldd;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      float v = srow[base + j];
+      if (dense) v -= ex[j] / row_den * mean;
+      if (base + j < a.E) {
+        if constexpr (sizeof(T) == 2)
+          out[base + j] = (T)f32_to_bf16_rne(v);
+        else
+          out[base + j] = v;
+      }
+    }
+    wave_fence();  // the row is rewritten for the next token
+  }
+}
+
+namespace {
+
+int row_grid(int T) {
+  const int64_t need = ((int64_t)T + 3) / 4, cap = (int64_t)device_info().cus * 32;
+  return (int)(need < cap ? need : cap);
+}
+
+template <typename T>
+hipError_t launch_topk(const RouterArgs& a, int cnt, hipStream_t s) {
+  const int g = row_grid(a.T);
+  if (cnt <= 1) router_topk_kernel<T, 1><<<g, 256, 0, s>>>(a);
+  else if (cnt <= 2) router_topk_kernel<T, 2><<<g, 256, 0, s>>>(a);
+  else if (cnt <= 4) router_topk_kernel<T, 4><<<g, 256, 0, s>>>(a);
+  else if (cnt <= 8) router_topk_kernel<T, 8><<<g, 256, 0, s>>>(a);
+  else if (cnt <= 16) router_topk_kernel<T, 16><<<g, 256, 0, s>>>(a);
+  else router_topk_kernel<T, 32><<<g, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_bwd(const RouterBwdArgs& a, hipStream_t s) {
+  const int g = row_grid(a.T), cnt = (a.E + 63) / 64;
+  if (cnt <= 1) router_topk_bwd_kernel<T, 1><<<g, 256, 0, s>>>(a);
+  else if (cnt <= 2) router_topk_bwd_kernel<T, 2><<<g, 256, 0, s>>>(a);
+  else if (cnt <= 4) router_topk_bwd_kernel<T, 4><<<g, 256, 0, s>>>(a);
+  else if (cnt <= 8) router_topk_bwd_kernel<T, 8><<<g, 256, 0, s>>>(a);
+  else router_topk_bwd_kernel<T, 16><<<g, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_router_topk(const RouterArgs& a, hipStream_t s) {
+  int gp = 1;
+  while (gp < a.G) gp *= 2;
+  const int lpg = 64 / gp, cnt = (a.E / a.G + lpg - 1) / lpg;
+  return a.bf16 ? launch_topk<uint16_t>(a, cnt, s) : launch_topk<float>(a, cnt, s);
+}
+
+hipError_t launch_router_topk_bwd(const RouterBwdArgs& a, hipStream_t s) {
+  return a.bf16 ? launch_bwd<uint16_t>(a, s) : launch_bwd<float>(a, s);
+}
+
+}  // namespace moe

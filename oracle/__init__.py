@@ -61,6 +61,7 @@ from .quant import (
     INT8_MAX,
     quant_int8,
     dequant_int8,
+    quant_act_t,
 )
 from .routing import (
     DEV_ID_RANGE,
@@ -69,9 +70,10 @@ from .routing import (
     route,
     pack_rows,
 )
-from .gemm import (grouped_gemm_bf16, grouped_gemm_fp8, grouped_gemm_fp8_fp4, grouped_gemm_int4, grouped_gemm_int8,
-                   segments)
-from .combine import combine, combine_fp32, f32_to_bf16_bits
+from .gemm import (dense_gemm_fp8, grouped_gemm_bf16, grouped_gemm_fp8, grouped_gemm_fp8_fp4, grouped_gemm_int4,
+                   grouped_gemm_int8, segments)
+from .combine import combine, combine_bwd, combine_fp32, f32_to_bf16_bits
+from .router import router_scores, router_topk, router_topk_bwd, router_weights
 from .activation import quant_act_values, silu, swiglu, swiglu_quant
 from .metrics import calc_diff, elementwise_ok, elementwise_excess
 
@@ -88,4 +90,6 @@ __all__ = [
     "calc_diff", "elementwise_ok", "elementwise_excess",
     "silu", "swiglu", "quant_act_values", "swiglu_quant",
     "INT8_MAX", "quant_int8", "dequant_int8", "grouped_gemm_int8",
+    "quant_act_t", "dense_gemm_fp8", "combine_bwd",
+    "router_scores", "router_topk", "router_topk_bwd", "router_weights",
 ]

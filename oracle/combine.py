@@ -95,3 +95,28 @@ def combine_fp32(y_bits: np.ndarray, output_index: np.ndarray, topk_weights: np.
         nxt = _fma_f32(np.broadcast_to(w[ok, r][:, None], (int(ok.sum()), N)), yv[p[ok]], acc[ok])
         acc[ok] = nxt
     return f32_to_bf16_bits(acc)
+
+
+def combine_bwd(dz, y, output_index, topk_weights):
+    """Gradient of combine() in float64: (dY [rows, N], named bool [rows], dweights [T, k]).
+
+    dY[p] is the sum over the slots naming p of weight * dZ[t]; rows that no slot names are not part of the
+    result (named is False there).  Slots with output_index outside [0, rows) are skipped.
+
+    Pinned by: the adjoint identity <dZ, combine(y + h v)> - <dZ, combine(y)> = h <dY, v> (combine is linear in
+    y), and the same in the weights.
+    """
+    dz = np.asarray(dz, dtype=np.float64)
+    y = np.asarray(y, dtype=np.float64)
+    T, k = output_index.shape
+    dy = np.zeros_like(y)
+    named = np.zeros(y.shape[0], dtype=bool)
+    dw = np.zeros((T, k), dtype=np.float64)
+    for t in range(T):
+        for r in range(k):
+            p = int(output_index[t, r])
+            if 0 <= p < y.shape[0]:
+                dy[p] += float(topk_weights[t, r]) * dz[t]
+                named[p] = True
+                dw[t, r] = float(dz[t] @ y[p])
+    return dy, named, dw

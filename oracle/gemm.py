@@ -36,7 +36,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from .formats import bf16_bits_to_f64
+from .formats import bf16_bits_to_f64, e4m3_decode_table
 from .quant import dequant_act, dequant_int8, dequant_weight_fp4, dequant_weight_fp8, dequant_weight_int4
 
 
@@ -176,3 +176,22 @@ def grouped_gemm_int8(a_q, sa, w_q, sw, counts, seg_offsets, rows_out=None, expe
         p0 = int(seg_offsets[e])
         out[p0:p0 + c] = dequant_int8(a_q[p0:p0 + c], sa[p0:p0 + c]) @ dequant_int8(w_q[wi], sw[wi]).T
     return out
+
+
+def dense_gemm_fp8(a_codes, sfa, w_codes, sfw, gran_n=128, c=None):
+    """(D, mag) float64 [M, N]: D = c + sum_kb sfa[m,kb] * sfw[n // gran_n, kb] * sum_{k in kb} a * w, and the same
+    sum over magnitudes (what rounding errors are relative to).  Scales are any fp32 values.
+
+    Pinned by: a plain loop over (m, n, k) on small operands, and grouped_gemm_fp8 with one expert on
+    power-of-two scales.
+    """
+    tab = e4m3_decode_table()
+    M, K = a_codes.shape
+    N = w_codes.shape[0]
+    sa = np.repeat(np.asarray(sfa, dtype=np.float64), 128, axis=1)
+    sw = np.repeat(np.asarray(sfw, dtype=np.float64)[np.arange(N) // gran_n], 128, axis=1)
+    a, w = tab[a_codes] * sa, tab[w_codes] * sw
+    d, mag = a @ w.T, np.abs(a) @ np.abs(w).T
+    if c is not None:
+        d, mag = d + np.asarray(c, dtype=np.float64), mag + np.abs(np.asarray(c, dtype=np.float64))
+    return d, mag

@@ -252,3 +252,15 @@ def quant_int8(x_bits: np.ndarray):
 def dequant_int8(q: np.ndarray, s: np.ndarray) -> np.ndarray:
     """float64 [..., K] = q * s of the value's 128-block."""
     return np.asarray(q, dtype=np.float64) * np.repeat(np.asarray(s, dtype=np.float64), BLOCK, axis=-1)
+
+
+def quant_act_t(x_bits: np.ndarray):
+    """Transposing quantiser: bf16 patterns [M, K] -> codes uint8 [K, Mp], scales float32 [K, Mp/128], Mp = M
+    rounded up to 128, rows past M zero: quant_act of the padded transpose.
+
+    Pinned by: quant_act's own pins (the transposition and the padding are written out here).
+    """
+    M, K = x_bits.shape
+    pad = np.zeros((-(-M // BLOCK) * BLOCK, K), dtype=np.uint16)
+    pad[:M] = x_bits
+    return quant_act(np.ascontiguousarray(pad.T))
