@@ -13,6 +13,16 @@
 // result on normal data, at most 7 * 2^-13 of the sum of magnitudes.  A bf16 output rounds 100 times coarser, so it
 // takes them; an fp32 output (a gradient that is added up over steps) gets its products from the bf16
 // instruction, half as fast, in which E4M3 codes are exact and every product counts in full (1e-8).
+//
+// Tile.  A workgroup of WM x WN waves computes 16*RB*WM rows x 16*CB*WN columns.  The weight tile is the
+// instruction's A operand (output columns), the activations its B operand (rows), so a lane holds 4 consecutive
+// columns of one row.  Both operands' K blocks are copied global -> LDS (global_load_lds, 16-byte chunks XOR-swizzled
+// through the source address) into two slots; block kb + 1 is copied while block kb is multiplied.  The barrier that
+// publishes block kb + 1 sits before the promotion of the step's last row block, when every wave holds its last
+// fragments of block kb in registers, so the next block's first fragments are read behind matrix instructions and
+// promotions.  Scales come 4 K blocks at a time (one 16-byte copy per row).
+#include <type_traits>
+
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -20,11 +30,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kXcd = 8;
 
-__device__ __forceinline__ v4f mfma_fp8(const v8i w, const v8i x) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7f7f7f7f, 0,
-                                                          0x7f7f7f7f);
+// 64 lanes x 16 bytes global -> LDS: lane i's bytes from base + voff to lds + 16 i.
+__device__ __forceinline__ void copy16(uint32_t voff, const void* base, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds) : "memory");
 }
 
 // The bf16 values of 8 E4M3 codes (exact).
@@ -55,7 +65,10 @@ struct Frag<true> {
     v[3] = to_bf16(hi[2], hi[3]);
   }
 };
-__device__ __forceinline__ v4f block_sum(const Frag<false>& w, const Frag<false>& x) { return mfma_fp8(w.v, x.v); }
+__device__ __forceinline__ v4f block_sum(const Frag<false>& w, const Frag<false>& x) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7f7f7f7f, 0,
+                                                          0x7f7f7f7f);
+}
 __device__ __forceinline__ v4f block_sum(const Frag<true>& w, const Frag<true>& x) {
   v4f s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -63,76 +76,232 @@ __device__ __forceinline__ v4f block_sum(const Frag<true>& w, const Frag<true>& 
   return s;
 }
 
-// Four consecutive columns n .. n + 3 of row m.
-__device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v) {
-  if (m >= a.M) return;
+// Four consecutive columns n .. n + 3 of row m (vec: they may be accessed as one vector where all four exist).
+__device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v, bool vec) {
+  if (m >= a.M || n >= a.N) return;
+  const int64_t at = (int64_t)m * a.ldd + n;
+  if (vec && n + 4 <= a.N) {
+    if (a.f32) {
+      if (a.C) v += *(const v4f*)(a.C + (int64_t)m * a.ldc + n);
+      *(v4f*)((float*)a.D + at) = v;
+    } else {
+      uint2 o;
+      o.x = f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16);
+      o.y = f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16);
+      *(uint2*)((uint16_t*)a.D + at) = o;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (n + i >= a.N) return;
-    float o = v[i];
-    if (a.C) o += a.C[(int64_t)m * a.ldc + n + i];
     if (a.f32)
-      ((float*)a.D)[(int64_t)m * a.ldd + n + i] = o;
+      ((float*)a.D)[at + i] = a.C ? v[i] + a.C[(int64_t)m * a.ldc + n + i] : v[i];
     else
-      ((uint16_t*)a.D)[(int64_t)m * a.ldd + n + i] = (uint16_t)f32_to_bf16_rne(o);
+      ((uint16_t*)a.D)[at + i] = (uint16_t)f32_to_bf16_rne(v[i]);
   }
 }
 
-template <bool WIDE>
-__global__ __launch_bounds__(256) void gemm_dense_kernel(const DenseArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t sA[kTile * 128], sW[kTile * 128];
-  __shared__ float s_sa[kTile], s_sw[kTile];
-  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6);
+template <int RB, int CB, int WM, int WN>
+struct TileCfg {
+  static constexpr int NW = WM * WN;
+  static constexpr int BM = 16 * RB * WM, BN = 16 * CB * WN;
+  static constexpr int kPieces = (BM + BN) / 8;         // 1 KB copies (8 rows) per K block
+  static constexpr int kPw = (kPieces + NW - 1) / NW;   // per wave
+  static constexpr int kSlot = (BM + BN) * 128;
+  static constexpr int kScale = (BM + BN) * 16;         // one group of 4 K blocks
+  static constexpr int kLds = 2 * kSlot + 2 * kScale;
+  static_assert(kPieces % NW == 0, "every wave copies the same number of pieces");
+  static_assert((BM + BN) % 64 == 0 && BM % 64 == 0, "scale rows in whole waves");
+  static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs a) {
+  using C = TileCfg<RB, CB, WM, WN>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
+  const int lane = lane_id(), wv = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int KB = a.K / 128;
-  const int nt = (a.N + kTile - 1) / kTile;
-  const int m0 = (int)(blockIdx.x / nt) * kTile, n0 = (int)(blockIdx.x % nt) * kTile;
-  const int wm = (wv >> 1) * 64, wn = (wv & 1) * 64;
-  v4f acc[4][4];
+
+  // Workgroup b runs on XCD b % 8: consecutive tiles go to one XCD, and consecutive tiles are blocks of up to 8
+  // column tiles by a few row tiles, so an XCD's workgroups share both operands in its L2.
+  const int mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
+  const int tiles = mt * nt;
+  int t = blockIdx.x;
+  {
+    const int per = tiles / kXcd, rem = tiles % kXcd, x = t % kXcd, i = t / kXcd;
+    t = x * per + min(x, rem) + i;
+  }
+  const int gn = 8, g = t / (mt * gn), gw = min(gn, nt - g * gn), r = t - g * mt * gn;
+  const int m0 = uniform(r / gw * C::BM), n0 = uniform((g * gn + r % gw) * C::BN);
+
+  const int wm = (wv / WN) * 16 * RB, wn = (wv % WN) * 16 * CB;
+  const uint32_t lds0 = lds_offset(sm);
+
+  // copies: this wave's pieces q = wv, wv + NW, ...; rows of the A tile, then of the W tile
+  const uint8_t* abase = a.A + (int64_t)m0 * a.lda;
+  const uint8_t* wbase = a.W + (int64_t)n0 * a.ldw;
+  uint32_t voff[C::kPw];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int kb = 0; kb < KB; ++kb) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = tid + 256 * i, r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
-      *(v4i*)(sA + 16 * q) = *(const v4i*)(a.A + (int64_t)min(m0 + r, a.M - 1) * a.lda + (int64_t)kb * 128 + 16 * c);
-      *(v4i*)(sW + 16 * q) = *(const v4i*)(a.W + (int64_t)min(n0 + r, a.N - 1) * a.ldw + (int64_t)kb * 128 + 16 * c);
-    }
-    if (tid < kTile)
-      s_sa[tid] = a.SFA[(int64_t)min(m0 + tid, a.M - 1) * KB + kb];
+  for (int i = 0; i < C::kPw; ++i) {
+    const int q = wv + C::NW * i;
+    int row = 8 * q + (lane >> 3);
+    const int c = (lane & 7) ^ ((row >> 1) & 7);
+    if (row < C::BM)
+      voff[i] = (uint32_t)min(row, a.M - 1 - m0) * (uint32_t)a.lda + 16u * c;
     else
-      s_sw[tid - kTile] = a.SFW[(int64_t)(min(n0 + tid - kTile, a.N - 1) / a.gran_n) * KB + kb];
-    __syncthreads();
-    Frag<WIDE> xf[4];
+      voff[i] = (uint32_t)min(row - C::BM, a.N - 1 - n0) * (uint32_t)a.ldw + 16u * c;
+  }
+  auto copy_piece = [&](int kb, int i) {
+    const int q = wv + C::NW * i;
+    const uint8_t* base = (8 * q < C::BM ? abase : wbase) + (int64_t)kb * 128;
+    copy16(voff[i], base, uniform(lds0 + (kb & 1) * C::kSlot + 1024 * q));
+  };
+
+  // scales: group g4 (K blocks 4 g4 ..) of row r of the tiles at 16 r of buffer g4 & 1
+  const bool sc_vec = KB % 4 == 0 && (((uintptr_t)a.SFA | (uintptr_t)a.SFW) & 15) == 0;
+  auto scales = [&](int g4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = wm + 16 * i + l16, sw = (r >> 1) & 7;
-      const v4i lo = *(const v4i*)(sA + r * 128 + 16 * (lg ^ sw)), hi = *(const v4i*)(sA + r * 128 + 16 * ((4 + lg) ^ sw));
-      xf[i].load(lo, hi);
-    }
+    for (int q = 0; q < (C::BM + C::BN) / 64; q += C::NW) {
+      const int p = q + wv;
+      if (p * 64 >= C::BM + C::BN) break;
+      const int row = 64 * p + lane;
+      const bool is_a = 64 * p < C::BM;
+      const float* base = is_a ? a.SFA : a.SFW;
+      const int64_t sr = is_a ? min(m0 + row, a.M - 1) : (GRAN1 ? min(n0 + row - C::BM, a.N - 1)
+                                                                 : min(n0 + row - C::BM, a.N - 1) / 128);
+      const uint32_t dst = lds0 + 2 * C::kSlot + (g4 & 1) * C::kScale;
+      if (sc_vec) {
+        const int64_t sr0 = is_a ? m0 : (GRAN1 ? n0 : n0 / 128);
+        copy16((uint32_t)(sr - sr0) * (uint32_t)KB * 4u, base + sr0 * KB + 4 * g4, uniform(dst + 1024 * p));
+      } else {
+        const float* s = base + sr * KB;
+        v4f v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = wn + 16 * j + l16, sw = (r >> 1) & 7;
-      const v4i lo = *(const v4i*)(sW + r * 128 + 16 * (lg ^ sw)), hi = *(const v4i*)(sW + r * 128 + 16 * ((4 + lg) ^ sw));
-      Frag<WIDE> wf;
-      wf.load(lo, hi);
-      const v4f sw4 = *(const v4f*)(s_sw + wn + 16 * j + 4 * lg);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v4f p = block_sum(wf, xf[i]);
-        const float sa = s_sa[wm + 16 * i + l16];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], sa * sw4[e], acc[i][j][e]);
+        for (int j = 0; j < 4; ++j) v[j] = s[min(4 * g4 + j, KB - 1)];
+        *(v4f*)(sm + 2 * C::kSlot + (g4 & 1) * C::kScale + 16 * row) = v;
       }
     }
+  };
+
+  // fragment read offsets: row l16 of a 16-row block at 128 l16, its chunk c at position c ^ ((row >> 1) & 7)
+  const int fsw = (l16 >> 1) & 7;
+  const int off_lo = l16 * 128 + 16 * (lg ^ fsw), off_hi = l16 * 128 + 16 * ((4 + lg) ^ fsw);
+  auto frag = [&](Frag<WIDE>& f, int kb, int row) {
+    const uint8_t* p = sm + (kb & 1) * C::kSlot + row * 128;
+    f.load(*(const v4i*)(p + off_lo), *(const v4i*)(p + off_hi));
+  };
+
+  v4f acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  Frag<WIDE> wf[CB], xf[2];
+  float sa[RB];
+  v4f sw[GRAN1 ? CB : 1];
+
+  // the first fragments and the scales of block kb
+  auto first = [&](int kb) {
+#pragma unroll
+    for (int j = 0; j < CB; ++j) frag(wf[j], kb, C::BM + wn + 16 * j);
+    frag(xf[0], kb, wm);
+    const float* s = (const float*)(sm + 2 * C::kSlot + ((kb >> 2) & 1) * C::kScale) + (kb & 3);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) sa[i] = s[4 * (wm + 16 * i + l16)];
+    if constexpr (GRAN1) {
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sw[j][e] = s[4 * (C::BM + wn + 16 * j + 4 * lg + e)];
+    } else {
+      sw[0][0] = s[4 * (C::BM + wn)];
+    }
+  };
+
+  scales(0);
+#pragma unroll
+  for (int i = 0; i < C::kPw; ++i) copy_piece(0, i);
+  wait_vmcnt<0>();
+  barrier_lds();
+  first(0);
+
+  // One K block.  Row block i's matrix instructions alternate with the promotion of row block i - 1.
+  auto step = [&](int kb, auto more_c) {
+    constexpr bool more = decltype(more_c)::value;
+    v4f sum[2][CB];
+    float sax[RB];
+    v4f swx[GRAN1 ? CB : 1];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) sax[i] = GRAN1 ? sa[i] : sa[i] * sw[0][0];
+    if constexpr (GRAN1) {
+#pragma unroll
+      for (int j = 0; j < CB; ++j) swx[j] = sw[j];
+    }
+    auto promote = [&](int i, int j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float s = GRAN1 ? sax[i] * swx[j][e] : sax[i];
+        acc[i][j][e] = __builtin_fmaf(sum[i & 1][j][e], s, acc[i][j][e]);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      if (i + 1 < RB) frag(xf[(i + 1) & 1], kb, wm + 16 * (i + 1));
+      if constexpr (more) {  // the next block's copies, spread over the first row blocks
+        constexpr int kSpread = RB > 1 ? (RB + 1) / 2 : 1, kEach = (C::kPw + kSpread - 1) / kSpread;
+#pragma unroll
+        for (int c = i * kEach; c < (i + 1) * kEach && c < C::kPw; ++c) copy_piece(kb + 1, c);
+      }
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        sum[i & 1][j] = block_sum(wf[j], xf[i & 1]);
+        if (i > 0) promote(i - 1, j);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // keep the row blocks' order (hoisted fragments would spill)
+    }
+    if constexpr (more) {
+      wait_vmcnt<0>();
+      barrier_lds();
+      first(kb + 1);
+    }
+#pragma unroll
+    for (int j = 0; j < CB; ++j) promote(RB - 1, j);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int kb = 0; kb + 1 < KB; ++kb) {
+    if ((kb & 3) == 0 && kb + 4 < KB) scales((kb >> 2) + 1);
+    step(kb, std::true_type{});
   }
+  step(KB - 1, std::false_type{});
+
+  // The sums are whole before any lane's store is masked off: without this the compiler moves the last matrix
+  // instructions, and the loads of their operands, under the stores' masks, where the other lanes' operands are stale.
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RB; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) store4(a, m0 + wm + 16 * i + l16, n0 + wn + 16 * j + 4 * lg, acc[i][j]);
+    for (int j = 0; j < CB; ++j) asm volatile("" : "+v"(acc[i][j]));
+  const bool vec = a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
+                   (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) store4(a, m0 + wm + 16 * i + l16, n0 + wn + 16 * j + 4 * lg, acc[i][j], vec);
+}
+
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
+  using C = TileCfg<RB, CB, WM, WN>;
+  const int tiles = ((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN);
+  gemm_dense_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<(unsigned)tiles, WM * WN * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool WIDE, bool GRAN1>
+hipError_t launch_dense(const DenseArgs& a, hipStream_t s) {
+  if constexpr (WIDE) return launch_tile<WIDE, GRAN1, 4, 4, 2, 2>(a, s);
+  else return launch_tile<WIDE, GRAN1, 8, 4, 2, 4>(a, s);
 }
 
 }  // namespace
@@ -140,12 +309,9 @@ __global__ __launch_bounds__(256) void gemm_dense_kernel(const DenseArgs a) {
 int64_t dense_workspace_bytes(int, int, int) { return 0; }
 
 hipError_t launch_gemm_dense(const DenseArgs& a, hipStream_t s) {
-  const int64_t tiles = (int64_t)((a.M + kTile - 1) / kTile) * ((a.N + kTile - 1) / kTile);
-  if (a.f32)
-    gemm_dense_kernel<true><<<(unsigned)tiles, 256, 0, s>>>(a);
-  else
-    gemm_dense_kernel<false><<<(unsigned)tiles, 256, 0, s>>>(a);
-  return hipGetLastError();
+  const bool g1 = a.gran_n == 1;
+  if (a.f32) return g1 ? launch_dense<true, true>(a, s) : launch_dense<true, false>(a, s);
+  return g1 ? launch_dense<false, true>(a, s) : launch_dense<false, false>(a, s);
 }
 
 }  // namespace moe
