@@ -111,12 +111,13 @@ def load(path: str = LIB_PATH):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(status: int, fn: str):
@@ -140,25 +141,29 @@ def _dev(t, name, dtype=None, ndim=None):
 
 def _rows(t, name, dtypes):
     """A 2-D GPU tensor whose rows are contiguous; returns its row stride in elements."""
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    row_stride, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return row_stride if rows > 1 else max(cols, 1)
 
 
 def _one_device(fn, stream, *tensors):
-    """The tensors lie on one device, the stream's (or the current one): a kernel is launched there."""
-    dev = torch.cuda.current_device() if stream is None else stream.device.index
-    if dev != torch.cuda.current_device():
+    """The tensors lie on the current device, and so does the stream: a kernel is launched there.  Returns the stream's
+    handle."""
+    dev = torch._C._cuda_getDevice()
+    if stream is not None and stream.device.index != dev:
         raise ValueError(f"{fn}: the stream is not on the current device")
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{fn}: a tensor is on {t.device}, the call on cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _row_bytes(t) -> int:
@@ -505,10 +510,10 @@ def moe_unpermute_combine_bwd(dZ, Y, output_index, topk_weights, dY, dweights, w
                            ("dweights", dweights, (T, k)), ("Y", Y, (y_rows, N)), ("dY", dY, (y_rows, N))):
         if t is not None and tuple(t.shape) != shape:
             raise ValueError(f"moe_unpermute_combine_bwd: {name} is {tuple(t.shape)}, needs {shape}")
-    _one_device("moe_unpermute_combine_bwd", stream, dZ, Y, output_index, topk_weights, dY, dweights, workspace)
+    hs = _one_device("moe_unpermute_combine_bwd", stream, dZ, Y, output_index, topk_weights, dY, dweights, workspace)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().moe_unpermute_combine_bwd(_ptr(dZ), _ptr(Y), y_rows, _ptr(output_index), _ptr(topk_weights), T, k, N,
-                                            _ptr(dY), _ptr(dweights), _ptr(workspace), ws_bytes, _stream(stream)),
+                                            _ptr(dY), _ptr(dweights), _ptr(workspace), ws_bytes, hs),
            "moe_unpermute_combine_bwd")
 
 
@@ -532,10 +537,10 @@ def moe_router_topk(logits, topk_ids, topk_weights, score: str = "softmax", bias
     if topk_ids.shape[0] != T or tuple(topk_weights.shape) != (T, k) or (bias is not None and bias.shape[0] != E):
         raise ValueError(f"{fn}: shape mismatch")
     sc = _score(fn, score)
-    _one_device(fn, stream, logits, topk_ids, topk_weights, bias)
+    hs = _one_device(fn, stream, logits, topk_ids, topk_weights, bias)
     _check(load().moe_router_topk(_ptr(logits), BF16 if logits.dtype == torch.bfloat16 else F32, ld, _ptr(bias), T, E,
                                   k, sc, n_group, topk_group, group_top, int(renormalize), scale, _ptr(topk_ids),
-                                  _ptr(topk_weights), _stream(stream)), fn)
+                                  _ptr(topk_weights), hs), fn)
 
 
 def moe_router_topk_bwd(logits, topk_ids, dweights, dlogits, score: str = "softmax", renormalize: bool = True,
@@ -550,10 +555,10 @@ def moe_router_topk_bwd(logits, topk_ids, dweights, dlogits, score: str = "softm
     if tuple(dlogits.shape) != (T, E) or topk_ids.shape[0] != T or tuple(dweights.shape) != (T, k):
         raise ValueError(f"{fn}: shape mismatch")
     sc = _score(fn, score)
-    _one_device(fn, stream, logits, topk_ids, dweights, dlogits)
+    hs = _one_device(fn, stream, logits, topk_ids, dweights, dlogits)
     _check(load().moe_router_topk_bwd(_ptr(logits), BF16 if logits.dtype == torch.bfloat16 else F32, ld,
                                       _ptr(topk_ids), _ptr(dweights), T, E, k, sc, int(renormalize), scale,
-                                      _ptr(dlogits), ldd, _stream(stream)), fn)
+                                      _ptr(dlogits), ldd, hs), fn)
 
 
 def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -579,11 +584,11 @@ def moe_gemm_fp8(A, SFA, W, SFW, D, C=None, workspace=None, stream=None):
         raise ValueError(f"{fn}: SFA is {tuple(SFA.shape)} (needs {(M, K // 128)}), SFW {tuple(SFW.shape)} "
                          f"(needs {(nb, K // 128)} or {(N, K // 128)})")
     gran = 128 if SFW.shape[0] == nb else 1
-    _one_device(fn, stream, A, SFA, W, SFW, D, C, workspace)
+    hs = _one_device(fn, stream, A, SFA, W, SFW, D, C, workspace)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().moe_gemm_fp8(_ptr(A), lda, _ptr(SFA), _ptr(W), ldw, _ptr(SFW), gran, _ptr(D),
                                BF16 if D.dtype == torch.bfloat16 else F32, ldd, _ptr(C), ldc, M, N, K,
-                               _ptr(workspace), ws_bytes, _stream(stream)), fn)
+                               _ptr(workspace), ws_bytes, hs), fn)
 
 
 def moe_quant_act_t(x, q, sf, stream=None):
@@ -596,8 +601,8 @@ def moe_quant_act_t(x, q, sf, stream=None):
     mb = (M + 127) // 128
     if tuple(q.shape) != (K, 128 * mb) or tuple(sf.shape) != (K, mb):
         raise ValueError(f"{fn}: q is {tuple(q.shape)}, sf {tuple(sf.shape)}, need {(K, 128 * mb)} and {(K, mb)}")
-    _one_device(fn, stream, x, q, sf)
-    _check(load().moe_quant_act_t(_ptr(x), M, K, ldx, _ptr(q), _ptr(sf), _stream(stream)), fn)
+    hs = _one_device(fn, stream, x, q, sf)
+    _check(load().moe_quant_act_t(_ptr(x), M, K, ldx, _ptr(q), _ptr(sf), hs), fn)
 
 
 def moe_stream_read_words() -> int:

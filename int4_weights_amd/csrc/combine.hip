@@ -132,16 +132,21 @@ __device__ inline void shared_row(const CombineBwdArgs& a, int p, int64_t own, i
   }
 }
 
-__global__ __launch_bounds__(256) void combine_bwd_kernel(const CombineBwdArgs a) {
+// NT threads per token: 256 where there are tokens enough to fill the chip, else 1024, so that a row (up to 8192
+// columns) is in flight at once (61 tokens x 8 slots x 7168 columns: XX).
+template <int NT>
+__global__ __launch_bounds__(NT) void combine_bwd_kernel(const CombineBwdArgs a) {
   constexpr int B = 8;  // slots per batch
+  constexpr int kScan = (kRouteSmallMax + NT - 1) / NT;
   __shared__ int s_cnt[B], s_own[B];
-  __shared__ float s_sum[4][B];
+  __shared__ float s_sum[NT / 64][B];
   const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
   const int chunks = a.N / 8;
-  const int64_t R = (int64_t)a.T * a.k;
+  const int R = a.T * a.k;
+  const bool scan = a.dY && !a.who;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     for (int r0 = 0; r0 < a.k; r0 += B) {
-      const int64_t i0 = (int64_t)t * a.k + r0;
+      const int i0 = t * a.k + r0;
       int p[B];
       float w[B];
 #pragma unroll
@@ -150,71 +155,72 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const CombineBwdArgs a
         if (p[j] >= a.y_rows) p[j] = -1;
         w[j] = r0 + j < a.k && a.dY ? a.w[i0 + j] : 0.0f;
       }
+      int o[kScan];  // this thread's share of output_index: loaded with the batch's own, compared below
+#pragma unroll
+      for (int u = 0; u < kScan; ++u) o[u] = scan && tid + NT * u < R ? a.oi[tid + NT * u] : -1;
       bool write[B], shared = false;
-      if (a.dY) {
-        if (a.who) {
 #pragma unroll
-          for (int j = 0; j < B; ++j) {
-            write[j] = p[j] >= 0;
-            if (p[j] >= 0 && a.who[p[j]].x != 1) {
-              write[j] = false;
-              shared = true;
-            }
-          }
-        } else {
-          if (tid < B) {
-            s_cnt[tid] = 0;
-            s_own[tid] = 0x7fffffff;
-          }
-          __syncthreads();
-          for (int i = tid; i < (int)R; i += 256) {
-            const int o = a.oi[i];
+      for (int j = 0; j < B; ++j) write[j] = a.dY && p[j] >= 0;
+      if (a.dY && a.who) {
 #pragma unroll
-            for (int j = 0; j < B; ++j)
-              if (o == p[j] && o >= 0) {
-                atomicAdd(&s_cnt[j], 1);
-                atomicMin(&s_own[j], i);
-              }
+        for (int j = 0; j < B; ++j)
+          if (p[j] >= 0 && a.who[p[j]].x != 1) {
+            write[j] = false;
+            shared = true;
           }
-          __syncthreads();
-#pragma unroll
-          for (int j = 0; j < B; ++j) {
-            write[j] = p[j] >= 0 && s_cnt[j] == 1;
-            shared = shared || (p[j] >= 0 && s_cnt[j] != 1);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < B; ++j) write[j] = false;
       }
-
       float dot[B];
 #pragma unroll
       for (int j = 0; j < B; ++j) dot[j] = 0.0f;
-      for (int c = tid; c < chunks; c += 256) {
-        float dz[8];
-        unpack8(*(const v4i*)(a.dZ + (int64_t)t * a.N + 8 * c), dz);
-        if (a.dw) {
-          v4i y[B];
+      v4i dzv = {0, 0, 0, 0}, y[B];
+      auto load = [&](int c) {
+        dzv = *(const v4i*)(a.dZ + (int64_t)t * a.N + 8 * c);
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+          y[j] = a.dw && p[j] >= 0 ? __builtin_nontemporal_load((const v4i*)(a.Y + (int64_t)p[j] * a.N + 8 * c))
+                                   : v4i{0, 0, 0, 0};
+      };
+      if (tid < chunks) load(tid);
+      if (scan) {  // behind the first rows' loads
+        if (tid < B) {
+          s_cnt[tid] = 0;
+          s_own[tid] = 0x7fffffff;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kScan; ++u)
 #pragma unroll
           for (int j = 0; j < B; ++j)
-            y[j] = p[j] >= 0 ? __builtin_nontemporal_load((const v4i*)(a.Y + (int64_t)p[j] * a.N + 8 * c))
-                             : v4i{0, 0, 0, 0};
+            if (o[u] >= 0 && o[u] == p[j]) {
+              atomicAdd(&s_cnt[j], 1);
+              atomicMin(&s_own[j], tid + NT * u);
+            }
+        __syncthreads();
 #pragma unroll
-          for (int j = 0; j < B; ++j) {
-            float f[8];
-            unpack8(y[j], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(f[i], dz[i], dot[j]);
+        for (int j = 0; j < B; ++j)
+          if (p[j] >= 0 && s_cnt[j] != 1) {
+            write[j] = false;
+            shared = true;
           }
+      }
+      for (int c = tid; c < chunks; c += NT) {
+        if (c != tid) load(c);
+        float dz[8];
+        unpack8(dzv, dz);
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          float f[8];
+          unpack8(y[j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(f[i], dz[i], dot[j]);
         }
 #pragma unroll
         for (int j = 0; j < B; ++j) {
           if (!write[j]) continue;
-          float o[8];
+          float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = w[j] * dz[i];
-          __builtin_nontemporal_store(pack8(o), (v4i*)(a.dY + (int64_t)p[j] * a.N + 8 * c));
+          for (int i = 0; i < 8; ++i) v[i] = w[j] * dz[i];
+          __builtin_nontemporal_store(pack8(v), (v4i*)(a.dY + (int64_t)p[j] * a.N + 8 * c));
         }
       }
       if (shared) {
@@ -234,8 +240,12 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const CombineBwdArgs a
           if (lane == 0) s_sum[wv][j] = dot[j];
         }
         __syncthreads();
-        if (tid < B && r0 + tid < a.k)
-          a.dw[i0 + tid] = (s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]);
+        if (tid < B && r0 + tid < a.k) {
+          float s = 0.0f;
+#pragma unroll
+          for (int v = 0; v < NT / 64; ++v) s += s_sum[v][tid];
+          a.dw[i0 + tid] = s;
+        }
       }
       __syncthreads();  // s_cnt, s_own and s_sum are reused
     }
@@ -256,7 +266,10 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  combine_bwd_kernel<<<(unsigned)(a.T < cap ? a.T : cap), 256, 0, s>>>(a);
+  if (a.T < 2 * device_info().cus)
+    combine_bwd_kernel<1024><<<(unsigned)a.T, 1024, 0, s>>>(a);
+  else
+    combine_bwd_kernel<256><<<(unsigned)(a.T < cap ? a.T : cap), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

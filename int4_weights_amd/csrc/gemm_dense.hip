@@ -21,8 +21,6 @@
 // publishes block kb + 1 sits before the promotion of the step's last row block, when every wave holds its last
 // fragments of block kb in registers, so the next block's first fragments are read behind matrix instructions and
 // promotions.  Scales come 4 K blocks at a time (one 16-byte copy per row).
-#include <type_traits>
-
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -102,7 +100,7 @@ __device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v, 
   }
 }
 
-template <int RB, int CB, int WM, int WN>
+template <int RB, int CB, int WM, int WN, int S>
 struct TileCfg {
   static constexpr int NW = WM * WN;
   static constexpr int BM = 16 * RB * WM, BN = 16 * CB * WN;
@@ -110,19 +108,26 @@ struct TileCfg {
   static constexpr int kPw = (kPieces + NW - 1) / NW;   // per wave
   static constexpr int kSlot = (BM + BN) * 128;
   static constexpr int kScale = (BM + BN) * 16;         // one group of 4 K blocks
-  static constexpr int kLds = 2 * kSlot + 2 * kScale;
+  // Scale groups are copied kAhead groups early: their copies are older than the kPw * (S - 2) newest that the wait
+  // before their first use leaves in flight (4 blocks' copies are issued per group).
+  static constexpr int kAhead = S > 6 ? 2 : 1, kScBufs = 2 * kAhead;
+  static constexpr int kLds = S * kSlot + kScBufs * kScale;
   static_assert(kPieces % NW == 0, "every wave copies the same number of pieces");
+  static_assert(S >= 2 && S <= 4 * kAhead + 2 && kPw * (S - 2) < 64, "scales ahead of their use; vmcnt's range");
   static_assert((BM + BN) % 64 == 0 && BM % 64 == 0, "scale rows in whole waves");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
-template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN, int S>
 __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs a) {
-  using C = TileCfg<RB, CB, WM, WN>;
+  using C = TileCfg<RB, CB, WM, WN, S>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
   const int lane = lane_id(), wv = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int KB = a.K / 128;
+  // this workgroup's K blocks (split K: a multiple of 4 per split)
+  const int per_split = ((KB + 3) / 4 + a.splits - 1) / a.splits * 4;
+  const int kb0 = uniform(min((int)blockIdx.y * per_split, KB)), kb1 = uniform(min(kb0 + per_split, KB));
 
   // Workgroup b runs on XCD b % 8: consecutive tiles go to one XCD, and consecutive tiles are blocks of up to 8
   // column tiles by a few row tiles, so an XCD's workgroups share both operands in its L2.
@@ -156,7 +161,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
   auto copy_piece = [&](int kb, int i) {
     const int q = wv + C::NW * i;
     const uint8_t* base = (8 * q < C::BM ? abase : wbase) + (int64_t)kb * 128;
-    copy16(voff[i], base, uniform(lds0 + (kb & 1) * C::kSlot + 1024 * q));
+    copy16(voff[i], base, uniform(lds0 + (kb % S) * C::kSlot + 1024 * q));
   };
 
   // scales: group g4 (K blocks 4 g4 ..) of row r of the tiles at 16 r of buffer g4 & 1
@@ -171,7 +176,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
       const float* base = is_a ? a.SFA : a.SFW;
       const int64_t sr = is_a ? min(m0 + row, a.M - 1) : (GRAN1 ? min(n0 + row - C::BM, a.N - 1)
                                                                  : min(n0 + row - C::BM, a.N - 1) / 128);
-      const uint32_t dst = lds0 + 2 * C::kSlot + (g4 & 1) * C::kScale;
+      const uint32_t dst = lds0 + S * C::kSlot + (g4 & (C::kScBufs - 1)) * C::kScale;
       if (sc_vec) {
         const int64_t sr0 = is_a ? m0 : (GRAN1 ? n0 : n0 / 128);
         copy16((uint32_t)(sr - sr0) * (uint32_t)KB * 4u, base + sr0 * KB + 4 * g4, uniform(dst + 1024 * p));
@@ -180,7 +185,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
         v4f v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = s[min(4 * g4 + j, KB - 1)];
-        *(v4f*)(sm + 2 * C::kSlot + (g4 & 1) * C::kScale + 16 * row) = v;
+        *(v4f*)(sm + S * C::kSlot + (g4 & (C::kScBufs - 1)) * C::kScale + 16 * row) = v;
       }
     }
   };
@@ -189,7 +194,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
   const int fsw = (l16 >> 1) & 7;
   const int off_lo = l16 * 128 + 16 * (lg ^ fsw), off_hi = l16 * 128 + 16 * ((4 + lg) ^ fsw);
   auto frag = [&](Frag<WIDE>& f, int kb, int row) {
-    const uint8_t* p = sm + (kb & 1) * C::kSlot + row * 128;
+    const uint8_t* p = sm + (kb % S) * C::kSlot + row * 128;
     f.load(*(const v4i*)(p + off_lo), *(const v4i*)(p + off_hi));
   };
 
@@ -207,7 +212,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
 #pragma unroll
     for (int j = 0; j < CB; ++j) frag(wf[j], kb, C::BM + wn + 16 * j);
     frag(xf[0], kb, wm);
-    const float* s = (const float*)(sm + 2 * C::kSlot + ((kb >> 2) & 1) * C::kScale) + (kb & 3);
+    const float* s = (const float*)(sm + S * C::kSlot + ((kb >> 2) & (C::kScBufs - 1)) * C::kScale) + (kb & 3);
 #pragma unroll
     for (int i = 0; i < RB; ++i) sa[i] = s[4 * (wm + 16 * i + l16)];
     if constexpr (GRAN1) {
@@ -220,16 +225,27 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
     }
   };
 
-  scales(0);
+  if (kb0 < kb1) {
 #pragma unroll
-  for (int i = 0; i < C::kPw; ++i) copy_piece(0, i);
-  wait_vmcnt<0>();
+  for (int g4 = 0; g4 < C::kAhead; ++g4)
+    if (kb0 + 4 * g4 < kb1) scales((kb0 >> 2) + g4);
+#pragma unroll
+  for (int b = 0; b < S - 1; ++b)
+    if (kb0 + b < kb1) {
+#pragma unroll
+      for (int i = 0; i < C::kPw; ++i) copy_piece(kb0 + b, i);
+    }
+  if (kb0 + S - 1 <= kb1)
+    wait_vmcnt<C::kPw * (S - 2)>();
+  else
+    wait_vmcnt<0>();
   barrier_lds();
-  first(0);
+  first(kb0);
 
   // One K block.  Row block i's matrix instructions alternate with the promotion of row block i - 1.
-  auto step = [&](int kb, auto more_c) {
-    constexpr bool more = decltype(more_c)::value;
+  // kind 2: block kb + S - 1 is copied meanwhile; 1: no more copies, but a next block; 0: the last block.
+  auto step = [&](int kb, auto kind) {
+    constexpr bool copies = decltype(kind)::value == 2, more = decltype(kind)::value > 0;
     v4f sum[2][CB];
     float sax[RB];
     v4f swx[GRAN1 ? CB : 1];
@@ -249,10 +265,10 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
       if (i + 1 < RB) frag(xf[(i + 1) & 1], kb, wm + 16 * (i + 1));
-      if constexpr (more) {  // the next block's copies, spread over the first row blocks
+      if constexpr (copies) {  // spread over the first row blocks
         constexpr int kSpread = RB > 1 ? (RB + 1) / 2 : 1, kEach = (C::kPw + kSpread - 1) / kSpread;
 #pragma unroll
-        for (int c = i * kEach; c < (i + 1) * kEach && c < C::kPw; ++c) copy_piece(kb + 1, c);
+        for (int c = i * kEach; c < (i + 1) * kEach && c < C::kPw; ++c) copy_piece(kb + S - 1, c);
       }
 #pragma unroll
       for (int j = 0; j < CB; ++j) {
@@ -262,7 +278,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
       __builtin_amdgcn_sched_barrier(0);  // keep the row blocks' order (hoisted fragments would spill)
     }
     if constexpr (more) {
-      wait_vmcnt<0>();
+      wait_vmcnt<copies ? C::kPw*(S - 2) : 0>();
       barrier_lds();
       first(kb + 1);
     }
@@ -270,11 +286,19 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
     for (int j = 0; j < CB; ++j) promote(RB - 1, j);
     __builtin_amdgcn_sched_barrier(0);
   };
-  for (int kb = 0; kb + 1 < KB; ++kb) {
-    if ((kb & 3) == 0 && kb + 4 < KB) scales((kb >> 2) + 1);
-    step(kb, std::true_type{});
+  int kb = kb0;
+  for (; kb + S - 1 < kb1; ++kb) {
+    if ((kb & 3) == 0 && kb + 4 * C::kAhead < kb1) scales((kb >> 2) + C::kAhead);
+    step(kb, IntC<2>{});
   }
-  step(KB - 1, std::false_type{});
+  if constexpr (S > 2) {
+    for (; kb + 1 < kb1; ++kb) {
+      if ((kb & 3) == 0 && kb + 4 * C::kAhead < kb1) scales((kb >> 2) + C::kAhead);
+      step(kb, IntC<1>{});
+    }
+  }
+  step(kb1 - 1, IntC<0>{});
+  }
 
   // The sums are whole before any lane's store is masked off: without this the compiler moves the last matrix
   // instructions, and the loads of their operands, under the stores' masks, where the other lanes' operands are stale.
@@ -282,31 +306,209 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < CB; ++j) asm volatile("" : "+v"(acc[i][j]));
-  const bool vec = a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
-                   (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
+  DenseArgs o = a;
+  if (a.splits > 1) {  // this split's sums, whole rows of 4
+    o.f32 = 1;
+    o.C = nullptr;
+    o.N = (a.N + 3) & ~3;
+    o.ldd = o.N;
+    o.D = a.ws + (int64_t)blockIdx.y * a.M * o.N;
+  }
+  const bool vec = o.ldd % 4 == 0 && ((uintptr_t)o.D & (o.f32 ? 15 : 7)) == 0 &&
+                   (!o.C || (o.ldc % 4 == 0 && ((uintptr_t)o.C & 15) == 0));
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
-    for (int j = 0; j < CB; ++j) store4(a, m0 + wm + 16 * i + l16, n0 + wn + 16 * j + 4 * lg, acc[i][j], vec);
+    for (int j = 0; j < CB; ++j) store4(o, m0 + wm + 16 * i + l16, n0 + wn + 16 * j + 4 * lg, acc[i][j], vec);
 }
 
-template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+// Split K: the splits' partial sums, added in split order, and the addend.
+__global__ __launch_bounds__(256) void gemm_dense_join_kernel(const DenseArgs a) {
+  const int np = (a.N + 3) / 4;
+  const int64_t total = (int64_t)a.M * np;
+  const bool vec = a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
+                   (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
+    v4f v = *(const v4f*)(a.ws + 4 * q);
+    for (int k = 1; k < a.splits; ++k) v += *(const v4f*)(a.ws + 4 * (q + k * total));
+    store4(a, (int)(q / np), 4 * (int)(q % np), v, vec);
+  }
+}
+
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN, int S>
 hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
-  using C = TileCfg<RB, CB, WM, WN>;
+  using C = TileCfg<RB, CB, WM, WN, S>;
   const int tiles = ((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN);
-  gemm_dense_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<(unsigned)tiles, WM * WN * 64, 0, s>>>(a);
+  gemm_dense_kernel<WIDE, GRAN1, RB, CB, WM, WN, S><<<dim3(tiles, a.splits), WM * WN * 64, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t need = ((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256, cap = (int64_t)device_info().cus * 16;
+  gemm_dense_join_kernel<<<(unsigned)(need < cap ? need : cap), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
+// Few rows (a decode step): every weight byte is used by one wave, so waves need nothing from one another.  A
+// workgroup takes 16 CB columns and all 16 RB rows; its KS waves split K into runs of groups of 4 blocks, each
+// with a ring of S blocks of its own in LDS (no barrier in the loop), and meet once at the end, where the partial
+// sums are added in wave order.  The way through LDS is for the load path: a fragment's lanes hold 16 different
+// rows, and loads in that order (4 lanes on 4 cache lines) pass a quarter of the bytes per clock that rows copied
+// whole do (64 rows x 4096 x 7168: 22 us with direct fragment loads).  Scales come like the rows, a group's 4 blocks
+// with one 16-byte copy per row.
+template <int RB, int CB, int KS, int S>
+struct StreamCfg {
+  static constexpr int kBlock = (RB + CB) * 2048, kPieces = 2 * (RB + CB);
+  static constexpr int kScRows = 16 * (RB + CB);                 // rows with scales: activations, then columns
+  static constexpr int kScCopies = (kScRows + 63) / 64, kScale = kScCopies * 1024;
+  static constexpr int kWave = S * kBlock + 2 * kScale;
+  static constexpr int kPart = 16 * RB * (16 * CB + 4) * 4;      // a wave's partial sums, over its ring
+  static constexpr int kLds = KS * kWave;
+  static_assert(kPart <= kWave && kLds <= 160 * 1024, "LDS");
+  static_assert(S >= 2 && S <= 4, "a group's scales are copied at most one group ahead");
+};
+
+template <bool WIDE, bool GRAN1, int RB, int CB, int KS, int S>
+__global__ __launch_bounds__(KS * 64) void gemm_stream_kernel(const DenseArgs a) {
+  using C = StreamCfg<RB, CB, KS, S>;
+  constexpr int kRows = 16 * RB, kCols = 16 * CB;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
+  const int lane = lane_id(), wv = uniform(threadIdx.x >> 6);
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int KB = a.K / 128, groups = (KB + 3) / 4;
+  const int n0 = blockIdx.x * kCols, m0 = blockIdx.y * kRows;
+  const int per = (groups + KS - 1) / KS;
+  const int kb0 = min(4 * wv * per, KB), nb = min(kb0 + 4 * per, KB) - kb0;
+  const bool sc_vec = KB % 4 == 0 && (((uintptr_t)a.SFA | (uintptr_t)a.SFW) & 15) == 0;
+  uint8_t* ring = sm + wv * C::kWave;
+  uint8_t* scl = ring + S * C::kBlock;
+
+  // sources of this lane's copies: piece q (1 KB) is rows 8q .. 8q + 7 of the activations, then of the columns
+  const uint8_t* src[C::kPieces];
+#pragma unroll
+  for (int q = 0; q < C::kPieces; ++q) {
+    const int row = 8 * q + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+    src[q] = 8 * q < kRows ? a.A + (int64_t)min(m0 + row, a.M - 1) * a.lda : a.W + (int64_t)min(n0 + row - kRows, a.N - 1) * a.ldw;
+    src[q] += (int64_t)kb0 * 128 + 16 * c;
+  }
+  const float* ssrc[C::kScCopies];
+#pragma unroll
+  for (int q = 0; q < C::kScCopies; ++q) {
+    const int row = min(64 * q + lane, C::kScRows - 1);
+    ssrc[q] = row < kRows ? a.SFA + (int64_t)min(m0 + row, a.M - 1) * KB
+                          : a.SFW + (int64_t)(min(n0 + row - kRows, a.N - 1) / (GRAN1 ? 1 : 128)) * KB;
+    ssrc[q] += kb0;
+  }
+  auto issue = [&](int b) {  // block b of this wave's run
+    if ((b & 3) == 0) {
+      uint8_t* dst = scl + ((b >> 2) & 1) * C::kScale;
+      // float u of row r: at 4 r + u where rows can be copied as vectors, else at 64 u + r (per 64 rows)
+#pragma unroll
+      for (int q = 0; q < C::kScCopies; ++q) {
+        if (sc_vec) {
+          dma16(ssrc[q] + b, dst + 1024 * q);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dma4(ssrc[q] + min(b + u, KB - 1 - kb0), dst + 1024 * q + 256 * u);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < C::kPieces; ++q) dma16(src[q] + (int64_t)b * 128, ring + (b % S) * C::kBlock + 1024 * q);
+  };
+
+  const int fsw = (l16 >> 1) & 7;
+  const int off_lo = l16 * 128 + 16 * (lg ^ fsw), off_hi = l16 * 128 + 16 * ((4 + lg) ^ fsw);
+  v4f acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int b = 0; b < S - 1; ++b)
+    if (b < nb) issue(b);
+  for (int b = 0; b < nb; ++b) {
+    if (b + S - 1 < nb) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot's last reads are in registers
+      issue(b + S - 1);
+      wait_vmcnt<(S - 1) * C::kPieces>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    asm volatile("" ::: "memory");  // reads below stay behind the wait
+    const uint8_t* blk = ring + (b % S) * C::kBlock;
+    const float* sc = (const float*)(scl + ((b >> 2) & 1) * C::kScale);
+    auto scale = [&](int row) { return sc_vec ? sc[4 * row + (b & 3)] : sc[(row & ~63) * 4 + 64 * (b & 3) + (row & 63)]; };
+    Frag<WIDE> x[RB];
+    float sa[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      x[i].load(*(const v4i*)(blk + 2048 * i + off_lo), *(const v4i*)(blk + 2048 * i + off_hi));
+      sa[i] = scale(16 * i + l16);
+    }
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      Frag<WIDE> w;
+      w.load(*(const v4i*)(blk + 2048 * (RB + j) + off_lo), *(const v4i*)(blk + 2048 * (RB + j) + off_hi));
+      float sw[GRAN1 ? 4 : 1];
+#pragma unroll
+      for (int e = 0; e < (GRAN1 ? 4 : 1); ++e) sw[e] = scale(kRows + 16 * j + (GRAN1 ? 4 * lg + e : 0));
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const v4f p = block_sum(w, x[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], sa[i] * sw[GRAN1 ? e : 0], acc[i][j][e]);
+      }
+    }
+  }
+  // over the wave's own ring, whose copies have all landed and been read; lane: columns 4 lg .. + 3 of row l16
+  float* part = (float*)ring;
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) *(v4f*)(part + (16 * i + l16) * (kCols + 4) + 16 * j + 4 * lg) = acc[i][j];
+  __syncthreads();
+  const bool vec = a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
+                   (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
+  for (int q = threadIdx.x; q < kRows * kCols / 4; q += KS * 64) {
+    const int m = q / (kCols / 4), n = 4 * (q % (kCols / 4));
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) v += *(const v4f*)((const float*)(sm + k * C::kWave) + m * (kCols + 4) + n);
+    store4(a, m0 + m, n0 + n, v, vec);
+  }
+}
+
+template <bool WIDE, bool GRAN1, int RB, int CB, int KS, int S>
+hipError_t launch_stream(const DenseArgs& a, hipStream_t s) {
+  const dim3 grid((a.N + 16 * CB - 1) / (16 * CB), (a.M + 16 * RB - 1) / (16 * RB));
+  gemm_stream_kernel<WIDE, GRAN1, RB, CB, KS, S><<<grid, KS * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+#ifndef V1
+#define V1 1, 1, 8, 4
+#define V2 2, 1, 8, 3
+#define V4 4, 1, 4, 3
+#define TW 4, 4, 2, 2, 2
+#define TN 8, 4, 2, 4, 2
+#define SP 1
+#define MS 64
+#endif
 template <bool WIDE, bool GRAN1>
-hipError_t launch_dense(const DenseArgs& a, hipStream_t s) {
-  if constexpr (WIDE) return launch_tile<WIDE, GRAN1, 4, 4, 2, 2>(a, s);
-  else return launch_tile<WIDE, GRAN1, 8, 4, 2, 4>(a, s);
+hipError_t launch_dense(DenseArgs a, hipStream_t s) {
+  a.splits = 1;
+  if (a.M <= 16) return launch_stream<WIDE, GRAN1, V1>(a, s);
+  if (a.M <= 32 && MS >= 32) return launch_stream<WIDE, GRAN1, V2>(a, s);
+  if (a.M <= 64 && MS >= 64) return launch_stream<WIDE, GRAN1, V4>(a, s);
+  a.splits = SP;
+  if constexpr (WIDE) return launch_tile<WIDE, GRAN1, TW>(a, s);
+  else return launch_tile<WIDE, GRAN1, TN>(a, s);
 }
 
 }  // namespace
 
-int64_t dense_workspace_bytes(int, int, int) { return 0; }
+int64_t dense_workspace_bytes(int M, int N, int K) { return SP > 1 ? 4ll * SP * M * ((N + 3) & ~3) : 0; }
 
 hipError_t launch_gemm_dense(const DenseArgs& a, hipStream_t s) {
   const bool g1 = a.gran_n == 1;

@@ -19,9 +19,12 @@
 // fp32 keys: they carry a bound es + 2^-23 |key| on their error (es: 2^-20 for
 // sigmoid scores, 2^-18 times the largest probability for softmax ones; the
 // evaluation below stays within half of that), and a row whose neighbouring
-// winners, or the groups around the last kept one, are closer than the bounds
-// allow is selected again with fp64 scores.  Without a bias the keys are the
-// logits themselves and need no such check.
+// candidates are closer than the bounds allow has its candidates (those down to the
+// first clear gap after the k-th) ordered by fp64 keys, one per lane; a row whose
+// groups around the last kept one are that close, or with more than 64
+// candidates, is selected again with fp64 keys throughout.  (Selecting every close row again cost 6 us, the whole kernel's
+// tail, with about 12 such rows in 4096.)  Without a bias the keys are the logits themselves
+// and need no check.
 //
 // A logit of -inf or NaN marks an expert that this token may not use; slots
 // left over get id -1 and weight 0, which moe_route_pack skips.
@@ -70,10 +73,20 @@ __device__ __forceinline__ int wave_max_i32(int v) {
 }
 __device__ __forceinline__ float wave_max_f32(float v) { return unordered(wave_max_i32(ordered(v))); }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float old, float v) {
+  return __int_as_float(dpp<CTRL>(__float_as_int(old), __float_as_int(v)));
+}
+
+// Sum over the wave, in every lane.
 __device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  v += dpp_f32<0xB1>(v, v);
+  v += dpp_f32<0x4E>(v, v);
+  v += dpp_f32<0x141>(v, v);
+  v += dpp_f32<0x140>(v, v);
+  v += dpp_f32<0x142>(0.0f, v);
+  v += dpp_f32<0x143>(0.0f, v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
@@ -121,45 +134,81 @@ struct Pick {
   float x;  // and its logit
 };
 
-// Two largest of the group's keys, in all its lanes.
-template <typename F>
-__device__ __forceinline__ void group_top2(F& a1, F& a2, int lpg) {
+// Two largest of the group's keys, in all its lanes: pairs, quads, 8 and 16 lanes meet inside the VALU (a mirror
+// reaches the other half where each half is uniform), wider groups through the lane crossbar.
+__device__ __forceinline__ void meet_top2(float& a1, float& a2, float b1, float b2) {
+  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+  a1 = fmaxf(a1, b1);
+}
+__device__ __forceinline__ void group_top2(float& a1, float& a2, int lpg) {
+  if (lpg > 1) meet_top2(a1, a2, dpp_f32<0xB1>(a1, a1), dpp_f32<0xB1>(a2, a2));
+  if (lpg > 2) meet_top2(a1, a2, dpp_f32<0x4E>(a1, a1), dpp_f32<0x4E>(a2, a2));
+  if (lpg > 4) meet_top2(a1, a2, dpp_f32<0x141>(a1, a1), dpp_f32<0x141>(a2, a2));
+  if (lpg > 8) meet_top2(a1, a2, dpp_f32<0x140>(a1, a1), dpp_f32<0x140>(a2, a2));
+  if (lpg > 16) meet_top2(a1, a2, __shfl_xor(a1, 16, 64), __shfl_xor(a2, 16, 64));
+}
+__device__ __forceinline__ void group_top2(double& a1, double& a2, int lpg) {
   for (int off = 1; off < lpg; off <<= 1) {
-    const F b1 = __shfl_xor(a1, off, 64), b2 = __shfl_xor(a2, off, 64);
-    const F lo = a1 < b1 ? a1 : b1;
-    const F m2 = a2 > b2 ? a2 : b2;
+    const double b1 = __shfl_xor(a1, off, 64), b2 = __shfl_xor(a2, off, 64);
+    const double lo = a1 < b1 ? a1 : b1;
+    const double m2 = a2 > b2 ? a2 : b2;
     a1 = a1 > b1 ? a1 : b1;
     a2 = lo > m2 ? lo : m2;
   }
 }
 
-// The choice in 64 bits (every lane of the wave calls it).
+// Largest logit and the sum of exponentials of the row, in 64 bits (softmax).
+template <int VPL>
+__device__ __forceinline__ void softmax_f64(const float (&x)[VPL], double& m, double& den) {
+  float mf = -__builtin_huge_valf();
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) mf = fmaxf(mf, x[j]);
+  m = (double)wave_max_f32(mf);
+  double s = 0.0;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    if (x[j] > -__builtin_huge_valf()) s += (double)x[j] == m ? 1.0 : exp((double)x[j] - m);
+  den = wave_sum_f64(s);
+}
+__device__ __forceinline__ double score_f64(int score, double x, double m, double den) {
+  return score == 0 ? (x == m ? 1.0 : exp(x - m)) / den : 1.0 / (1.0 + exp(-x));
+}
+
+// Order in 64 bits of the candidates in lanes 0 .. c - 1 (one expert each, none outside them can be among the best k):
+// each counts those ahead of it and moves to that lane.
+template <int VPL>
+__device__ __forceinline__ Pick order_f64(const RouterArgs& a, const float (&x)[VPL], Pick p, int c, int lane) {
+  double m = 0.0, den = 1.0;
+  if (a.score == 0) softmax_f64(x, m, den);
+  const double key = lane < c ? score_f64(a.score, (double)p.x, m, den) + (double)a.bias[p.id] : 0.0;
+  int ahead = 0;
+  for (int j = 0; j < c; ++j) {
+    const int lo = __builtin_amdgcn_readlane((int)(__double_as_longlong(key)), j);
+    const int hi = __builtin_amdgcn_readlane((int)(__double_as_longlong(key) >> 32), j);
+    const double kj = __longlong_as_double(((long long)hi << 32) | (uint32_t)lo);
+    const int ij = __builtin_amdgcn_readlane(p.id, j);
+    ahead += kj > key || (kj == key && ij < p.id);
+  }
+  const int to = 4 * (lane < c ? ahead : lane);
+  Pick o;
+  o.id = __builtin_amdgcn_ds_permute(to, p.id);
+  o.x = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(p.x)));
+  if (lane >= a.k) o.id = -1;
+  return o;
+}
+
+// The whole choice in 64 bits (every lane of the wave calls it).
 template <int VPL>
 __device__ __forceinline__ Pick select_f64(const RouterArgs& a, const float (&x)[VPL], const float (&b)[VPL],
                                            const LaneExperts& le, int lane) {
   const double ninf = -__builtin_huge_val();
   double key[VPL];
   double den = 1.0, m = 0.0;
-  if (a.score == 0) {
-    float mf = -__builtin_huge_valf();
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) mf = fmaxf(mf, x[j]);
-    m = (double)wave_max_f32(mf);
-    double s = 0.0;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (x[j] > -__builtin_huge_valf()) s += (double)x[j] == m ? 1.0 : exp((double)x[j] - m);
-    den = wave_sum_f64(s);
-  }
+  if (a.score == 0) softmax_f64(x, m, den);
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const double xd = (double)x[j];
-    double s;
-    if (a.score == 0)
-      s = (xd == m ? 1.0 : exp(xd - m)) / den;
-    else
-      s = 1.0 / (1.0 + exp(-xd));
-    key[j] = a.bias ? s + (double)b[j] : s;
+    const double sc = score_f64(a.score, (double)x[j], m, den);
+    key[j] = a.bias ? sc + (double)b[j] : sc;
     if (!(x[j] > -__builtin_huge_valf()) || !(key[j] > ninf)) key[j] = ninf;
   }
   bool kept = true;
@@ -337,10 +386,12 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
         const float v = a.bias ? key[j] : x[j];
         ik[j] = kept && key[j] > ninf ? ordered(v) : kNone;
       }
-      const int rounds = a.bias ? a.k + 1 : a.k;  // with a bias, the best loser has to be clearly below too
+      // With a bias, extraction goes on until the next key is clearly below (r counts the candidates by then); where
+      // two of them were too close, their order is settled in 64 bits.
       float prev = 0.0f;
       bool close = false;
-      for (int r = 0; r < rounds; ++r) {
+      int r = 0;
+      for (;; ++r) {
         int best = ik[0];
 #pragma unroll
         for (int j = 1; j < VPL; ++j) best = max(best, ik[j]);
@@ -348,12 +399,17 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
         if (mk == kNone) break;
         if (a.bias) {
           const float v = unordered(mk);
-          if (r > 0 && !(prev - v > 2.0f * es + 0x1p-23f * (fabsf(prev) + fabsf(v)))) {
+          if (r > 0 && !(prev - v > 2.0f * es + 0x1p-23f * (fabsf(prev) + fabsf(v))))
             close = true;
+          else if (r >= a.k)
+            break;
+          if (r == 64) {
+            unsure = true;
             break;
           }
           prev = v;
-          if (r == a.k) break;
+        } else if (r == a.k) {
+          break;
         }
         const int wl = __builtin_ctzll(__ballot(best == mk));
         int e = -1;
@@ -372,7 +428,7 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
           p.x = xw;
         }
       }
-      unsure = close;
+      if (close && !unsure) p = order_f64(a, x, p, r, lane);
     }
     if (__any(unsure)) p = select_f64<VPL>(a, x, b, le, lane);
 
