@@ -11,8 +11,8 @@
 //
 // moe_unpermute_combine_bwd: its gradient, dY[output_index[t,r]] = p[t,r] * dZ[t]
 // and dp[t,r] = <dZ[t], Y[output_index[t,r]]>.
-// One workgroup per token: the token's dZ row is read once per batch of 8
-// slots, every named row of Y is streamed once and its gradient row written
+// One workgroup per token and batch of slots: the token's dZ row is read once per
+// batch, every named row of Y is streamed once and its gradient row written
 // once (nontemporal).  HBM-bound.
 // A row is normally named by one slot (moe_route_pack gives every route a row
 // of its own).  A row named by several slots gets the sum over them in route
@@ -132,11 +132,11 @@ __device__ inline void shared_row(const CombineBwdArgs& a, int p, int64_t own, i
   }
 }
 
-// NT threads per token: 256 where there are tokens enough to fill the chip, else 1024, so that a row (up to 8192
-// columns) is in flight at once (61 tokens x 8 slots x 7168 columns: XX).
-template <int NT>
+// NT threads per B slots of a token: 256 and 8 where there are tokens enough to fill the chip, so that dZ is read once;
+// else 1024 and 2, so that a row (up to 8192 columns) is in flight at once and the slots spread over more compute
+// units.
+template <int NT, int B>
 __global__ __launch_bounds__(NT) void combine_bwd_kernel(const CombineBwdArgs a) {
-  constexpr int B = 8;  // slots per batch
   constexpr int kScan = (kRouteSmallMax + NT - 1) / NT;
   __shared__ int s_cnt[B], s_own[B];
   __shared__ float s_sum[NT / 64][B];
@@ -144,111 +144,111 @@ __global__ __launch_bounds__(NT) void combine_bwd_kernel(const CombineBwdArgs a)
   const int chunks = a.N / 8;
   const int R = a.T * a.k;
   const bool scan = a.dY && !a.who;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    for (int r0 = 0; r0 < a.k; r0 += B) {
-      const int i0 = t * a.k + r0;
-      int p[B];
-      float w[B];
+  const int batches = (a.k + B - 1) / B;
+  const int64_t total = (int64_t)a.T * batches;
+  for (int64_t q = blockIdx.x; q < total; q += gridDim.x) {
+    const int t = (int)(q / batches), r0 = (int)(q % batches) * B, i0 = t * a.k + r0;
+    int p[B];
+    float w[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      p[j] = r0 + j < a.k ? a.oi[i0 + j] : -1;
+      if (p[j] >= a.y_rows) p[j] = -1;
+      w[j] = r0 + j < a.k && a.dY ? a.w[i0 + j] : 0.0f;
+    }
+    int o[kScan];  // this thread's share of output_index: loaded with the batch's own, compared below
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) o[u] = scan && tid + NT * u < R ? a.oi[tid + NT * u] : -1;
+    bool write[B], shared = false;
+#pragma unroll
+    for (int j = 0; j < B; ++j) write[j] = a.dY && p[j] >= 0;
+    if (a.dY && a.who) {
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (p[j] >= 0 && a.who[p[j]].x != 1) {
+          write[j] = false;
+          shared = true;
+        }
+    }
+    float dot[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) dot[j] = 0.0f;
+    v4i dzv = {0, 0, 0, 0}, y[B];
+    auto load = [&](int c) {
+      dzv = *(const v4i*)(a.dZ + (int64_t)t * a.N + 8 * c);
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        y[j] = a.dw && p[j] >= 0 ? __builtin_nontemporal_load((const v4i*)(a.Y + (int64_t)p[j] * a.N + 8 * c))
+                                 : v4i{0, 0, 0, 0};
+    };
+    if (tid < chunks) load(tid);
+    if (scan) {  // behind the first rows' loads
+      if (tid < B) {
+        s_cnt[tid] = 0;
+        s_own[tid] = 0x7fffffff;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kScan; ++u)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+          if (o[u] >= 0 && o[u] == p[j]) {
+            atomicAdd(&s_cnt[j], 1);
+            atomicMin(&s_own[j], tid + NT * u);
+          }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (p[j] >= 0 && s_cnt[j] != 1) {
+          write[j] = false;
+          shared = true;
+        }
+    }
+    for (int c = tid; c < chunks; c += NT) {
+      if (c != tid) load(c);
+      float dz[8];
+      unpack8(dzv, dz);
 #pragma unroll
       for (int j = 0; j < B; ++j) {
-        p[j] = r0 + j < a.k ? a.oi[i0 + j] : -1;
-        if (p[j] >= a.y_rows) p[j] = -1;
-        w[j] = r0 + j < a.k && a.dY ? a.w[i0 + j] : 0.0f;
+        float f[8];
+        unpack8(y[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(f[i], dz[i], dot[j]);
       }
-      int o[kScan];  // this thread's share of output_index: loaded with the batch's own, compared below
 #pragma unroll
-      for (int u = 0; u < kScan; ++u) o[u] = scan && tid + NT * u < R ? a.oi[tid + NT * u] : -1;
-      bool write[B], shared = false;
+      for (int j = 0; j < B; ++j) {
+        if (!write[j]) continue;
+        float v[8];
 #pragma unroll
-      for (int j = 0; j < B; ++j) write[j] = a.dY && p[j] >= 0;
-      if (a.dY && a.who) {
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (p[j] >= 0 && a.who[p[j]].x != 1) {
-            write[j] = false;
-            shared = true;
-          }
+        for (int i = 0; i < 8; ++i) v[i] = w[j] * dz[i];
+        __builtin_nontemporal_store(pack8(v), (v4i*)(a.dY + (int64_t)p[j] * a.N + 8 * c));
       }
-      float dot[B];
-#pragma unroll
-      for (int j = 0; j < B; ++j) dot[j] = 0.0f;
-      v4i dzv = {0, 0, 0, 0}, y[B];
-      auto load = [&](int c) {
-        dzv = *(const v4i*)(a.dZ + (int64_t)t * a.N + 8 * c);
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          y[j] = a.dw && p[j] >= 0 ? __builtin_nontemporal_load((const v4i*)(a.Y + (int64_t)p[j] * a.N + 8 * c))
-                                   : v4i{0, 0, 0, 0};
-      };
-      if (tid < chunks) load(tid);
-      if (scan) {  // behind the first rows' loads
-        if (tid < B) {
-          s_cnt[tid] = 0;
-          s_own[tid] = 0x7fffffff;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kScan; ++u)
-#pragma unroll
-          for (int j = 0; j < B; ++j)
-            if (o[u] >= 0 && o[u] == p[j]) {
-              atomicAdd(&s_cnt[j], 1);
-              atomicMin(&s_own[j], tid + NT * u);
-            }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (p[j] >= 0 && s_cnt[j] != 1) {
-            write[j] = false;
-            shared = true;
-          }
-      }
-      for (int c = tid; c < chunks; c += NT) {
-        if (c != tid) load(c);
-        float dz[8];
-        unpack8(dzv, dz);
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-          float f[8];
-          unpack8(y[j], f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(f[i], dz[i], dot[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-          if (!write[j]) continue;
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = w[j] * dz[i];
-          __builtin_nontemporal_store(pack8(v), (v4i*)(a.dY + (int64_t)p[j] * a.N + 8 * c));
-        }
-      }
-      if (shared) {
-        for (int j = 0; j < B; ++j) {
-          const int pj = r0 + j < a.k ? a.oi[i0 + j] : -1;
-          if (pj < 0 || pj >= a.y_rows) continue;
-          const int cnt = a.who ? a.who[pj].x : s_cnt[j];
-          const int own = a.who ? a.who[pj].y : s_own[j];
-          if (cnt > 1 && own == i0 + j) shared_row(a, pj, own, cnt);
-        }
-      }
-      if (a.dw) {
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-#pragma unroll
-          for (int off = 32; off; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
-          if (lane == 0) s_sum[wv][j] = dot[j];
-        }
-        __syncthreads();
-        if (tid < B && r0 + tid < a.k) {
-          float s = 0.0f;
-#pragma unroll
-          for (int v = 0; v < NT / 64; ++v) s += s_sum[v][tid];
-          a.dw[i0 + tid] = s;
-        }
-      }
-      __syncthreads();  // s_cnt, s_own and s_sum are reused
     }
+    if (shared) {
+      for (int j = 0; j < B; ++j) {
+        const int pj = r0 + j < a.k ? a.oi[i0 + j] : -1;
+        if (pj < 0 || pj >= a.y_rows) continue;
+        const int cnt = a.who ? a.who[pj].x : s_cnt[j];
+        const int own = a.who ? a.who[pj].y : s_own[j];
+        if (cnt > 1 && own == i0 + j) shared_row(a, pj, own, cnt);
+      }
+    }
+    if (a.dw) {
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+#pragma unroll
+        for (int off = 32; off; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
+        if (lane == 0) s_sum[wv][j] = dot[j];
+      }
+      __syncthreads();
+      if (tid < B && r0 + tid < a.k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NT / 64; ++v) s += s_sum[v][tid];
+        a.dw[i0 + tid] = s;
+      }
+    }
+    __syncthreads();  // s_cnt, s_own and s_sum are reused
   }
 }
 
@@ -266,10 +266,12 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.T < 2 * device_info().cus)
-    combine_bwd_kernel<1024><<<(unsigned)a.T, 1024, 0, s>>>(a);
-  else
-    combine_bwd_kernel<256><<<(unsigned)(a.T < cap ? a.T : cap), 256, 0, s>>>(a);
+  if (a.T < 2 * device_info().cus) {
+    combine_bwd_kernel<1024, 2><<<(unsigned)((int64_t)a.T * ((a.k + 1) / 2)), 1024, 0, s>>>(a);
+  } else {
+    const int64_t total = (int64_t)a.T * ((a.k + 7) / 8);
+    combine_bwd_kernel<256, 8><<<(unsigned)(total < cap ? total : cap), 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

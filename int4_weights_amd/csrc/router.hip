@@ -21,10 +21,11 @@
 // evaluation below stays within half of that), and a row whose neighbouring
 // candidates are closer than the bounds allow has its candidates (those down to the
 // first clear gap after the k-th) ordered by fp64 keys, one per lane; a row whose
-// groups around the last kept one are that close, or with more than 64
-// candidates, is selected again with fp64 keys throughout.  (Selecting every close row again cost 6 us, the whole kernel's
-// tail, with about 12 such rows in 4096.)  Without a bias the keys are the logits themselves
-// and need no check.
+// groups around the last kept one are that close has its group scores summed in
+// fp64; only a row with more than 64 close candidates is selected again
+// with fp64 keys throughout.  (A whole second selection for every such row cost 6 to 14 us, the
+// kernel's tail, with about 12 of them in 4096.)  Without a bias the keys are the logits
+// themselves and need no check.
 //
 // A logit of -inf or NaN marks an expert that this token may not use; slots
 // left over get id -1 and weight 0, which moe_route_pack skips.
@@ -112,6 +113,80 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A lane's candidates in descending order: keys, and their positions j packed 4 bits each (first candidate lowest).
+// Equal keys keep the lower position first (the comparison is of (key, -j) as one 64-bit integer).  Popping the lane's
+// best is then a shift, and no round of the selection searches the lane again (8 rounds over 256 experts: 55
+// instructions a round with the search, 28 with the shift).
+template <int VPL>
+struct Sorted {
+  int key[VPL];
+  uint32_t pos;
+  static __device__ __forceinline__ void order(int64_t& a, int64_t& b) {
+    const int64_t hi = a > b ? a : b, lo = a > b ? b : a;
+    a = hi;
+    b = lo;
+  }
+  __device__ __forceinline__ void sort(const int (&ik)[VPL]) {
+    static_assert(VPL == 1 || VPL == 2 || VPL == 4 || VPL == 8, "sorting networks below");
+    int64_t v[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) v[j] = (int64_t)((uint64_t)(uint32_t)ik[j] << 32 | (uint32_t)(VPL - 1 - j));
+    // odd-even merge sort
+#pragma unroll
+    for (int p = 1; p < VPL; p *= 2)
+#pragma unroll
+      for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+        for (int j = q % p; j + q < VPL; j += 2 * q)
+#pragma unroll
+          for (int i = 0; i < q; ++i)
+            if (i + j + q < VPL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order(v[i + j], v[i + j + q]);
+    pos = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      key[j] = (int)(v[j] >> 32);
+      pos |= (VPL - 1 - (uint32_t)v[j]) << (4 * j);
+    }
+  }
+  __device__ __forceinline__ int best() const { return key[0]; }
+  __device__ __forceinline__ int best_pos(int) const { return (int)(pos & 15); }
+  __device__ __forceinline__ void pop(int) {
+#pragma unroll
+    for (int j = 0; j + 1 < VPL; ++j) key[j] = key[j + 1];
+    key[VPL - 1] = kNone;
+    pos >>= 4;
+  }
+};
+// More candidates per lane than are worth sorting: searched again in every round.
+template <int VPL>
+struct Unsorted {
+  int key[VPL];
+  __device__ __forceinline__ void sort(const int (&ik)[VPL]) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = ik[j];
+  }
+  __device__ __forceinline__ int best() const {
+    int b = key[0];
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) b = max(b, key[j]);
+    return b;
+  }
+  __device__ __forceinline__ int best_pos(int mk) const {
+    int p = 0;
+#pragma unroll
+    for (int j = VPL - 1; j >= 0; --j) p = key[j] == mk ? j : p;
+    return p;
+  }
+  __device__ __forceinline__ void pop(int p) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = j == p ? kNone : key[j];
+  }
+};
+template <int VPL, bool SMALL>
+struct Cands : Sorted<VPL> {};
+template <int VPL>
+struct Cands<VPL, false> : Unsorted<VPL> {};
+
 // Where this lane's experts are: expert base + j for j < n.
 struct LaneExperts {
   int base, n, lpg;  // lpg: lanes per group
@@ -147,39 +222,44 @@ __device__ __forceinline__ void group_top2(float& a1, float& a2, int lpg) {
   if (lpg > 8) meet_top2(a1, a2, dpp_f32<0x140>(a1, a1), dpp_f32<0x140>(a2, a2));
   if (lpg > 16) meet_top2(a1, a2, __shfl_xor(a1, 16, 64), __shfl_xor(a2, 16, 64));
 }
-__device__ __forceinline__ void group_top2(double& a1, double& a2, int lpg) {
-  for (int off = 1; off < lpg; off <<= 1) {
-    const double b1 = __shfl_xor(a1, off, 64), b2 = __shfl_xor(a2, off, 64);
-    const double lo = a1 < b1 ? a1 : b1;
-    const double m2 = a2 > b2 ? a2 : b2;
-    a1 = a1 > b1 ? a1 : b1;
-    a2 = lo > m2 ? lo : m2;
-  }
+
+// What follows in 64 bits is for a few rows in a thousand: it reads the row again, one expert per lane and turn, and
+// keeps its keys in LDS, so that it costs the other rows no registers (inlined with its keys in registers the kernel
+// held 108 of them and 4 waves a SIMD).
+
+template <typename T>
+__device__ __forceinline__ float logit_or_none(const T* row, int e) {
+  const float x = load_logit(row + e);
+  return x > -__builtin_huge_valf() ? x : -__builtin_huge_valf();
 }
 
-// Largest logit and the sum of exponentials of the row, in 64 bits (softmax).
-template <int VPL>
-__device__ __forceinline__ void softmax_f64(const float (&x)[VPL], double& m, double& den) {
+// Largest logit and the sum of exponentials of the row (softmax).
+template <typename T>
+__device__ __forceinline__ void softmax_f64(const T* row, int E, int lane, double& m, double& den) {
   float mf = -__builtin_huge_valf();
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) mf = fmaxf(mf, x[j]);
-  m = (double)wave_max_f32(mf);
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) mf = fmaxf(mf, logit_or_none(row, e));
+  mf = wave_max_f32(mf);
+  m = (double)mf;
   double s = 0.0;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j)
-    if (x[j] > -__builtin_huge_valf()) s += (double)x[j] == m ? 1.0 : exp((double)x[j] - m);
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    const float x = logit_or_none(row, e);
+    if (x > -__builtin_huge_valf()) s += x == mf ? 1.0 : exp((double)x - m);
+  }
   den = wave_sum_f64(s);
 }
 __device__ __forceinline__ double score_f64(int score, double x, double m, double den) {
-  return score == 0 ? (x == m ? 1.0 : exp(x - m)) / den : 1.0 / (1.0 + exp(-x));
+  const double t = exp(score == 0 ? x - m : -x);
+  return score == 0 ? (x == m ? 1.0 : t) / den : 1.0 / (1.0 + t);
 }
 
 // Order in 64 bits of the candidates in lanes 0 .. c - 1 (one expert each, none outside them can be among the best k):
 // each counts those ahead of it and moves to that lane.
-template <int VPL>
-__device__ __forceinline__ Pick order_f64(const RouterArgs& a, const float (&x)[VPL], Pick p, int c, int lane) {
+template <typename T>
+__device__ __forceinline__ Pick order_f64(const RouterArgs& a, const T* row, Pick p, int c, int lane) {
   double m = 0.0, den = 1.0;
-  if (a.score == 0) softmax_f64(x, m, den);
+  if (a.score == 0) softmax_f64(row, a.E, lane, m, den);
   const double key = lane < c ? score_f64(a.score, (double)p.x, m, den) + (double)a.bias[p.id] : 0.0;
   int ahead = 0;
   for (int j = 0; j < c; ++j) {
@@ -197,76 +277,113 @@ __device__ __forceinline__ Pick order_f64(const RouterArgs& a, const float (&x)[
   return o;
 }
 
-// The whole choice in 64 bits (every lane of the wave calls it).
-template <int VPL>
-__device__ __forceinline__ Pick select_f64(const RouterArgs& a, const float (&x)[VPL], const float (&b)[VPL],
-                                           const LaneExperts& le, int lane) {
+// Whether this lane's expert group is among the kept ones, by group scores in 64 bits.
+template <typename T>
+__device__ __forceinline__ bool group_kept_f64(const RouterArgs& a, const T* row, const LaneExperts& le, int lane) {
   const double ninf = -__builtin_huge_val();
-  double key[VPL];
+  double den = 1.0, m = 0.0, a1 = ninf, a2 = ninf;
+  if (a.score == 0) softmax_f64(row, a.E, lane, m, den);
+#pragma unroll 1
+  for (int j = 0; j < le.n; ++j) {
+    const float x = logit_or_none(row, le.base + j);
+    double v = score_f64(a.score, (double)x, m, den);
+    if (a.bias) v += (double)a.bias[le.base + j];
+    v = x > -__builtin_huge_valf() && v > ninf ? v : ninf;
+    const double lo = v < a1 ? v : a1;
+    a1 = v > a1 ? v : a1;
+    a2 = lo > a2 ? lo : a2;
+  }
+#pragma unroll 1
+  for (int off = 1; off < le.lpg; off <<= 1) {
+    const double b1 = __shfl_xor(a1, off, 64), b2 = __shfl_xor(a2, off, 64);
+    const double lo = a1 < b1 ? a1 : b1, m2 = a2 > b2 ? a2 : b2;
+    a1 = a1 > b1 ? a1 : b1;
+    a2 = lo > m2 ? lo : m2;
+  }
+  const double gs = a.gtop == 1 || !(a2 > ninf) ? a1 : a1 + a2;
+  const int g = lane / le.lpg;
+  int better = 0;
+#pragma unroll 1
+  for (int o = 0; o < a.G; ++o) {
+    const double go = __shfl(gs, o * le.lpg, 64);
+    better += go > gs || (go == gs && o < g);
+  }
+  return better < a.TG;
+}
+
+__device__ __forceinline__ double wave_max_f64(double v) {
+#pragma unroll 1
+  for (int off = 1; off < 64; off <<= 1) {
+    const double o = __shfl_xor(v, off, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// The whole choice in 64 bits, with a bias (every lane of the wave calls it): lane l holds experts l, l + 64, ... in
+// key[] (LDS).
+template <typename T>
+__device__ __forceinline__ Pick select_f64(const RouterArgs& a, const T* row, double* key, int lane) {
+  const double ninf = -__builtin_huge_val();
   double den = 1.0, m = 0.0;
-  if (a.score == 0) softmax_f64(x, m, den);
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const double sc = score_f64(a.score, (double)x[j], m, den);
-    key[j] = a.bias ? sc + (double)b[j] : sc;
-    if (!(x[j] > -__builtin_huge_valf()) || !(key[j] > ninf)) key[j] = ninf;
+  if (a.score == 0) softmax_f64(row, a.E, lane, m, den);
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    const float x = logit_or_none(row, e);
+    double v = score_f64(a.score, (double)x, m, den);
+    v += (double)a.bias[e];
+    key[e] = x > -__builtin_huge_valf() && v > ninf ? v : ninf;
   }
-  bool kept = true;
+  wave_fence();
   if (a.G > 1) {
+    // lane g: group g (at most 64)
+    const int S = a.E / a.G;
     double a1 = ninf, a2 = ninf;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      // by logit where there is no bias and only the largest counts: the order of the scores
-      const double v = !a.bias && a.gtop == 1 ? (key[j] > ninf ? (double)x[j] : ninf) : key[j];
-      const double lo = v < a1 ? v : a1;
-      a1 = v > a1 ? v : a1;
-      a2 = lo > a2 ? lo : a2;
+    if (lane < a.G) {
+#pragma unroll 1
+      for (int e = lane * S; e < (lane + 1) * S; ++e) {
+        const double v = key[e];
+        const double lo = v < a1 ? v : a1;
+        a1 = v > a1 ? v : a1;
+        a2 = lo > a2 ? lo : a2;
+      }
     }
-    group_top2(a1, a2, le.lpg);
     const double gs = a.gtop == 1 || !(a2 > ninf) ? a1 : a1 + a2;
-    const int g = lane / le.lpg;
     int better = 0;
+#pragma unroll 1
     for (int o = 0; o < a.G; ++o) {
-      const double go = __shfl(gs, o * le.lpg, 64);
-      better += go > gs || (go == gs && o < g);
+      const double go = __shfl(gs, o, 64);
+      better += go > gs || (go == gs && o < lane);
     }
-    kept = better < a.TG;
-  }
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    if (!a.bias) key[j] = key[j] > ninf ? (double)x[j] : ninf;
-    if (!kept) key[j] = ninf;
+    const uint64_t kept = __ballot(lane < a.G && better < a.TG);
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64)
+      if (!(kept >> (e / S) & 1)) key[e] = ninf;
   }
   Pick p{-1, 0.0f};
+#pragma unroll 1
   for (int r = 0; r < a.k; ++r) {
     double best = ninf;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) best = key[j] > best ? key[j] : best;
-    double m2 = best;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double o = __shfl_xor(m2, off, 64);
-      m2 = o > m2 ? o : m2;
-    }
-    if (!(m2 > ninf)) break;
-    const uint64_t who = __ballot(best == m2);
-    const int wl = __builtin_ctzll(who);
-    int e = -1;
-    float xs = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (e < 0 && key[j] == m2) {
-        e = le.base + j;
-        xs = x[j];
-        if (lane == wl) key[j] = ninf;
+    int be = a.E;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      if (key[e] > best) {
+        best = key[e];
+        be = e;
       }
-    const int ew = __builtin_amdgcn_readlane(e, wl);
-    const float xw = readlane_f32(xs, wl);
+    }
+    const double mk = wave_max_f64(best);
+    if (!(mk > ninf)) break;
+    int we = best == mk ? be : a.E;  // the lowest expert of the lanes that hold the largest key
+#pragma unroll 1
+    for (int off = 1; off < 64; off <<= 1) we = min(we, __shfl_xor(we, off, 64));
+    if (we == be && best == mk) key[we] = ninf;
     if (lane == r) {
-      p.id = ew;
-      p.x = xw;
+      p.id = we;
+      p.x = load_logit(row + we);
     }
   }
+  wave_fence();  // key[] is rewritten by the next row
   return p;
 }
 
@@ -294,22 +411,27 @@ __device__ __forceinline__ float slot_weight(int score, int norm, float scale, b
 
 }  // namespace
 
-template <typename T, int VPL>
+// BIAS and GROUPS (a.bias, a.G > 1) are compiled apart: a scalar branch per round costs as much as the round's work.
+template <typename T, int VPL, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
+  __shared__ double s_key[4][BIAS ? 64 * (VPL < 16 ? VPL : 16) : 1];  // E <= 1024
   const int lane = lane_id();
   const float ninf = -__builtin_huge_valf();
-  const LaneExperts le = lane_experts(a.E, a.G, lane);
-  const bool by_score = a.bias || (a.G > 1 && a.gtop == 2);
+  const LaneExperts le = lane_experts(a.E, GROUPS ? a.G : 1, lane);
+  const bool by_score = BIAS || (GROUPS && a.gtop == 2);
+  float b[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    b[j] = 0.0f;
+    if constexpr (BIAS) b[j] = a.bias[min(le.base + j, a.E - 1)];
+  }
   for (int t = blockIdx.x * 4 + uniform(threadIdx.x >> 6); t < a.T; t += gridDim.x * 4) {
-    const T* row = (const T*)a.logits + (int64_t)t * a.ld + le.base;
-    float x[VPL], b[VPL];
+    const T* row = (const T*)a.logits + (int64_t)t * a.ld;
+    float x[VPL];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      x[j] = j < le.n ? load_logit(row + j) : ninf;
-      b[j] = a.bias && j < le.n ? a.bias[le.base + j] : 0.0f;
-    }
+    for (int j = 0; j < VPL; ++j) x[j] = load_logit(row + min(le.base + j, a.E - 1));
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) x[j] = x[j] > ninf ? x[j] : ninf;  // NaN is -inf
+    for (int j = 0; j < VPL; ++j) x[j] = j < le.n && x[j] > ninf ? x[j] : ninf;  // NaN is -inf
 
     float row_m = 0.0f, row_den = 1.0f, ex[VPL];
     if (a.score == 0 && (by_score || !a.norm)) {
@@ -343,8 +465,8 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
       for (int j = 0; j < VPL; ++j) key[j] = x[j];
     }
 
-    bool unsure = false, kept = true;
-    if (a.G > 1) {
+    bool kept = true;
+    if constexpr (GROUPS) {
       float a1 = ninf, a2 = ninf;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
@@ -366,7 +488,7 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
           maybe += !(readlane_f32(hi, o * le.lpg) < lo);
         }
         kept = above < a.TG;
-        unsure = kept && maybe >= a.TG && gs > ninf;
+        if (__any(kept && maybe >= a.TG && gs > ninf)) kept = group_kept_f64(a, row, le, lane);
       } else {
         int better = 0;
         for (int o = 0; o < a.G; ++o) {
@@ -378,26 +500,27 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
     }
 
     Pick p{-1, 0.0f};
-    if (!__any(unsure)) {
+    bool unsure = false;  // more close candidates than lanes
+    {
       int ik[VPL];
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
         // without a bias the experts' order is the logits'
-        const float v = a.bias ? key[j] : x[j];
+        const float v = BIAS ? key[j] : x[j];
         ik[j] = kept && key[j] > ninf ? ordered(v) : kNone;
       }
       // With a bias, extraction goes on until the next key is clearly below (r counts the candidates by then); where
       // two of them were too close, their order is settled in 64 bits.
+      Cands<VPL, (VPL <= 8)> cand;
+      cand.sort(ik);
       float prev = 0.0f;
       bool close = false;
       int r = 0;
       for (;; ++r) {
-        int best = ik[0];
-#pragma unroll
-        for (int j = 1; j < VPL; ++j) best = max(best, ik[j]);
+        const int best = cand.best();
         const int mk = wave_max_i32(best);
         if (mk == kNone) break;
-        if (a.bias) {
+        if constexpr (BIAS) {
           const float v = unordered(mk);
           if (r > 0 && !(prev - v > 2.0f * es + 0x1p-23f * (fabsf(prev) + fabsf(v))))
             close = true;
@@ -412,25 +535,20 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
           break;
         }
         const int wl = __builtin_ctzll(__ballot(best == mk));
-        int e = -1;
-        float xs = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j)
-          if (e < 0 && ik[j] == mk) {
-            e = le.base + j;
-            xs = x[j];
-            if (lane == wl) ik[j] = kNone;
-          }
-        const int ew = __builtin_amdgcn_readlane(e, wl);
-        const float xw = readlane_f32(xs, wl);
+        const int pos = cand.best_pos(mk);
+        const int ew = __builtin_amdgcn_readlane(le.base + pos, wl);
+        if (lane == wl) cand.pop(pos);
         if (lane == r) {
           p.id = ew;
-          p.x = xw;
+          p.x = unordered(mk);
         }
       }
-      if (close && !unsure) p = order_f64(a, x, p, r, lane);
+      if (BIAS && lane < r) p.x = load_logit(row + p.id);  // the key is not the logit
+      if constexpr (BIAS)
+        if (close && !unsure) p = order_f64(a, row, p, r, lane);
     }
-    if (__any(unsure)) p = select_f64<VPL>(a, x, b, le, lane);
+    if constexpr (BIAS)
+      if (unsure) p = select_f64(a, row, s_key[threadIdx.x >> 6], lane);
 
     const bool on = p.id >= 0;
     const float w = slot_weight(a.score, a.norm, a.scale, on, p.x, row_m, row_den);
@@ -540,15 +658,22 @@ int row_grid(int T) {
   return (int)(need < cap ? need : cap);
 }
 
+template <typename T, int VPL>
+void launch_topk_vpl(const RouterArgs& a, hipStream_t s) {
+  const int g = row_grid(a.T);
+  if (a.bias && a.G > 1) router_topk_kernel<T, VPL, true, true><<<g, 256, 0, s>>>(a);
+  else if (a.bias) router_topk_kernel<T, VPL, true, false><<<g, 256, 0, s>>>(a);
+  else if (a.G > 1) router_topk_kernel<T, VPL, false, true><<<g, 256, 0, s>>>(a);
+  else router_topk_kernel<T, VPL, false, false><<<g, 256, 0, s>>>(a);
+}
 template <typename T>
 hipError_t launch_topk(const RouterArgs& a, int cnt, hipStream_t s) {
-  const int g = row_grid(a.T);
-  if (cnt <= 1) router_topk_kernel<T, 1><<<g, 256, 0, s>>>(a);
-  else if (cnt <= 2) router_topk_kernel<T, 2><<<g, 256, 0, s>>>(a);
-  else if (cnt <= 4) router_topk_kernel<T, 4><<<g, 256, 0, s>>>(a);
-  else if (cnt <= 8) router_topk_kernel<T, 8><<<g, 256, 0, s>>>(a);
-  else if (cnt <= 16) router_topk_kernel<T, 16><<<g, 256, 0, s>>>(a);
-  else router_topk_kernel<T, 32><<<g, 256, 0, s>>>(a);
+  if (cnt <= 1) launch_topk_vpl<T, 1>(a, s);
+  else if (cnt <= 2) launch_topk_vpl<T, 2>(a, s);
+  else if (cnt <= 4) launch_topk_vpl<T, 4>(a, s);
+  else if (cnt <= 8) launch_topk_vpl<T, 8>(a, s);
+  else if (cnt <= 16) launch_topk_vpl<T, 16>(a, s);
+  else launch_topk_vpl<T, 32>(a, s);
   return hipGetLastError();
 }
 
