@@ -30,6 +30,18 @@ namespace {
 
 constexpr int kXcd = 8;
 
+// Workgroups of up to 512 threads are declared as 512: at two waves per SIMD a wave has 256 registers.  Given 512, the
+// compiler takes every K block's sums through the same four accumulation registers, each matrix instruction waiting for
+// the previous one's sums to be read out (a 64x64 wave tile: 125 clocks per instruction instead of 32).
+#define TWO_WAVES __launch_bounds__(512)
+
+// barrier_lds() whose wait the compiler sees: it then knows that fragments read before the barrier are in registers,
+// instead of waiting for the reads issued since.
+__device__ __forceinline__ void barrier_reads() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+
 // 64 lanes x 16 bytes global -> LDS: lane i's bytes from base + voff to lds + 16 i.
 __device__ __forceinline__ void copy16(uint32_t voff, const void* base, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds) : "memory");
@@ -52,6 +64,7 @@ struct Frag {
   __device__ __forceinline__ void load(const v4i lo, const v4i hi) {
     v = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   }
+  __device__ __forceinline__ void take(const Frag<false>& c) { v = c.v; }
 };
 template <>
 struct Frag<true> {
@@ -61,6 +74,10 @@ struct Frag<true> {
     v[1] = to_bf16(lo[2], lo[3]);
     v[2] = to_bf16(hi[0], hi[1]);
     v[3] = to_bf16(hi[2], hi[3]);
+  }
+  __device__ __forceinline__ void take(const Frag<false>& c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = to_bf16(c.v[2 * i], c.v[2 * i + 1]);
   }
 };
 __device__ __forceinline__ v4f block_sum(const Frag<false>& w, const Frag<false>& x) {
@@ -72,6 +89,12 @@ __device__ __forceinline__ v4f block_sum(const Frag<true>& w, const Frag<true>& 
 #pragma unroll
   for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], s, 0, 0, 0);
   return s;
+}
+
+// Whether rows of D (and C) can be accessed 4 columns at a time.
+__device__ __forceinline__ bool can_store4(const DenseArgs& a) {
+  return a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
+         (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
 }
 
 // Four consecutive columns n .. n + 3 of row m (vec: they may be accessed as one vector where all four exist).
@@ -104,69 +127,86 @@ template <int RB, int CB, int WM, int WN, int S>
 struct TileCfg {
   static constexpr int NW = WM * WN;
   static constexpr int BM = 16 * RB * WM, BN = 16 * CB * WN;
-  static constexpr int kPieces = (BM + BN) / 8;         // 1 KB copies (8 rows) per K block
-  static constexpr int kPw = (kPieces + NW - 1) / NW;   // per wave
+  static constexpr int kPieces = (BM + BN) / 8;  // 1 KB copies (8 rows) per K block
+  static constexpr int kPw = kPieces / NW;       // per wave
   static constexpr int kSlot = (BM + BN) * 128;
-  static constexpr int kScale = (BM + BN) * 16;         // one group of 4 K blocks
-  // Scale groups are copied kAhead groups early: their copies are older than the kPw * (S - 2) newest that the wait
-  // before their first use leaves in flight (4 blocks' copies are issued per group).
-  static constexpr int kAhead = S > 6 ? 2 : 1, kScBufs = 2 * kAhead;
-  static constexpr int kLds = S * kSlot + kScBufs * kScale;
+  static constexpr int kScale = (BM + BN) * 16;  // one group of 4 K blocks
+  // Scale groups are copied kAhead groups before their first block: at least 3 blocks' copies are issued after a
+  // group's and before the wait that precedes its first use, more than that wait leaves in flight (S - 2 blocks).
+  static constexpr int kAhead = S > 5 ? 2 : 1, kScBufs = 2 * kAhead;
+  static constexpr int kScOff = S * kSlot;
+  static constexpr int kLds = kScOff + kScBufs * kScale;
   static_assert(kPieces % NW == 0, "every wave copies the same number of pieces");
-  static_assert(S >= 2 && S <= 4 * kAhead + 2 && kPw * (S - 2) < 64, "scales ahead of their use; vmcnt's range");
+  static_assert(S >= 2 && S <= 4 * kAhead + 1 && kPw * (S - 1) < 64, "scales ahead of their use; vmcnt's range");
   static_assert((BM + BN) % 64 == 0 && BM % 64 == 0, "scale rows in whole waves");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
-template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN, int S>
-__global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs a) {
+// A workgroup's tile: where it lies, the copies of its operands and scales into LDS, and the reads of them.
+template <bool GRAN1, int RB, int CB, int WM, int WN, int S>
+struct Tile {
   using C = TileCfg<RB, CB, WM, WN, S>;
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
-  const int lane = lane_id(), wv = uniform(threadIdx.x >> 6);
-  const int l16 = lane & 15, lg = lane >> 4;
-  const int KB = a.K / 128;
-  // this workgroup's K blocks (split K: a multiple of 4 per split)
-  const int per_split = ((KB + 3) / 4 + a.splits - 1) / a.splits * 4;
-  const int kb0 = uniform(min((int)blockIdx.y * per_split, KB)), kb1 = uniform(min(kb0 + per_split, KB));
-
-  // Workgroup b runs on XCD b % 8: consecutive tiles go to one XCD, and consecutive tiles are blocks of up to 8
-  // column tiles by a few row tiles, so an XCD's workgroups share both operands in its L2.
-  const int mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
-  const int tiles = mt * nt;
-  int t = blockIdx.x;
-  {
-    const int per = tiles / kXcd, rem = tiles % kXcd, x = t % kXcd, i = t / kXcd;
-    t = x * per + min(x, rem) + i;
-  }
-  const int gn = 8, g = t / (mt * gn), gw = min(gn, nt - g * gn), r = t - g * mt * gn;
-  const int m0 = uniform(r / gw * C::BM), n0 = uniform((g * gn + r % gw) * C::BN);
-
-  const int wm = (wv / WN) * 16 * RB, wn = (wv % WN) * 16 * CB;
-  const uint32_t lds0 = lds_offset(sm);
-
-  // copies: this wave's pieces q = wv, wv + NW, ...; rows of the A tile, then of the W tile
-  const uint8_t* abase = a.A + (int64_t)m0 * a.lda;
-  const uint8_t* wbase = a.W + (int64_t)n0 * a.ldw;
+  const DenseArgs& a;
+  uint8_t* sm;
+  uint32_t lds0;
+  int lane, wv, l16, lg, KB, kb0, kb1, m0, n0, wm, wn;
+  const uint8_t *abase, *wbase;
   uint32_t voff[C::kPw];
+  int off_lo, off_hi;
+  bool sc_vec;
+
+  __device__ __forceinline__ Tile(const DenseArgs& args, uint8_t* smem) : a(args), sm(smem) {
+    lane = lane_id();
+    wv = uniform(threadIdx.x >> 6);
+    l16 = lane & 15;
+    lg = lane >> 4;
+    lds0 = lds_offset(sm);
+    KB = a.K / 128;
+    // this workgroup's K blocks (split K: a multiple of 4 per split)
+    const int per_split = ((KB + 3) / 4 + a.splits - 1) / a.splits * 4;
+    kb0 = uniform(min((int)blockIdx.y * per_split, KB));
+    kb1 = uniform(min(kb0 + per_split, KB));
+    // Workgroup b runs on XCD b % 8: consecutive tiles go to one XCD, and consecutive tiles are blocks of up to 8
+    // column tiles by a few row tiles, so an XCD's workgroups share both operands in its L2.
+    const int mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN, tiles = mt * nt;
+    const int per = tiles / kXcd, rem = tiles % kXcd, x = blockIdx.x % kXcd;
+    const int t = x * per + min(x, rem) + blockIdx.x / kXcd;
+    const int gn = 8, g = t / (mt * gn), gw = min(gn, nt - g * gn), r = t - g * mt * gn;
+    m0 = uniform(r / gw * C::BM);
+    n0 = uniform((g * gn + r % gw) * C::BN);
+    wm = (wv / WN) * 16 * RB;
+    wn = (wv % WN) * 16 * CB;
+    // copies: this wave's pieces q = wv, wv + NW, ...; rows of the A tile, then of the W tile
+    abase = a.A + (int64_t)m0 * a.lda;
+    wbase = a.W + (int64_t)n0 * a.ldw;
 #pragma unroll
-  for (int i = 0; i < C::kPw; ++i) {
-    const int q = wv + C::NW * i;
-    int row = 8 * q + (lane >> 3);
-    const int c = (lane & 7) ^ ((row >> 1) & 7);
-    if (row < C::BM)
-      voff[i] = (uint32_t)min(row, a.M - 1 - m0) * (uint32_t)a.lda + 16u * c;
-    else
-      voff[i] = (uint32_t)min(row - C::BM, a.N - 1 - n0) * (uint32_t)a.ldw + 16u * c;
+    for (int i = 0; i < C::kPw; ++i) {
+      const int row = 8 * (wv + C::NW * i) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+      voff[i] = row < C::BM ? (uint32_t)min(row, a.M - 1 - m0) * (uint32_t)a.lda + 16u * c
+                            : (uint32_t)min(row - C::BM, a.N - 1 - n0) * (uint32_t)a.ldw + 16u * c;
+    }
+    // fragment read offsets: row l16 of a 16-row block at 128 l16, its chunk c at position c ^ ((row >> 1) & 7)
+    const int fsw = (l16 >> 1) & 7;
+    off_lo = l16 * 128 + 16 * (lg ^ fsw);
+    off_hi = l16 * 128 + 16 * ((4 + lg) ^ fsw);
+    sc_vec = KB % 4 == 0 && (((uintptr_t)a.SFA | (uintptr_t)a.SFW) & 15) == 0;
   }
-  auto copy_piece = [&](int kb, int i) {
+
+  __device__ __forceinline__ void copy_piece(int kb, int i) const {
     const int q = wv + C::NW * i;
     const uint8_t* base = (8 * q < C::BM ? abase : wbase) + (int64_t)kb * 128;
     copy16(voff[i], base, uniform(lds0 + (kb % S) * C::kSlot + 1024 * q));
-  };
-
-  // scales: group g4 (K blocks 4 g4 ..) of row r of the tiles at 16 r of buffer g4 & 1
-  const bool sc_vec = KB % 4 == 0 && (((uintptr_t)a.SFA | (uintptr_t)a.SFW) & 15) == 0;
-  auto scales = [&](int g4) {
+  }
+  // The K block that a0 and w0 point at, a wave's piece i, into slot SLOT.  (The copy's offset field moves its LDS address
+  // too, so the block's offset is in the pointers.)
+  template <int SLOT>
+  __device__ __forceinline__ void copy_piece_at(const uint8_t* a0, const uint8_t* w0, int i) const {
+    const int q = wv + C::NW * i;
+    copy16(voff[i], 8 * q < C::BM ? a0 : w0, uniform(lds0 + SLOT * C::kSlot + 1024 * q));
+  }
+  // the scales of K blocks 4 g4 .. of row r of the tiles at 16 r of a group buffer
+  __device__ __forceinline__ int scale_buf(int g4) const { return C::kScOff + (g4 & (C::kScBufs - 1)) * C::kScale; }
+  __device__ __forceinline__ void copy_scales(int g4) const {
 #pragma unroll
     for (int q = 0; q < (C::BM + C::BN) / 64; q += C::NW) {
       const int p = q + wv;
@@ -174,45 +214,32 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
       const int row = 64 * p + lane;
       const bool is_a = 64 * p < C::BM;
       const float* base = is_a ? a.SFA : a.SFW;
-      const int64_t sr = is_a ? min(m0 + row, a.M - 1) : (GRAN1 ? min(n0 + row - C::BM, a.N - 1)
-                                                                 : min(n0 + row - C::BM, a.N - 1) / 128);
-      const uint32_t dst = lds0 + S * C::kSlot + (g4 & (C::kScBufs - 1)) * C::kScale;
+      const int sr = is_a ? min(m0 + row, a.M - 1) : min(n0 + row - C::BM, a.N - 1) / (GRAN1 ? 1 : 128);
       if (sc_vec) {
-        const int64_t sr0 = is_a ? m0 : (GRAN1 ? n0 : n0 / 128);
-        copy16((uint32_t)(sr - sr0) * (uint32_t)KB * 4u, base + sr0 * KB + 4 * g4, uniform(dst + 1024 * p));
+        const int sr0 = is_a ? m0 : n0 / (GRAN1 ? 1 : 128);
+        copy16((uint32_t)(sr - sr0) * (uint32_t)KB * 4u, base + (int64_t)sr0 * KB + 4 * g4,
+               uniform(lds0 + scale_buf(g4) + 1024 * p));
       } else {
-        const float* s = base + sr * KB;
+        const float* s = base + (int64_t)sr * KB;
         v4f v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = s[min(4 * g4 + j, KB - 1)];
-        *(v4f*)(sm + S * C::kSlot + (g4 & (C::kScBufs - 1)) * C::kScale + 16 * row) = v;
+        *(v4f*)(sm + scale_buf(g4) + 16 * row) = v;
       }
     }
-  };
+  }
+  // before step kb: the group that is first used kAhead groups later
+  __device__ __forceinline__ void copy_scales_at(int kb) const {
+    if ((kb & 3) == 0 && kb + 4 * C::kAhead < kb1) copy_scales((kb >> 2) + C::kAhead);
+  }
 
-  // fragment read offsets: row l16 of a 16-row block at 128 l16, its chunk c at position c ^ ((row >> 1) & 7)
-  const int fsw = (l16 >> 1) & 7;
-  const int off_lo = l16 * 128 + 16 * (lg ^ fsw), off_hi = l16 * 128 + 16 * ((4 + lg) ^ fsw);
-  auto frag = [&](Frag<WIDE>& f, int kb, int row) {
+  template <typename F>
+  __device__ __forceinline__ void frag(F& f, int kb, int row) const {
     const uint8_t* p = sm + (kb % S) * C::kSlot + row * 128;
     f.load(*(const v4i*)(p + off_lo), *(const v4i*)(p + off_hi));
-  };
-
-  v4f acc[RB][CB];
-#pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  Frag<WIDE> wf[CB], xf[2];
-  float sa[RB];
-  v4f sw[GRAN1 ? CB : 1];
-
-  // the first fragments and the scales of block kb
-  auto first = [&](int kb) {
-#pragma unroll
-    for (int j = 0; j < CB; ++j) frag(wf[j], kb, C::BM + wn + 16 * j);
-    frag(xf[0], kb, wm);
-    const float* s = (const float*)(sm + S * C::kSlot + ((kb >> 2) & (C::kScBufs - 1)) * C::kScale) + (kb & 3);
+  }
+  __device__ __forceinline__ void read_scales(int kb, float (&sa)[RB], v4f (&sw)[GRAN1 ? CB : 1]) const {
+    const float* s = (const float*)(sm + scale_buf(kb >> 2)) + (kb & 3);
 #pragma unroll
     for (int i = 0; i < RB; ++i) sa[i] = s[4 * (wm + 16 * i + l16)];
     if constexpr (GRAN1) {
@@ -223,111 +250,274 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_dense_kernel(const DenseArgs
     } else {
       sw[0][0] = s[4 * (C::BM + wn)];
     }
+  }
+
+  __device__ __forceinline__ void store(v4f (&acc)[RB][CB]) const {
+    // The sums are whole before any lane's store is masked off: without this the compiler moves the last matrix
+    // instructions, and the loads of their operands, under the stores' masks, where the other lanes' operands are stale.
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j) asm volatile("" : "+v"(acc[i][j]));
+    DenseArgs o = a;
+    if (a.splits > 1) {  // this split's sums, whole rows of 4
+      o.f32 = 1;
+      o.C = nullptr;
+      o.N = (a.N + 3) & ~3;
+      o.ldd = o.N;
+      o.D = a.ws + (int64_t)blockIdx.y * a.M * o.N;
+    }
+    const bool vec = can_store4(o);
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j) store4(o, m0 + wm + 16 * i + l16, n0 + wn + 16 * j + 4 * lg, acc[i][j], vec);
+  }
+};
+
+// One K block's sum into the accumulator.
+template <bool GRAN1>
+__device__ __forceinline__ void promote(v4f& acc, const v4f sum, float sa, const v4f sw) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(sum[e], GRAN1 ? sa * sw[e] : sa, acc[e]);
+}
+
+// Tiles whose fragments fit the registers twice: block kb + 1's fragments and scales are read while block kb is
+// multiplied, and block kb + 4 is copied meanwhile into the slot that block kb left when it was read.  With few matrix
+// instructions per step a wave's time is its instruction count, so the loop is unrolled over the 4 slots (and the 4 blocks of
+// a scale group): slots, offsets and scale positions are constants (64x64 tile: 200 instructions and 0.31 us per K block
+// with computed ones).
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+__global__ TWO_WAVES void gemm_dense_small_kernel(const DenseArgs a) {
+  constexpr int S = 4;
+  using C = TileCfg<RB, CB, WM, WN, S>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
+  const Tile<GRAN1, RB, CB, WM, WN, S> T(a, sm);
+  const int kb0 = T.kb0, kb1 = T.kb1;  // kb0 is a multiple of 4: block kb lies in slot (kb - kb0) & 3 = kb & 3
+  v4f acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  struct Regs {
+    Frag<false> w[CB], x[RB];  // codes; widened when multiplied
+    float sa[RB];
+    v4f sw[GRAN1 ? CB : 1];
+  } reg[2];
+  const uint8_t* pa = sm + T.wm * 128;
+  const uint8_t* pw = sm + (C::BM + T.wn) * 128;
+  // fragment f (columns first, then rows) of a block in slot `slot`
+  auto read_frag = [&](Regs& r, int slot, int f) {
+    const uint8_t* p = f < CB ? pw + slot * C::kSlot + 2048 * f : pa + slot * C::kSlot + 2048 * (f - CB);
+    Frag<false>& to = f < CB ? r.w[f < CB ? f : 0] : r.x[f < CB ? 0 : f - CB];
+    to.load(*(const v4i*)(p + T.off_lo), *(const v4i*)(p + T.off_hi));
+  };
+  auto read_scales = [&](Regs& r, int slot, const float* sc) {  // sc: the block's scale group
+#pragma unroll
+    for (int i = 0; i < RB; ++i) r.sa[i] = sc[4 * (T.wm + 16 * i + T.l16) + slot];
+    if constexpr (GRAN1) {
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.sw[j][e] = sc[4 * (C::BM + T.wn + 16 * j + 4 * T.lg + e) + slot];
+    } else {
+      r.sw[0][0] = sc[4 * (C::BM + T.wn) + slot];
+    }
+  };
+  // Multiply a block; beside its matrix instructions, one piece of the other work after each: fragments of the next
+  // block (more), copies (copies), promotions two tiles behind.  Issued in one go, the reads, the copies and the matrix
+  // instructions take turns instead of overlapping: every wave waits at the same queue.
+  auto multiply = [&](const Regs& r, bool more, Regs& next, int next_slot, const float* next_sc, bool copies,
+                      auto copy) {
+    constexpr int NM = RB * CB, NF = RB + CB, D = NM > 2 ? 2 : 1;
+    Frag<WIDE> w[CB], x;
+#pragma unroll
+    for (int j = 0; j < CB; ++j) w[j].take(r.w[j]);
+    v4f sum[D + 1];
+    static_for<0, NM + D>([&](auto mc) {
+      constexpr int m = decltype(mc)::value;
+      if constexpr (m < NM) {
+        if constexpr (m % CB == 0) x.take(r.x[m / CB]);
+        sum[m % (D + 1)] = block_sum(w[m % CB], x);
+        if (more) {
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+            if (f * NM / NF == m) read_frag(next, next_slot, f);
+          if (m == NM - 1) read_scales(next, next_slot, next_sc);
+        }
+        if (copies) {
+#pragma unroll
+          for (int i = 0; i < C::kPw; ++i)
+            if (i * NM / C::kPw == m) copy(i);
+        }
+      }
+      if constexpr (m >= D) {
+        constexpr int o = m - D, oi = o / CB, oj = o % CB;
+        promote<GRAN1>(acc[oi][oj], sum[o % (D + 1)], GRAN1 ? r.sa[oi] : r.sa[oi] * r.sw[0][0], r.sw[GRAN1 ? oj : 0]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  auto scale_group = [&](int kb) { return (const float*)(sm + T.scale_buf(kb >> 2)); };
+
+  if (kb0 < kb1) {
+    const uint8_t *a0 = T.abase + (int64_t)kb0 * 128, *w0 = T.wbase + (int64_t)kb0 * 128;
+    T.copy_scales(kb0 >> 2);
+    static_for<0, S>([&](auto u) {
+      if (kb0 + decltype(u)::value < kb1) {
+#pragma unroll
+        for (int i = 0; i < C::kPw; ++i) T.template copy_piece_at<decltype(u)::value>(a0, w0, i);
+      }
+      a0 += 128;
+      w0 += 128;
+    });
+    const bool full = kb0 + S <= kb1;
+    if (full)
+      wait_vmcnt<C::kPw*(S - 1)>();
+    else
+      wait_vmcnt<0>();
+    barrier_reads();
+#pragma unroll
+    for (int f = 0; f < RB + CB; ++f) read_frag(reg[0], 0, f);
+    read_scales(reg[0], 0, scale_group(kb0));
+    if (full) wait_vmcnt<C::kPw*(S - 2)>();
+    barrier_reads();  // block kb0 is in registers, block kb0 + 1 in LDS
+    // kind 2: block k + S is copied; 1: no more copies, but a next block; 0: the last block
+    auto step = [&](int k, auto uc, auto kind) {
+      constexpr int u = decltype(uc)::value;
+      constexpr bool more = decltype(kind)::value > 0, copies = decltype(kind)::value == 2;
+      if constexpr (u == 0) T.copy_scales_at(k);
+      multiply(reg[u & 1], more, reg[(u + 1) & 1], (u + 1) & 3, scale_group(k + 1), copies,
+               [&](int i) { T.template copy_piece_at<u>(a0, w0, i); });
+      if constexpr (copies) {
+        a0 += 128;
+        w0 += 128;
+      }
+      if constexpr (more) {
+        wait_vmcnt<copies ? C::kPw*(S - 2) : 0>();
+        barrier_reads();
+      }
+    };
+    int kb = kb0;
+    for (; kb + 2 * S <= kb1; kb += S)  // whole rounds of the ring
+      static_for<0, S>([&](auto u) { step(kb + decltype(u)::value, u, IntC<2>{}); });
+    for (; kb < kb1; kb += S)
+      static_for<0, S>([&](auto u) {
+        const int k = kb + decltype(u)::value;
+        if (k + S < kb1) step(k, u, IntC<2>{});
+        else if (k + 1 < kb1) step(k, u, IntC<1>{});
+        else if (k < kb1) step(k, u, IntC<0>{});
+      });
+  }
+  T.store(acc);
+}
+
+// The 256x256 tile (8 waves of 128x64: two per SIMD, so that one wave's promotions run beside the other's matrix
+// instructions; a wave's 128 accumulators leave room for its fragments once).  LDS traffic (64 KB copied in and 192
+// KB read per K block) takes as long as the matrix instructions, so both have to run all the time:
+//  * row blocks 0 .. RB-3 in turn, their fragments read two blocks ahead;
+//  * then the barrier that publishes block kb + 1, every fragment of block kb being in registers, and the last two row
+//    blocks column by column: after column j's two matrix instructions its weight fragment is read anew for block kb + 1;
+//  * block kb + 2 is copied into the half slots that block kb leaves: its weights from the first row block of step kb on (a
+//    second barrier says that every wave has read them), its activations from the barrier on, so that a copy has about 1.75 and one
+//    step to arrive.
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+__global__ TWO_WAVES void gemm_dense_kernel(const DenseArgs a) {
+  constexpr int S = 2;
+  using C = TileCfg<RB, CB, WM, WN, S>;
+  static_assert(RB >= 8 && RB % 4 == 0 && C::kPw == 2 * CB && C::BM == 8 * C::NW * CB,
+                "fragment ring; a wave's first CB pieces are rows of A, its last CB rows of W");
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
+  const Tile<GRAN1, RB, CB, WM, WN, S> T(a, sm);
+  const int kb0 = T.kb0, kb1 = T.kb1;
+  v4f acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  Frag<WIDE> w[CB], x[4];
+
+  // kind 2: block kb + 2 exists; 1: block kb + 1 does; 0: the last block
+  auto step = [&](int kb, auto kind) {
+    constexpr int more = decltype(kind)::value;
+    float sa[RB];
+    v4f sw[GRAN1 ? CB : 1];
+    T.read_scales(kb, sa, sw);
+    v4f sum[2][CB];
+    auto prom = [&](int i, int j) {
+      promote<GRAN1>(acc[i][j], sum[i & 1][j], GRAN1 ? sa[i] : sa[i] * sw[0][0], sw[GRAN1 ? j : 0]);
+    };
+#pragma unroll
+    for (int i = 0; i < RB - 2; ++i) {
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        sum[i & 1][j] = block_sum(w[j], x[i & 3]);
+        if (j == 0) T.frag(x[(i + 2) & 3], kb, T.wm + 16 * (i + 2));
+        if constexpr (more == 2)
+          if (j == 2 && i >= 1 && i <= CB) T.copy_piece(kb + 2, CB + i - 1);  // the weights of block kb + 2
+        if (i > 0) prom(i - 1, j);
+        __builtin_amdgcn_sched_barrier(0);  // one piece of the other work after each matrix instruction
+      }
+      // every wave has used its weight fragments of block kb, i.e. read them: their half of the slot is free
+      if constexpr (more == 2)
+        if (i == 0) asm volatile("s_barrier" ::: "memory");
+    }
+    if constexpr (more > 0) {
+      wait_vmcnt<more == 2 ? CB : 0>();  // all but block kb + 2's weights
+      barrier_reads();
+      T.frag(x[0], kb + 1, T.wm);
+      T.frag(x[1], kb + 1, T.wm + 16);
+    }
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+      const v4f s0 = block_sum(w[j], x[(RB - 2) & 3]), s1 = block_sum(w[j], x[(RB - 1) & 3]);
+      prom(RB - 3, j);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (more > 0) T.frag(w[j], kb + 1, C::BM + T.wn + 16 * j);
+      if constexpr (more == 2) T.copy_piece(kb + 2, j);
+      sum[(RB - 2) & 1][j] = s0;
+      prom(RB - 2, j);
+      sum[(RB - 1) & 1][j] = s1;
+      prom(RB - 1, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
   if (kb0 < kb1) {
+    T.copy_scales(kb0 >> 2);
 #pragma unroll
-  for (int g4 = 0; g4 < C::kAhead; ++g4)
-    if (kb0 + 4 * g4 < kb1) scales((kb0 >> 2) + g4);
-#pragma unroll
-  for (int b = 0; b < S - 1; ++b)
-    if (kb0 + b < kb1) {
-#pragma unroll
-      for (int i = 0; i < C::kPw; ++i) copy_piece(kb0 + b, i);
-    }
-  if (kb0 + S - 1 <= kb1)
-    wait_vmcnt<C::kPw * (S - 2)>();
-  else
+    for (int i = 0; i < C::kPw; ++i) T.copy_piece(kb0, i);
     wait_vmcnt<0>();
-  barrier_lds();
-  first(kb0);
-
-  // One K block.  Row block i's matrix instructions alternate with the promotion of row block i - 1.
-  // kind 2: block kb + S - 1 is copied meanwhile; 1: no more copies, but a next block; 0: the last block.
-  auto step = [&](int kb, auto kind) {
-    constexpr bool copies = decltype(kind)::value == 2, more = decltype(kind)::value > 0;
-    v4f sum[2][CB];
-    float sax[RB];
-    v4f swx[GRAN1 ? CB : 1];
+    barrier_reads();
+    T.frag(x[0], kb0, T.wm);
+    T.frag(x[1], kb0, T.wm + 16);
 #pragma unroll
-    for (int i = 0; i < RB; ++i) sax[i] = GRAN1 ? sa[i] : sa[i] * sw[0][0];
-    if constexpr (GRAN1) {
+    for (int j = 0; j < CB; ++j) T.frag(w[j], kb0, C::BM + T.wn + 16 * j);
+    if (kb0 + 1 < kb1) {
 #pragma unroll
-      for (int j = 0; j < CB; ++j) swx[j] = sw[j];
+      for (int i = 0; i < C::kPw; ++i) T.copy_piece(kb0 + 1, i);
     }
-    auto promote = [&](int i, int j) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float s = GRAN1 ? sax[i] * swx[j][e] : sax[i];
-        acc[i][j][e] = __builtin_fmaf(sum[i & 1][j][e], s, acc[i][j][e]);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      if (i + 1 < RB) frag(xf[(i + 1) & 1], kb, wm + 16 * (i + 1));
-      if constexpr (copies) {  // spread over the first row blocks
-        constexpr int kSpread = RB > 1 ? (RB + 1) / 2 : 1, kEach = (C::kPw + kSpread - 1) / kSpread;
-#pragma unroll
-        for (int c = i * kEach; c < (i + 1) * kEach && c < C::kPw; ++c) copy_piece(kb + S - 1, c);
-      }
-#pragma unroll
-      for (int j = 0; j < CB; ++j) {
-        sum[i & 1][j] = block_sum(wf[j], xf[i & 1]);
-        if (i > 0) promote(i - 1, j);
-      }
-      __builtin_amdgcn_sched_barrier(0);  // keep the row blocks' order (hoisted fragments would spill)
+    int kb = kb0;
+    for (; kb + 2 < kb1; ++kb) {
+      T.copy_scales_at(kb);
+      step(kb, IntC<2>{});
     }
-    if constexpr (more) {
-      wait_vmcnt<copies ? C::kPw*(S - 2) : 0>();
-      barrier_lds();
-      first(kb + 1);
-    }
-#pragma unroll
-    for (int j = 0; j < CB; ++j) promote(RB - 1, j);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  int kb = kb0;
-  for (; kb + S - 1 < kb1; ++kb) {
-    if ((kb & 3) == 0 && kb + 4 * C::kAhead < kb1) scales((kb >> 2) + C::kAhead);
-    step(kb, IntC<2>{});
-  }
-  if constexpr (S > 2) {
-    for (; kb + 1 < kb1; ++kb) {
-      if ((kb & 3) == 0 && kb + 4 * C::kAhead < kb1) scales((kb >> 2) + C::kAhead);
+    if (kb + 1 < kb1) {
+      T.copy_scales_at(kb);
       step(kb, IntC<1>{});
+      ++kb;
     }
+    step(kb, IntC<0>{});
   }
-  step(kb1 - 1, IntC<0>{});
-  }
-
-  // The sums are whole before any lane's store is masked off: without this the compiler moves the last matrix
-  // instructions, and the loads of their operands, under the stores' masks, where the other lanes' operands are stale.
-#pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < CB; ++j) asm volatile("" : "+v"(acc[i][j]));
-  DenseArgs o = a;
-  if (a.splits > 1) {  // this split's sums, whole rows of 4
-    o.f32 = 1;
-    o.C = nullptr;
-    o.N = (a.N + 3) & ~3;
-    o.ldd = o.N;
-    o.D = a.ws + (int64_t)blockIdx.y * a.M * o.N;
-  }
-  const bool vec = o.ldd % 4 == 0 && ((uintptr_t)o.D & (o.f32 ? 15 : 7)) == 0 &&
-                   (!o.C || (o.ldc % 4 == 0 && ((uintptr_t)o.C & 15) == 0));
-#pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < CB; ++j) store4(o, m0 + wm + 16 * i + l16, n0 + wn + 16 * j + 4 * lg, acc[i][j], vec);
+  T.store(acc);
 }
 
 // Split K: the splits' partial sums, added in split order, and the addend.
 __global__ __launch_bounds__(256) void gemm_dense_join_kernel(const DenseArgs a) {
   const int np = (a.N + 3) / 4;
   const int64_t total = (int64_t)a.M * np;
-  const bool vec = a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
-                   (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
+  const bool vec = can_store4(a);
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
     v4f v = *(const v4f*)(a.ws + 4 * q);
     for (int k = 1; k < a.splits; ++k) v += *(const v4f*)(a.ws + 4 * (q + k * total));
@@ -338,8 +528,11 @@ __global__ __launch_bounds__(256) void gemm_dense_join_kernel(const DenseArgs a)
 template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN, int S>
 hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
   using C = TileCfg<RB, CB, WM, WN, S>;
-  const int tiles = ((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN);
-  gemm_dense_kernel<WIDE, GRAN1, RB, CB, WM, WN, S><<<dim3(tiles, a.splits), WM * WN * 64, 0, s>>>(a);
+  const dim3 grid(((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN), a.splits);
+  if constexpr (S == 2)
+    gemm_dense_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
+  else
+    gemm_dense_small_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t need = ((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256, cap = (int64_t)device_info().cus * 16;
@@ -367,7 +560,7 @@ struct StreamCfg {
 };
 
 template <bool WIDE, bool GRAN1, int RB, int CB, int KS, int S>
-__global__ __launch_bounds__(KS * 64) void gemm_stream_kernel(const DenseArgs a) {
+__global__ TWO_WAVES void gemm_stream_kernel(const DenseArgs a) {
   using C = StreamCfg<RB, CB, KS, S>;
   constexpr int kRows = 16 * RB, kCols = 16 * CB;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
@@ -468,8 +661,7 @@ __global__ __launch_bounds__(KS * 64) void gemm_stream_kernel(const DenseArgs a)
 #pragma unroll
     for (int j = 0; j < CB; ++j) *(v4f*)(part + (16 * i + l16) * (kCols + 4) + 16 * j + 4 * lg) = acc[i][j];
   __syncthreads();
-  const bool vec = a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
-                   (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
+  const bool vec = can_store4(a);
   for (int q = threadIdx.x; q < kRows * kCols / 4; q += KS * 64) {
     const int m = q / (kCols / 4), n = 4 * (q % (kCols / 4));
     v4f v = {0.f, 0.f, 0.f, 0.f};
@@ -490,7 +682,7 @@ hipError_t launch_stream(const DenseArgs& a, hipStream_t s) {
 #define V1 1, 1, 8, 4
 #define V2 2, 1, 8, 3
 #define V4 4, 1, 4, 3
-#define TW 4, 4, 2, 2, 2
+#define TW 4, 2, 2, 4, 4
 #define TN 8, 4, 2, 4, 2
 #define SP 1
 #define MS 64
