@@ -77,7 +77,10 @@ struct Frag<true> {
   }
   __device__ __forceinline__ void take(const Frag<false>& c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = to_bf16(c.v[2 * i], c.v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) take_quarter(c, i);
+  }
+  __device__ __forceinline__ void take_quarter(const Frag<false>& c, int i) {
+    v[i] = to_bf16(c.v[2 * i], c.v[2 * i + 1]);
   }
 };
 __device__ __forceinline__ v4f block_sum(const Frag<false>& w, const Frag<false>& x) {
@@ -104,7 +107,7 @@ __device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v, 
   if (vec && n + 4 <= a.N) {
     if (a.f32) {
       if (a.C) v += *(const v4f*)(a.C + (int64_t)m * a.ldc + n);
-      *(v4f*)((float*)a.D + at) = v;
+      __builtin_nontemporal_store(v, (v4f*)((float*)a.D + at));
     } else {
       uint2 o;
       o.x = f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16);
@@ -426,8 +429,9 @@ template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
 __global__ TWO_WAVES void gemm_dense_kernel(const DenseArgs a) {
   constexpr int S = 2;
   using C = TileCfg<RB, CB, WM, WN, S>;
-  static_assert(RB >= 8 && RB % 4 == 0 && C::kPw == 2 * CB && C::BM == 8 * C::NW * CB,
+  static_assert(RB >= 4 && RB % 4 == 0 && C::kPw == 2 * CB && C::BM == 8 * C::NW * CB,
                 "fragment ring; a wave's first CB pieces are rows of A, its last CB rows of W");
+  static_assert(!WIDE || CB == 4, "a row's 4 quarters are widened beside 4 columns");
   __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
   const Tile<GRAN1, RB, CB, WM, WN, S> T(a, sm);
   const int kb0 = T.kb0, kb1 = T.kb1;
@@ -436,7 +440,12 @@ __global__ TWO_WAVES void gemm_dense_kernel(const DenseArgs a) {
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  Frag<WIDE> w[CB], x[4];
+  Frag<false> xr[4];          // row fragments as read, in a ring
+  Frag<WIDE> w[CB], xw[2];    // as multiplied (xw: WIDE only)
+  auto x = [&](int i) -> const Frag<WIDE>& {
+    if constexpr (WIDE) return xw[i & 1];
+    else return xr[i & 3];
+  };
 
   // kind 2: block kb + 2 exists; 1: block kb + 1 does; 0: the last block
   auto step = [&](int kb, auto kind) {
@@ -452,10 +461,13 @@ __global__ TWO_WAVES void gemm_dense_kernel(const DenseArgs a) {
     for (int i = 0; i < RB - 2; ++i) {
 #pragma unroll
       for (int j = 0; j < CB; ++j) {
-        sum[i & 1][j] = block_sum(w[j], x[i & 3]);
-        if (j == 0) T.frag(x[(i + 2) & 3], kb, T.wm + 16 * (i + 2));
-        if constexpr (more == 2)
-          if (j == 2 && i >= 1 && i <= CB) T.copy_piece(kb + 2, CB + i - 1);  // the weights of block kb + 2
+        sum[i & 1][j] = block_sum(w[j], x(i));
+        if (j == 0) T.frag(xr[(i + 2) & 3], kb, T.wm + 16 * (i + 2));
+        if constexpr (WIDE) xw[(i + 1) & 1].take_quarter(xr[(i + 1) & 3], j);
+        if constexpr (more == 2) {  // the weights of block kb + 2
+          const int c = RB >= 8 ? (j == 2 ? i - 1 : -1) : (i == 1 ? j : -1);
+          if (c >= 0 && c < CB) T.copy_piece(kb + 2, CB + c);
+        }
         if (i > 0) prom(i - 1, j);
         __builtin_amdgcn_sched_barrier(0);  // one piece of the other work after each matrix instruction
       }
@@ -466,21 +478,32 @@ __global__ TWO_WAVES void gemm_dense_kernel(const DenseArgs a) {
     if constexpr (more > 0) {
       wait_vmcnt<more == 2 ? CB : 0>();  // all but block kb + 2's weights
       barrier_reads();
-      T.frag(x[0], kb + 1, T.wm);
-      T.frag(x[1], kb + 1, T.wm + 16);
+    }
+    Frag<WIDE> xl = x(RB - 2), xm;  // the last two rows
+    xm.take(xr[(RB - 1) & 3]);
+    Frag<false> wr[2];
+    if constexpr (more > 0) {
+      T.frag(xr[0], kb + 1, T.wm);
+      T.frag(xr[1], kb + 1, T.wm + 16);
     }
 #pragma unroll
     for (int j = 0; j < CB; ++j) {
-      const v4f s0 = block_sum(w[j], x[(RB - 2) & 3]), s1 = block_sum(w[j], x[(RB - 1) & 3]);
+      const v4f s0 = block_sum(w[j], xl), s1 = block_sum(w[j], xm);
       prom(RB - 3, j);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (more > 0) T.frag(w[j], kb + 1, C::BM + T.wn + 16 * j);
+      if constexpr (more > 0) T.frag(wr[j & 1], kb + 1, C::BM + T.wn + 16 * j);
       if constexpr (more == 2) T.copy_piece(kb + 2, j);
+      if constexpr (more > 0)
+        if (j > 0) w[j - 1].take(wr[(j - 1) & 1]);
       sum[(RB - 2) & 1][j] = s0;
       prom(RB - 2, j);
       sum[(RB - 1) & 1][j] = s1;
       prom(RB - 1, j);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (more > 0) {
+      w[CB - 1].take(wr[(CB - 1) & 1]);
+      if constexpr (WIDE) xw[0].take(xr[0]);
     }
   };
 
@@ -490,10 +513,15 @@ __global__ TWO_WAVES void gemm_dense_kernel(const DenseArgs a) {
     for (int i = 0; i < C::kPw; ++i) T.copy_piece(kb0, i);
     wait_vmcnt<0>();
     barrier_reads();
-    T.frag(x[0], kb0, T.wm);
-    T.frag(x[1], kb0, T.wm + 16);
+    T.frag(xr[0], kb0, T.wm);
+    T.frag(xr[1], kb0, T.wm + 16);
+    if constexpr (WIDE) xw[0].take(xr[0]);
 #pragma unroll
-    for (int j = 0; j < CB; ++j) T.frag(w[j], kb0, C::BM + T.wn + 16 * j);
+    for (int j = 0; j < CB; ++j) {
+      Frag<false> f;
+      T.frag(f, kb0, C::BM + T.wn + 16 * j);
+      w[j].take(f);
+    }
     if (kb0 + 1 < kb1) {
 #pragma unroll
       for (int i = 0; i < C::kPw; ++i) T.copy_piece(kb0 + 1, i);
@@ -525,19 +553,26 @@ __global__ __launch_bounds__(256) void gemm_dense_join_kernel(const DenseArgs a)
   }
 }
 
-template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN, int S>
-hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
-  using C = TileCfg<RB, CB, WM, WN, S>;
-  const dim3 grid(((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN), a.splits);
-  if constexpr (S == 2)
-    gemm_dense_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
-  else
-    gemm_dense_small_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+hipError_t launch_join(const DenseArgs& a, hipStream_t s) {
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t need = ((int64_t)a.M * ((a.N + 3) / 4) + 255) / 256, cap = (int64_t)device_info().cus * 16;
   gemm_dense_join_kernel<<<(unsigned)(need < cap ? need : cap), 256, 0, s>>>(a);
   return hipGetLastError();
+}
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+hipError_t launch_small(const DenseArgs& a, hipStream_t s) {
+  using C = TileCfg<RB, CB, WM, WN, 4>;
+  const dim3 grid(((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN), a.splits);
+  gemm_dense_small_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
+  return launch_join(a, s);
+}
+template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
+hipError_t launch_big(const DenseArgs& a, hipStream_t s) {
+  using C = TileCfg<RB, CB, WM, WN, 2>;
+  const dim3 grid(((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN), a.splits);
+  gemm_dense_kernel<WIDE, GRAN1, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
+  return launch_join(a, s);
 }
 
 // Few rows (a decode step): every weight byte is used by one wave, so waves need nothing from one another.  A
@@ -678,29 +713,92 @@ hipError_t launch_stream(const DenseArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-#ifndef V1
-#define V1 1, 1, 8, 4
-#define V2 2, 1, 8, 3
-#define V4 4, 1, 4, 3
-#define TW 4, 2, 2, 4, 4
-#define TN 8, 4, 2, 4, 2
-#define SP 1
-#define MS 64
-#endif
+// Which kernel, by sizes alone.  Times in us per K block of one round of tiles over the 256 compute units, as
+// measured with the whole chip busy (first: one workgroup per compute unit; second, where two fit: both); the tile with
+// the smallest sum of rounds is taken.  Measured (us, N x K = 4096 x 7168, bf16 output): 256 rows 64x64 22.2, 64x128
+// 29.7, 128x128 40.0; 512 rows 34.3, 30.4, 39.6; 1024 rows 58.9, 51.1, 40.8; 2048 rows 128x128 72.7, 256x256 86; 4096
+// rows 141, 111.
+enum Kind { kStream16, kStream32, kStream64, k64x64, k64x128, k128x128, k128x128two, k256x256 };
+struct Plan {
+  Kind kind;
+  int splits;
+};
+struct TileCost {
+  Kind kind;
+  int bm, bn;
+  float one, two;  // two = 0: one workgroup per compute unit
+};
+constexpr int kCus = 256;
+
+Plan plan_dense(int M, int N, int K, bool wide) {
+  if (M <= 16) return {kStream16, 1};
+  if (M <= 32) return {kStream32, 1};
+  if (M <= 64) return {kStream64, 1};
+  constexpr TileCost narrow_t[] = {{k64x64, 64, 64, 0.33f, 0.57f},
+                                   {k64x128, 64, 128, 0.5f, 0.0f},
+                                   {k128x128, 128, 128, 0.69f, 0.0f},
+                                   {k256x256, 256, 256, 1.9f, 0.0f}};
+  constexpr TileCost wide_t[] = {{k64x64, 64, 64, 0.5f, 0.76f},
+                                 {k64x128, 64, 128, 0.74f, 0.0f},
+                                 {k128x128, 128, 128, 1.3f, 0.0f},
+                                 {k128x128two, 128, 128, 1.7f, 2.05f}};
+  Plan best{k64x64, 1};
+  float least = 0.0f;
+  int64_t best_tiles = 0;
+  auto consider = [&](const TileCost& c) {
+    const int64_t t = (int64_t)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    const float f = c.two == 0.0f ? c.one * (float)((t + kCus - 1) / kCus)
+                                  : (t <= kCus ? c.one : c.two * (float)((t + 2 * kCus - 1) / (2 * kCus)));
+    if (best_tiles == 0 || f < least) {
+      least = f;
+      best.kind = c.kind;
+      best_tiles = t;
+    }
+  };
+  if (wide)
+    for (const TileCost& c : wide_t) consider(c);
+  else
+    for (const TileCost& c : narrow_t) consider(c);
+  // Few tiles and a long K: split it so that the chip fills, at least 8 blocks each, where that saves more than the second
+  // launch takes (131 x 1000 x 7168, 48 tiles: 14.7 us whole, 12.1 in two, 11.9 in five).
+  const int KB = K / 128;
+  int s = (int)(kCus / best_tiles);
+  if (s > KB / 8) s = KB / 8;
+  if (s > 8) s = 8;
+  if (s > 1 && (float)KB * least * (1.0f - 1.0f / (float)s) > 5.0f) best.splits = s;
+  return best;
+}
+
 template <bool WIDE, bool GRAN1>
 hipError_t launch_dense(DenseArgs a, hipStream_t s) {
-  a.splits = 1;
-  if (a.M <= 16) return launch_stream<WIDE, GRAN1, V1>(a, s);
-  if (a.M <= 32 && MS >= 32) return launch_stream<WIDE, GRAN1, V2>(a, s);
-  if (a.M <= 64 && MS >= 64) return launch_stream<WIDE, GRAN1, V4>(a, s);
-  a.splits = SP;
-  if constexpr (WIDE) return launch_tile<WIDE, GRAN1, TW>(a, s);
-  else return launch_tile<WIDE, GRAN1, TN>(a, s);
+  const Plan p = plan_dense(a.M, a.N, a.K, WIDE);
+  a.splits = p.splits;
+  // streaming workgroups: 16 columns and 8 waves while they fit the chip once, else 32 columns and 4 waves (7168 x 2048,
+  // 16 rows: 8.0 and 5.9 us)
+  const bool many = (a.N + 15) / 16 > kCus;
+  switch (p.kind) {
+    case kStream16:
+      return many ? launch_stream<WIDE, GRAN1, 1, 2, 4, 4>(a, s) : launch_stream<WIDE, GRAN1, 1, 1, 8, 3>(a, s);
+    case kStream32:
+      return many ? launch_stream<WIDE, GRAN1, 2, 2, 4, 4>(a, s) : launch_stream<WIDE, GRAN1, 2, 1, 8, 3>(a, s);
+    case kStream64:
+      return many ? launch_stream<WIDE, GRAN1, 4, 2, 4, 2>(a, s) : launch_stream<WIDE, GRAN1, 4, 1, 4, 3>(a, s);
+    case k64x64: return launch_small<WIDE, GRAN1, 2, 2, 2, 2>(a, s);
+    case k64x128: return launch_small<WIDE, GRAN1, 2, 2, 2, 4>(a, s);
+    case k128x128: return launch_small<WIDE, GRAN1, 4, 2, 2, 4>(a, s);
+    default:  // the largest of either list
+      if constexpr (WIDE) return launch_big<WIDE, GRAN1, 4, 4, 2, 2>(a, s);
+      else return launch_big<WIDE, GRAN1, 8, 4, 2, 4>(a, s);
+  }
 }
 
 }  // namespace
 
-int64_t dense_workspace_bytes(int M, int N, int K) { return SP > 1 ? 4ll * SP * M * ((N + 3) & ~3) : 0; }
+int64_t dense_workspace_bytes(int M, int N, int K) {
+  // either output type may be asked for: the larger need
+  const int a = plan_dense(M, N, K, false).splits, b = plan_dense(M, N, K, true).splits, s = a > b ? a : b;
+  return s > 1 ? 4ll * s * M * ((N + 3) & ~3) : 0;
+}
 
 hipError_t launch_gemm_dense(const DenseArgs& a, hipStream_t s) {
   const bool g1 = a.gran_n == 1;
