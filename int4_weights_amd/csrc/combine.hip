@@ -111,24 +111,39 @@ __device__ __forceinline__ v4i pack8(const float (&f)[8]) {
   return o;
 }
 
-// dY of a row named by `cnt` slots, the lowest of them `own`: the whole workgroup sums them in route order.
-__device__ inline void shared_row(const CombineBwdArgs& a, int p, int64_t own, int cnt) {
+// dY of a row named by `cnt` slots, the lowest of them `own`: the whole workgroup sums them in route order, searching
+// the table NT entries at a time (a thread searching alone: R / 2 dependent loads per row, 10 s where 2^20 routes name
+// half as many rows).
+template <int NT>
+__device__ __forceinline__ void shared_row(const CombineBwdArgs& a, int p, int own, int cnt) {
+  __shared__ uint64_t s_hit[NT / 64];
   const int64_t R = (int64_t)a.T * a.k;
-  for (int c = threadIdx.x; c < a.N / 8; c += blockDim.x) {
+  const int chunks = a.N / 8;
+  for (int c0 = 0; c0 < chunks; c0 += NT) {
+    const int c = c0 + (int)threadIdx.x;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     int left = cnt;
-    for (int64_t i = own; i < R && left > 0; ++i) {
-      if (a.oi[i] != p) continue;
-      --left;
-      float dz[8];
-      unpack8(*(const v4i*)(a.dZ + i / a.k * a.N + 8 * c), dz);
-      const float w = a.w[i];
+    for (int64_t i0 = own; i0 < R && left > 0; i0 += NT) {
+      const bool hit = i0 + threadIdx.x < R && a.oi[i0 + threadIdx.x] == p;
+      const uint64_t m = __ballot(hit);
+      __syncthreads();  // the previous entries' hits are used up
+      if ((threadIdx.x & 63) == 0) s_hit[threadIdx.x >> 6] = m;
+      __syncthreads();
+      for (int v = 0; v < NT / 64; ++v)
+        for (uint64_t h = s_hit[v]; h; h &= h - 1) {
+          const int64_t i = i0 + 64 * v + __builtin_ctzll(h);
+          --left;
+          if (c >= chunks) continue;
+          float dz[8];
+          unpack8(*(const v4i*)(a.dZ + i / a.k * a.N + 8 * c), dz);
+          const float w = a.w[i];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = __builtin_fmaf(w, dz[j], acc[j]);
+          for (int j = 0; j < 8; ++j) acc[j] = __builtin_fmaf(w, dz[j], acc[j]);
+        }
     }
-    *(v4i*)(a.dY + (int64_t)p * a.N + 8 * c) = pack8(acc);
+    if (c < chunks) *(v4i*)(a.dY + (int64_t)p * a.N + 8 * c) = pack8(acc);
   }
 }
 
@@ -146,7 +161,7 @@ __global__ __launch_bounds__(NT) void combine_bwd_kernel(const CombineBwdArgs a)
   const bool scan = a.dY && !a.who;
   const int batches = (a.k + B - 1) / B;
   const int64_t total = (int64_t)a.T * batches;
-  for (int64_t q = blockIdx.x; q < total; q += gridDim.x) {
+  for (int64_t q = blockIdx.x; q < total; q += gridDim.x) {  // uniform in the workgroup, as all that decides shared_row is
     const int t = (int)(q / batches), r0 = (int)(q % batches) * B, i0 = t * a.k + r0;
     int p[B];
     float w[B];
@@ -230,7 +245,7 @@ __global__ __launch_bounds__(NT) void combine_bwd_kernel(const CombineBwdArgs a)
         if (pj < 0 || pj >= a.y_rows) continue;
         const int cnt = a.who ? a.who[pj].x : s_cnt[j];
         const int own = a.who ? a.who[pj].y : s_own[j];
-        if (cnt > 1 && own == i0 + j) shared_row(a, pj, own, cnt);
+        if (cnt > 1 && own == i0 + j) shared_row<NT>(a, pj, own, cnt);
       }
     }
     if (a.dw) {

@@ -81,6 +81,32 @@ def test_rows_named_several_times(T, k, N, rows):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("T,k,N,rows", [(30, 8, 8216, 200), (1030, 4, 2072, 3000)])
+def test_rows_named_several_times_wide(T, k, N, rows):
+    """Rows wider than one turn of a workgroup's threads."""
+    require_gpu()
+    dz, y, oi, w = _inputs(T, k, N, rows, T, unique=False)
+    _check(dz, y, oi.to(DEV), w)
+
+
+def test_many_rows_named_twice():
+    """Half a million routes, every row named by two of them far apart."""
+    require_gpu()
+    T, k, N = 65536, 8, 8
+    g = torch.Generator().manual_seed(1)
+    rows = T * k // 2
+    oi = torch.cat([torch.randperm(rows, generator=g), torch.randperm(rows, generator=g)]).view(T, k)
+    dz = torch.randn(T, N, generator=g).to(torch.bfloat16).to(DEV)
+    w = torch.rand(T, k, generator=g).to(DEV)
+    y = torch.zeros(rows, N, dtype=torch.bfloat16, device=DEV)
+    dY, _ = _run(dz, y, oi.to(torch.int32).to(DEV), w)
+    v = (w.double()[:, :, None] * dz.double()[:, None]).view(-1, N)
+    at = oi.view(-1).to(DEV)
+    ref = torch.zeros(rows, N, dtype=torch.float64, device=DEV).index_add_(0, at, v)
+    mag = torch.zeros_like(ref).index_add_(0, at, v.abs())
+    assert ((dY.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 3 * U * 1.01 * mag + 1e-38).all()
+
+
 @pytest.mark.parametrize("T", [50, 600])
 def test_outputs_alone(T):
     require_gpu()
