@@ -608,8 +608,9 @@ moe_status moe_router_topk_bwd(const void* logits, int logits_type, int64_t logi
  *   (moe_quant_act), W the transposed weight.  Weight gradient [N, K]: A and W
  *   the output gradient and the input as moe_quant_act_t writes them, gran_n 1.
  *   Requires K % 128 == 0, lda and ldw multiples of 16, >= K and < 2^23; A and W
- *   16-byte aligned, D aligned to its type; M and N < 2^30.  M == 0 is a no-op.
- *   D must not overlap A, W or the scales.
+ *   16-byte aligned, D aligned to its type; M and N <= 2^28, and
+ *   ceil(M/64) * ceil(N/64) < 2^24.  M == 0 is a no-op.
+ *   D must not overlap A, W or the scales, nor C in part.
  *   workspace: at least moe_gemm_fp8_workspace_bytes(M, N, K) bytes, 16-byte
  *   aligned (may be NULL when that is 0; it is not 0 only where few output tiles
  *   make it pay to split K); calls that overlap in time must not share it.
@@ -627,8 +628,8 @@ moe_status moe_gemm_fp8(const uint8_t* A, int64_t lda, const float* SFA,
  *   qt [K, Mp] E4M3FN codes and sft [K, Mp/128] fp32: row k of qt is column k of
  *   x, quantised by the rule of moe_quant_act (power-of-two scale per 128
  *   consecutive m), rows of x past M counting as zeros.
- *   Requires K % 8 == 0, ldx % 8 == 0 and >= K, x and qt 16-byte aligned, sft
- *   4-byte aligned; the outputs must not overlap x.  M == 0 is a no-op. */
+ *   Requires K % 8 == 0, ldx % 8 == 0 and >= K, ceil(M/128) * ceil(K/64) < 2^24,
+ *   x and qt 16-byte aligned, sft 4-byte aligned; the outputs must not overlap x.  M == 0 is a no-op. */
 moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx,
                            uint8_t* qt, float* sft, void* stream);
 

@@ -753,8 +753,15 @@ moe_status moe_router_topk_bwd(const void* logits, int logits_type, int64_t logi
   return hip_status(launch_router_topk_bwd(a, (hipStream_t)stream), fn);
 }
 
+// A launch has fewer than 2^32 threads: tiles of 64x64 or more have 256 threads, or 512 for twice the area; few rows (up
+// to 64) take 256 threads per 32 columns.
+static bool dense_size_ok(int M, int N) {
+  return M >= 0 && M <= (1 << 28) && N >= 1 && N <= (1 << 28) &&
+         (int64_t)((M + 63) / 64) * ((N + 63) / 64) < (1 << 24);
+}
+
 int64_t moe_gemm_fp8_workspace_bytes(int M, int N, int K) {
-  if (M < 0 || M >= (1 << 30) || N < 1 || N >= (1 << 30) || K < 1 || K % 128) return -1;
+  if (!dense_size_ok(M, N) || K < 1 || K % 128) return -1;
   return dense_workspace_bytes(M, N, K);
 }
 
@@ -765,6 +772,7 @@ moe_status moe_gemm_fp8(const uint8_t* A, int64_t lda, const float* SFA, const u
   const char* fn = "moe_gemm_fp8";
   if (M < 0 || M >= (1 << 30) || N < 1 || N >= (1 << 30) || K < 1)
     return fail(MOE_ERR_SHAPE, "%s: M=%d N=%d K=%d", fn, M, N, K);
+  if (!dense_size_ok(M, N)) return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d x N=%d is too large", fn, M, N);
   if (K % 128) return fail(MOE_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 128", fn, K);
   if (gran_n != 1 && gran_n != 128) return fail(MOE_ERR_UNSUPPORTED, "%s: gran_n=%d must be 1 or 128", fn, gran_n);
   if (out_type != MOE_F32 && out_type != MOE_BF16)
@@ -774,9 +782,6 @@ moe_status moe_gemm_fp8(const uint8_t* A, int64_t lda, const float* SFA, const u
     return fail(MOE_ERR_SHAPE, "%s: a row stride is shorter than its row", fn);
   if (lda >= (1 << 23) || ldw >= (1 << 23))
     return fail(MOE_ERR_UNSUPPORTED, "%s: lda and ldw must be below 2^23 bytes", fn);
-  // tiles are numbered in 32 bits
-  if (((int64_t)(M + 15) / 16) * ((N + 15) / 16) > 0x7fffffff)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d x N=%d is too large", fn, M, N);
   if (M == 0) return MOE_OK;
   if (!A || !SFA || !W || !SFW || !D) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
   if (!aligned(A, 16) || !aligned(W, 16) || lda % 16 || ldw % 16 || !aligned(SFA, 4) || !aligned(SFW, 4) ||
@@ -812,8 +817,8 @@ moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx, uin
   const char* fn = "moe_quant_act_t";
   if (M < 0 || K <= 0 || ldx < K) return fail(MOE_ERR_SHAPE, "%s: M=%lld K=%d ldx=%lld", fn, (long long)M, K, (long long)ldx);
   if (K % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 8", fn, K);
-  // one workgroup per 128 rows x 64 columns
-  if (M > (1ll << 40) || ((M + 127) / 128) * ((K + 63) / 64) > 0x7fffffff)
+  // one workgroup of 256 threads per 128 rows x 64 columns, fewer than 2^32 threads in all
+  if (M > (1ll << 40) || ((M + 127) / 128) * ((K + 63) / 64) >= (1 << 24))
     return fail(MOE_ERR_UNSUPPORTED, "%s: M=%lld x K=%d is too large", fn, (long long)M, K);
   if (M == 0) return MOE_OK;
   if (!x || !qt || !sft) return fail(MOE_ERR_NULL, "%s: null pointer", fn);

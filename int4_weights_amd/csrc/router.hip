@@ -425,8 +425,8 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
     b[j] = 0.0f;
     if constexpr (BIAS) b[j] = a.bias[min(le.base + j, a.E - 1)];
   }
-  for (int t = blockIdx.x * 4 + uniform(threadIdx.x >> 6); t < a.T; t += gridDim.x * 4) {
-    const T* row = (const T*)a.logits + (int64_t)t * a.ld;
+  for (int64_t t = blockIdx.x * 4 + uniform(threadIdx.x >> 6); t < a.T; t += gridDim.x * 4) {
+    const T* row = (const T*)a.logits + t * a.ld;
     float x[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) x[j] = load_logit(row + min(le.base + j, a.E - 1));
@@ -553,8 +553,8 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
     const bool on = p.id >= 0;
     const float w = slot_weight(a.score, a.norm, a.scale, on, p.x, row_m, row_den);
     if (lane < a.k) {
-      a.ids[(int64_t)t * a.k + lane] = p.id;
-      a.w[(int64_t)t * a.k + lane] = w;
+      a.ids[t * a.k + lane] = p.id;
+      a.w[t * a.k + lane] = w;
     }
   }
 }
@@ -573,16 +573,16 @@ __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const RouterBwdArg
   float* srow = s_row[wv];
   const bool dense = a.score == 0 && !a.norm;
   const int base = lane * VPL;
-  for (int t = blockIdx.x * 4 + wv; t < a.T; t += gridDim.x * 4) {
-    const T* row = (const T*)a.logits + (int64_t)t * a.ld;
+  for (int64_t t = blockIdx.x * 4 + wv; t < a.T; t += gridDim.x * 4) {
+    const T* row = (const T*)a.logits + t * a.ld;
     int id = -1;
     float g = 0.0f, x = ninf;
     if (lane < a.k) {
-      id = a.ids[(int64_t)t * a.k + lane];
+      id = a.ids[t * a.k + lane];
       if (id < 0 || id >= a.E) id = -1;
       if (id >= 0) {
         x = load_logit(row + id);
-        g = a.dw[(int64_t)t * a.k + lane];
+        g = a.dw[t * a.k + lane];
       }
     }
     const bool on = x > ninf;  // an empty slot, or an expert that was not available: no gradient
@@ -635,7 +635,7 @@ __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const RouterBwdArg
     wave_fence();
     if (first) srow[id] = sum;
     wave_fence();
-    T* out = (T*)a.dlogits + (int64_t)t * a.ldd;
+    T* out = (T*)a.dlogits + t * a.ldd;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       float v = srow[base + j];

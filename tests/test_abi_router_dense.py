@@ -92,6 +92,18 @@ def test_dense_product_refusals(lib, kw, status):
                             None) == status
 
 
+@pytest.mark.parametrize("M,N", [((1 << 28) + 1, 1), (1, (1 << 28) + 1), (1 << 28, 256), (1 << 17, 1 << 19)])
+def test_dense_product_too_large_for_one_launch(lib, M, N):
+    assert lib.moe_gemm_fp8(_p(P), 128, _p(P), _p(P), 128, _p(P), 128, _p(P), 1, N, None, 0, M, N, 128, None, 0,
+                            None) == UNSUPPORTED
+    assert moe.moe_gemm_fp8_workspace_bytes(M, N, 128) == -1
+
+
+@pytest.mark.parametrize("M,K", [(1 << 31, 8), (1 << 20, 1 << 17)])
+def test_transposing_quantiser_too_large_for_one_launch(lib, M, K):
+    assert lib.moe_quant_act_t(_p(P), M, K, K, _p(P), _p(P), None) == UNSUPPORTED
+
+
 def test_dense_product_workspace(lib):
     assert moe.moe_gemm_fp8_workspace_bytes(4, 4, 100) == -1
     assert moe.moe_gemm_fp8_workspace_bytes(-1, 4, 128) == -1
