@@ -115,6 +115,20 @@ class MoeFP8Layer:
         L.moe_unpermute_combine(D, oi, topk_weights, Z)
         return Z
 
+    def combine_backward(self, dZ, topk_weights, dD, dweights, D=None, workspace=None):
+        """Gradient of combine() with the routing of the last route()/quant_route(): dZ [T, N] -> dD, the gradient of the
+        packed rows D (default: this layer's GEMM output) that a token was routed to (the padding's are not written),
+        and dweights [T, topk].  workspace: moe_unpermute_combine_bwd_workspace_bytes(T, topk, rows of D) bytes; without
+        one, a call that needs it allocates it."""
+        T = dZ.shape[0]
+        D = self.D if D is None else D
+        if workspace is None:
+            need = L.moe_unpermute_combine_bwd_workspace_bytes(T, self.topk, D.shape[0])
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dZ.device)
+        L.moe_unpermute_combine_bwd(dZ, D, self.output_index[:T], topk_weights, dD, dweights, workspace=workspace)
+        return dD, dweights
+
     def forward(self, x, topk_ids, topk_weights, fused_quant=False):
         """fused_quant: quantise while packing (quant_route) instead of quant() then route()."""
         if fused_quant:
@@ -179,3 +193,88 @@ class MoeInt4Layer:
         self.route(x, topk_ids)
         self.gemm()
         return self.combine(topk_weights)
+
+
+class MoeRouter:
+    """The router before a layer: gate logits -> (topk_ids, topk_weights), with the gradient back to the logits.
+
+    Holds the balance bias and the output buffers for up to max_tokens tokens; a call allocates nothing."""
+
+    def __init__(self, E: int, topk: int, max_tokens: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                 n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                 scale: float = 1.0, device="cuda"):
+        self.E, self.topk, self.bias = E, topk, bias
+        self.score, self.renormalize, self.scale = score, renormalize, scale
+        self.groups = dict(n_group=n_group, topk_group=topk_group, group_top=group_top)
+        self.topk_ids = torch.empty(max_tokens, topk, dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty(max_tokens, topk, dtype=torch.float32, device=device)
+
+    def forward(self, logits):
+        """logits float32 or bf16 [T, E] -> this router's topk_ids and topk_weights, [T, topk] each."""
+        T = logits.shape[0]
+        ids, w = self.topk_ids[:T], self.topk_weights[:T]
+        L.moe_router_topk(logits, ids, w, score=self.score, bias=self.bias, renormalize=self.renormalize,
+                          scale=self.scale, **self.groups)
+        return ids, w
+
+    def backward(self, logits, topk_ids, dweights, dlogits):
+        """d logits of the weights that forward(logits) gave for topk_ids."""
+        L.moe_router_topk_bwd(logits, topk_ids, dweights, dlogits, score=self.score, renormalize=self.renormalize,
+                              scale=self.scale)
+        return dlogits
+
+
+class DenseFP8Linear:
+    """y = x W^T for one weight matrix that every token uses (a shared expert, a projection), block-scaled FP8.
+
+    w_codes uint8 [N, K] and sfw float32 [ceil(N/128), K/128], any fp32 scales; for grad_input wt_codes [K, N] and
+    sfwt [ceil(K/128), N/128] hold the transposed weight (N % 128 == 0).  The activations' codes have buffers for
+    max_tokens tokens, so calls of one object that overlap in time must not run on two streams.  A product that splits
+    K (few output tiles) and grad_weight take their scratch from torch's allocator, which a graph's capture keeps."""
+
+    def __init__(self, w_codes: torch.Tensor, sfw: torch.Tensor, max_tokens: int, wt_codes: torch.Tensor | None = None,
+                 sfwt: torch.Tensor | None = None):
+        self.N, self.K = w_codes.shape
+        self.w, self.sfw, self.wt, self.sfwt = w_codes, sfw, wt_codes, sfwt
+        dev = w_codes.device
+        wide = self.K if wt_codes is None else max(self.K, self.N)
+        self.max_tokens = max_tokens
+        self.q = torch.empty(max_tokens * wide, dtype=torch.uint8, device=dev)
+        self.sf = torch.empty(max_tokens * (wide // 128), dtype=torch.float32, device=dev)
+
+    def _gemm(self, A, SFA, W, SFW, out, C=None):
+        need = L.moe_gemm_fp8_workspace_bytes(A.shape[0], W.shape[0], A.shape[1])
+        ws = torch.empty(need, dtype=torch.uint8, device=A.device) if need > 0 else None
+        L.moe_gemm_fp8(A, SFA, W, SFW, out, C=C, workspace=ws)
+        return out
+
+    def _product(self, x, w, sfw, out):
+        T, K = x.shape
+        if T > self.max_tokens or K != w.shape[1]:
+            raise ValueError(f"x is {tuple(x.shape)}, needs [at most {self.max_tokens}, {w.shape[1]}]")
+        q, sf = self.q[:T * K].view(T, K), self.sf[:T * (K // 128)].view(T, K // 128)
+        L.moe_quant_act(x, q, sf)
+        return self._gemm(q, sf, w, sfw, out)
+
+    def forward(self, x, out):
+        """x bf16 [T, K] -> out bf16 or float32 [T, N]."""
+        return self._product(x, self.w, self.sfw, out)
+
+    def grad_input(self, dy, dx):
+        """dy bf16 [T, N] -> dx bf16 or float32 [T, K]."""
+        if self.wt is None:
+            raise ValueError("grad_input needs the transposed weight (wt_codes, sfwt)")
+        return self._product(dy, self.wt, self.sfwt, dx)
+
+    def grad_weight(self, dy, x, dw, accumulate=True):
+        """dw float32 [N, K] (+)= dy^T x of dy bf16 [T, N] and x bf16 [T, K], both quantised along the tokens."""
+        mb = (x.shape[0] + 127) // 128
+        if mb == 0:
+            return dw if accumulate else dw.zero_()
+        qs = []
+        for t in (dy, x):
+            q = torch.empty(t.shape[1], 128 * mb, dtype=torch.uint8, device=t.device)
+            sf = torch.empty(t.shape[1], mb, dtype=torch.float32, device=t.device)
+            L.moe_quant_act_t(t, q, sf)
+            qs += [q, sf]
+        return self._gemm(*qs, dw, C=dw if accumulate else None)

@@ -79,7 +79,8 @@ def _check(d, a, sa, w, sw, gran, c=None):
 
 SIZES = [(1, 1, 128), (1, 64, 256), (1, 4096, 1024), (2, 130, 384), (7, 33, 128), (16, 16, 2048), (17, 257, 640),
          (31, 1000, 512), (33, 128, 128), (64, 320, 1152), (65, 127, 256), (100, 96, 7168), (129, 129, 896),
-         (200, 640, 384), (255, 513, 128), (257, 250, 256), (300, 1100, 640), (512, 384, 512), (777, 259, 384)]
+         (200, 640, 384), (255, 513, 128), (257, 250, 256), (300, 1100, 640), (512, 384, 512), (777, 259, 384), (40, 5000, 384), (5, 4200, 1280),
+         (20, 4500, 640), (66, 300, 4096), (130, 64, 32768), (1100, 3000, 384), (1030, 4100, 256), (2100, 4500, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -142,6 +143,23 @@ def test_powers_of_two_match_the_grouped_product():
     a, w = q.cpu().numpy(), wq[0].cpu().numpy()
     for d in (D, G):
         _check(d, a, sf.cpu().numpy(), w, ws[0].cpu().numpy(), 128)
+
+
+@pytest.mark.parametrize("M", [10, 40, 140, 600])
+def test_special_values_bf16(M):
+    """The same in bf16 output, on every kernel's path."""
+    require_gpu()
+    N, K = 1100, 512
+    a, sa, w, sw = _operands(M, N, K, 128, M)
+    sa, sw = np.abs(sa) + 0.1, np.abs(sw) + 0.1
+    clean = _run(a, sa, w, sw, torch.bfloat16)
+    a2, w2 = a.copy(), w.copy()
+    a2[M - 3, 129] = 0xFF
+    w2[1050, 511] = 0x7F
+    d = _run(a2, sa, w2, sw, torch.bfloat16)
+    rows, cols = torch.arange(M) != M - 3, torch.arange(N) != 1050
+    assert torch.isnan(d[M - 3]).all() and torch.isnan(d[:, 1050]).all()
+    assert torch.equal(d[rows][:, cols], clean[rows][:, cols])
 
 
 def test_special_values():
