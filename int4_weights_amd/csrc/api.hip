@@ -646,8 +646,8 @@ moe_status moe_unpermute_combine_bwd(const uint16_t* dZ, const uint16_t* Y, int6
     return fail(MOE_ERR_SHAPE, "%s: T=%d k=%d N=%d y_rows=%lld", fn, T, k, N, (long long)y_rows);
   if ((int64_t)T * k > 0x7fffffff) return fail(MOE_ERR_SHAPE, "%s: T*k too large", fn);
   if (N % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d must be a multiple of 8", fn, N);
-  if (!dY && !dweights) return fail(MOE_ERR_NULL, "%s: dY and dweights are both null", fn);
   if (T == 0) return MOE_OK;
+  if (!dY && !dweights) return fail(MOE_ERR_NULL, "%s: dY and dweights are both null", fn);
   if (!dZ || !output_index || (dY && !topk_weights) || (dweights && !Y && y_rows > 0))
     return fail(MOE_ERR_NULL, "%s: null pointer", fn);
   if (!aligned(dZ, 16) || !aligned(Y, 16) || !aligned(dY, 16) || !aligned(output_index, 4) ||

@@ -60,6 +60,7 @@ def test_router_gradient_refusals(lib, kw, status):
     (dict(dY=None, dw=None), NULL), (dict(dZ=None), NULL), (dict(oi=None), NULL), (dict(w=None), NULL),
     (dict(Y=None), NULL), (dict(dZ=P + 8), ALIGN), (dict(dY=P + 8), ALIGN), (dict(T=1024, ws=None), WORKSPACE),
     (dict(T=1024, wsb=8 * 10000 - 1), WORKSPACE), (dict(T=1024, ws=P + 4), WORKSPACE), (dict(T=0), OK),
+    (dict(T=0, y_rows=0, dZ=None, Y=None, oi=None, w=None, dY=None, dw=None, ws=None), OK),  # all empty
 ])
 def test_combine_gradient_refusals(lib, kw, status):
     a = dict(dZ=P, Y=P, y_rows=10000, oi=P, w=P, T=512, k=8, N=64, dY=P, dw=P, ws=P, wsb=8 * 10000)
