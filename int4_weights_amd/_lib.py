@@ -22,6 +22,8 @@ LAYOUT_MASKED = 1
 WEIGHTS_PACKED = 0x10  # flag for moe_grouped_gemm_fp8's layout: W in moe_pack_weight_fp8 order
 F32, BF16 = 0, 1
 SCORES = {"softmax": 0, "sigmoid": 1}
+_FLOATS = (torch.float32, torch.bfloat16)
+_CODES = (torch.uint8,)
 DEV_ID_RANGE = 1
 DEV_CAPACITY = 2
 
@@ -139,31 +141,65 @@ def _dev(t, name, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
 
 
-def _rows(t, name, dtypes):
-    """A 2-D GPU tensor whose rows are contiguous; returns its row stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    rows, cols = t.shape
+def _whole(fn, dev, t, name, dtype, shape) -> int:
+    """The pointer of a contiguous tensor of this type and shape on GPU dev.  (One test of everything: these calls are
+    short enough on the GPU for the host's checks to show.)"""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _dev(t, name, dtype, len(shape))
+        if t.shape != shape:
+            raise ValueError(f"{fn}: {name} is {tuple(t.shape)}, needs {tuple(shape)}")
+        raise ValueError(f"{fn}: {name} is on {t.device}, the call on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _rows(fn, dev, t, name, dtypes, shape) -> int:
+    """The row stride in elements of a 2-D tensor of this shape on GPU dev whose rows are contiguous."""
+    if t.get_device() != dev or t.shape != shape or t.dtype not in dtypes:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{fn}: {name} is {tuple(t.shape)}, needs {tuple(shape)}")
+        raise ValueError(f"{fn}: {name} is on {t.device}, the call on cuda:{dev}")
+    rows, cols = shape
     row_stride, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
     return row_stride if rows > 1 else max(cols, 1)
 
 
-def _one_device(fn, stream, *tensors):
-    """The tensors lie on the current device, and so does the stream: a kernel is launched there.  Returns the stream's
-    handle."""
-    dev = torch._C._cuda_getDevice()
-    if stream is not None and stream.device.index != dev:
+def _shape2(t, name):
+    """(rows, columns, GPU) of a 2-D GPU tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    rows, cols = t.shape
+    return rows, cols, dev
+
+
+def _queue(fn, dev, stream):
+    """Handle of the stream (default: the current one) that a call on tensors of GPU dev goes to: a kernel is launched on
+    the current device, so both have to be there."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{fn}: the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
         raise ValueError(f"{fn}: the stream is not on the current device")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{fn}: a tensor is on {t.device}, the call on cuda:{dev}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return stream.cuda_stream
+
+
+def _scratch(fn, dev, workspace):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _dev(workspace, "workspace")
+        raise ValueError(f"{fn}: workspace is on {workspace.device}, the call on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _row_bytes(t) -> int:
@@ -496,25 +532,24 @@ def moe_unpermute_combine_bwd_workspace_bytes(T: int, k: int, y_rows: int) -> in
 def moe_unpermute_combine_bwd(dZ, Y, output_index, topk_weights, dY, dweights, workspace=None, stream=None):
     """dZ bf16 [T, N] -> dY bf16 [y_rows, N] (rows that a slot names) and dweights float32 [T, k].  Either output may
     be None: without dY topk_weights may be None, without dweights Y may be None."""
-    _dev(dZ, "dZ", torch.bfloat16, 2), _dev(Y, "Y", torch.bfloat16, 2)
-    _dev(output_index, "output_index", torch.int32, 2), _dev(topk_weights, "topk_weights", torch.float32, 2)
-    _dev(dY, "dY", torch.bfloat16, 2), _dev(dweights, "dweights", torch.float32, 2), _dev(workspace, "workspace")
-    T, N = dZ.shape
-    k = output_index.shape[1]
+    fn = "moe_unpermute_combine_bwd"
     if dY is None and dweights is None:
-        raise ValueError("moe_unpermute_combine_bwd: dY and dweights are both None")
+        raise ValueError(f"{fn}: dY and dweights are both None")
     if (dweights is not None and Y is None) or (dY is not None and topk_weights is None):
-        raise ValueError("moe_unpermute_combine_bwd: dweights needs Y, dY needs topk_weights")
-    y_rows = (Y if Y is not None else dY).shape[0]
-    for name, t, shape in (("output_index", output_index, (T, k)), ("topk_weights", topk_weights, (T, k)),
-                           ("dweights", dweights, (T, k)), ("Y", Y, (y_rows, N)), ("dY", dY, (y_rows, N))):
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"moe_unpermute_combine_bwd: {name} is {tuple(t.shape)}, needs {shape}")
-    hs = _one_device("moe_unpermute_combine_bwd", stream, dZ, Y, output_index, topk_weights, dY, dweights, workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().moe_unpermute_combine_bwd(_ptr(dZ), _ptr(Y), y_rows, _ptr(output_index), _ptr(topk_weights), T, k, N,
-                                            _ptr(dY), _ptr(dweights), _ptr(workspace), ws_bytes, hs),
-           "moe_unpermute_combine_bwd")
+        raise ValueError(f"{fn}: dweights needs Y, dY needs topk_weights")
+    T, N, dev = _shape2(dZ, "dZ")
+    k = output_index.shape[-1]
+    y_rows = (dY if Y is None else Y).shape[0]
+    slots, rows = (T, k), (y_rows, N)
+    dz = _whole(fn, dev, dZ, "dZ", torch.bfloat16, (T, N))
+    y = None if Y is None else _whole(fn, dev, Y, "Y", torch.bfloat16, rows)
+    oi = _whole(fn, dev, output_index, "output_index", torch.int32, slots)
+    w = None if topk_weights is None else _whole(fn, dev, topk_weights, "topk_weights", torch.float32, slots)
+    dy = None if dY is None else _whole(fn, dev, dY, "dY", torch.bfloat16, rows)
+    dw = None if dweights is None else _whole(fn, dev, dweights, "dweights", torch.float32, slots)
+    ws, ws_bytes = _scratch(fn, dev, workspace)
+    _check(load().moe_unpermute_combine_bwd(dz, y, y_rows, oi, w, T, k, N, dy, dw, ws, ws_bytes,
+                                            _queue(fn, dev, stream)), fn)
 
 
 def _score(fn, score):
@@ -529,36 +564,30 @@ def moe_router_topk(logits, topk_ids, topk_weights, score: str = "softmax", bias
     """logits float32 or bf16 [T, E] (rows may be strided) -> topk_ids int32 and topk_weights float32 [T, k]; bias
     float32 [E] (in the choice only).  See include/moe.h."""
     fn = "moe_router_topk"
-    ld = _rows(logits, "logits", (torch.float32, torch.bfloat16))
-    _dev(topk_ids, "topk_ids", torch.int32, 2), _dev(topk_weights, "topk_weights", torch.float32, 2)
-    _dev(bias, "bias", torch.float32, 1)
-    T, E = logits.shape
-    k = topk_ids.shape[1]
-    if topk_ids.shape[0] != T or tuple(topk_weights.shape) != (T, k) or (bias is not None and bias.shape[0] != E):
-        raise ValueError(f"{fn}: shape mismatch")
-    sc = _score(fn, score)
-    hs = _one_device(fn, stream, logits, topk_ids, topk_weights, bias)
-    _check(load().moe_router_topk(_ptr(logits), BF16 if logits.dtype == torch.bfloat16 else F32, ld, _ptr(bias), T, E,
-                                  k, sc, n_group, topk_group, group_top, int(renormalize), scale, _ptr(topk_ids),
-                                  _ptr(topk_weights), hs), fn)
+    T, E, dev = _shape2(logits, "logits")
+    k = topk_ids.shape[-1]
+    ld = _rows(fn, dev, logits, "logits", _FLOATS, (T, E))
+    ids = _whole(fn, dev, topk_ids, "topk_ids", torch.int32, (T, k))
+    w = _whole(fn, dev, topk_weights, "topk_weights", torch.float32, (T, k))
+    b = None if bias is None else _whole(fn, dev, bias, "bias", torch.float32, (E,))
+    _check(load().moe_router_topk(logits.data_ptr(), BF16 if logits.dtype is torch.bfloat16 else F32, ld, b, T, E, k,
+                                  _score(fn, score), n_group, topk_group, group_top, int(renormalize), scale, ids, w,
+                                  _queue(fn, dev, stream)), fn)
 
 
 def moe_router_topk_bwd(logits, topk_ids, dweights, dlogits, score: str = "softmax", renormalize: bool = True,
                         scale: float = 1.0, stream=None):
     """dweights float32 [T, k] -> dlogits [T, E], of logits' type (rows may be strided), for the choice topk_ids."""
     fn = "moe_router_topk_bwd"
-    ld = _rows(logits, "logits", (torch.float32, torch.bfloat16))
-    ldd = _rows(dlogits, "dlogits", (logits.dtype,))
-    _dev(topk_ids, "topk_ids", torch.int32, 2), _dev(dweights, "dweights", torch.float32, 2)
-    T, E = logits.shape
-    k = topk_ids.shape[1]
-    if tuple(dlogits.shape) != (T, E) or topk_ids.shape[0] != T or tuple(dweights.shape) != (T, k):
-        raise ValueError(f"{fn}: shape mismatch")
-    sc = _score(fn, score)
-    hs = _one_device(fn, stream, logits, topk_ids, dweights, dlogits)
-    _check(load().moe_router_topk_bwd(_ptr(logits), BF16 if logits.dtype == torch.bfloat16 else F32, ld,
-                                      _ptr(topk_ids), _ptr(dweights), T, E, k, sc, int(renormalize), scale,
-                                      _ptr(dlogits), ldd, hs), fn)
+    T, E, dev = _shape2(logits, "logits")
+    k = topk_ids.shape[-1]
+    ld = _rows(fn, dev, logits, "logits", _FLOATS, (T, E))
+    ldd = _rows(fn, dev, dlogits, "dlogits", (logits.dtype,), (T, E))
+    ids = _whole(fn, dev, topk_ids, "topk_ids", torch.int32, (T, k))
+    dw = _whole(fn, dev, dweights, "dweights", torch.float32, (T, k))
+    _check(load().moe_router_topk_bwd(logits.data_ptr(), BF16 if logits.dtype is torch.bfloat16 else F32, ld, ids, dw,
+                                      T, E, k, _score(fn, score), int(renormalize), scale, dlogits.data_ptr(), ldd,
+                                      _queue(fn, dev, stream)), fn)
 
 
 def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -570,39 +599,31 @@ def moe_gemm_fp8(A, SFA, W, SFW, D, C=None, workspace=None, stream=None):
     [ceil(N/128), K/128] or [N, K/128]; D bf16 or float32 [M, N], C float32 [M, N] (float32 D only; may be D).  Rows of A, W, D
     and C may be strided.  workspace: moe_gemm_fp8_workspace_bytes(M, N, K) bytes."""
     fn = "moe_gemm_fp8"
-    lda, ldw = _rows(A, "A", (torch.uint8,)), _rows(W, "W", (torch.uint8,))
-    ldd = _rows(D, "D", (torch.bfloat16, torch.float32))
-    ldc = 0 if C is None else _rows(C, "C", (torch.float32,))
-    _dev(SFA, "SFA", torch.float32, 2), _dev(SFW, "SFW", torch.float32, 2), _dev(workspace, "workspace")
-    M, K = A.shape
+    M, K, dev = _shape2(A, "A")
     N = W.shape[0]
-    if W.shape[1] != K or tuple(D.shape) != (M, N) or (C is not None and tuple(C.shape) != (M, N)):
-        raise ValueError(f"{fn}: A is {tuple(A.shape)}, W {tuple(W.shape)}, D {tuple(D.shape)}"
-                         + ("" if C is None else f", C {tuple(C.shape)}"))
-    nb = (N + 127) // 128
-    if tuple(SFA.shape) != (M, K // 128) or tuple(SFW.shape) not in ((nb, K // 128), (N, K // 128)):
-        raise ValueError(f"{fn}: SFA is {tuple(SFA.shape)} (needs {(M, K // 128)}), SFW {tuple(SFW.shape)} "
-                         f"(needs {(nb, K // 128)} or {(N, K // 128)})")
-    gran = 128 if SFW.shape[0] == nb else 1
-    hs = _one_device(fn, stream, A, SFA, W, SFW, D, C, workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().moe_gemm_fp8(_ptr(A), lda, _ptr(SFA), _ptr(W), ldw, _ptr(SFW), gran, _ptr(D),
-                               BF16 if D.dtype == torch.bfloat16 else F32, ldd, _ptr(C), ldc, M, N, K,
-                               _ptr(workspace), ws_bytes, hs), fn)
+    lda = _rows(fn, dev, A, "A", _CODES, (M, K))
+    ldw = _rows(fn, dev, W, "W", _CODES, (N, K))
+    ldd = _rows(fn, dev, D, "D", _FLOATS, (M, N))
+    c, ldc = (None, 0) if C is None else (C.data_ptr(), _rows(fn, dev, C, "C", (torch.float32,), (M, N)))
+    gran = 128 if SFW.shape[0] == (N + 127) // 128 else 1
+    sfa = _whole(fn, dev, SFA, "SFA", torch.float32, (M, K // 128))
+    sfw = _whole(fn, dev, SFW, "SFW", torch.float32, ((N + gran - 1) // gran, K // 128))
+    ws, ws_bytes = _scratch(fn, dev, workspace)
+    _check(load().moe_gemm_fp8(A.data_ptr(), lda, sfa, W.data_ptr(), ldw, sfw, gran, D.data_ptr(),
+                               BF16 if D.dtype is torch.bfloat16 else F32, ldd, c, ldc, M, N, K, ws, ws_bytes,
+                               _queue(fn, dev, stream)), fn)
 
 
 def moe_quant_act_t(x, q, sf, stream=None):
     """x bf16 [M, K] (rows may be strided) -> q uint8 [K, Mp] (E4M3 codes of the transposed x) and sf float32
     [K, Mp/128], Mp = M rounded up to a multiple of 128."""
     fn = "moe_quant_act_t"
-    ldx = _rows(x, "x", (torch.bfloat16,))
-    _dev(q, "q", torch.uint8, 2), _dev(sf, "sf", torch.float32, 2)
-    M, K = x.shape
+    M, K, dev = _shape2(x, "x")
     mb = (M + 127) // 128
-    if tuple(q.shape) != (K, 128 * mb) or tuple(sf.shape) != (K, mb):
-        raise ValueError(f"{fn}: q is {tuple(q.shape)}, sf {tuple(sf.shape)}, need {(K, 128 * mb)} and {(K, mb)}")
-    hs = _one_device(fn, stream, x, q, sf)
-    _check(load().moe_quant_act_t(_ptr(x), M, K, ldx, _ptr(q), _ptr(sf), hs), fn)
+    ldx = _rows(fn, dev, x, "x", (torch.bfloat16,), (M, K))
+    qp = _whole(fn, dev, q, "q", torch.uint8, (K, 128 * mb))
+    sp = _whole(fn, dev, sf, "sf", torch.float32, (K, mb))
+    _check(load().moe_quant_act_t(x.data_ptr(), M, K, ldx, qp, sp, _queue(fn, dev, stream)), fn)
 
 
 def moe_stream_read_words() -> int:
