@@ -575,7 +575,7 @@ hipError_t launch_big(const DenseArgs& a, hipStream_t s) {
   return launch_join(a, s);
 }
 
-// Few rows (a decode step): every weight byte is used by one wave, so waves need nothing from one another.  A
+// Few rows (a decode step) or few outputs: every weight byte is used by one wave, so waves need nothing from one another.  A
 // workgroup takes 16 CB columns and all 16 RB rows; its KS waves split K into runs of groups of 4 blocks, each
 // with a ring of S blocks of its own in LDS (no barrier in the loop), and meet once at the end, where the partial
 // sums are added in wave order.  The way through LDS is for the load path: a fragment's lanes hold 16 different
@@ -766,6 +766,15 @@ Plan plan_dense(int M, int N, int K, bool wide) {
   if (s > KB / 8) s = KB / 8;
   if (s > 8) s = 8;
   if (s > 1 && (float)KB * least * (1.0f - 1.0f / (float)s) > 5.0f) best.splits = s;
+  // Where its workgroups of 64 x 16 outputs fit the chip once, the streaming kernel, whose waves split K among themselves (0.14
+  // us per K block, in fp32 0.18), unless splitting tiles is faster or the activations, which the columns' workgroups on every
+  // XCD read anew, take longer (6 TB/s).  us, tiles and streams: 192 x 1000 x 2048 6.9, 5.1, in fp32 10.3, 6.3; 131 x 512 x
+  // 7168 (tiles in seven splits) 10.1, 10.9; 4096 x 64 x 7168 12.8, 19.8; more than one round, 300 x 1000 x 2048: 7.0, 8.7.
+  const int64_t cols = (N + 15) / 16;
+  const float tiles_us = (float)KB * least / (float)best.splits + (best.splits > 1 ? 5.0f : 0.0f);
+  const float stream_us = (float)KB * (wide ? 0.18f : 0.14f);
+  const float reread_us = (float)M * (float)K * (float)(cols < kXcd ? cols : kXcd) / 6e6f;
+  if ((M + 63) / 64 * cols <= kCus && stream_us < tiles_us && reread_us < tiles_us) return {kStream64, 1};
   return best;
 }
 

@@ -80,7 +80,8 @@ def _check(d, a, sa, w, sw, gran, c=None):
 SIZES = [(1, 1, 128), (1, 64, 256), (1, 4096, 1024), (2, 130, 384), (7, 33, 128), (16, 16, 2048), (17, 257, 640),
          (31, 1000, 512), (33, 128, 128), (64, 320, 1152), (65, 127, 256), (100, 96, 7168), (129, 129, 896),
          (200, 640, 384), (255, 513, 128), (257, 250, 256), (300, 1100, 640), (512, 384, 512), (777, 259, 384), (40, 5000, 384), (5, 4200, 1280),
-         (20, 4500, 640), (66, 300, 4096), (130, 64, 32768), (1100, 3000, 384), (1030, 4100, 256), (2100, 4500, 640)]
+         (20, 4500, 640), (66, 300, 4096), (130, 64, 32768), (1100, 3000, 384), (1030, 4100, 256), (2100, 4500, 640), (70, 3000, 1280), (259, 1300, 640), (577, 800, 896),
+         (131, 2200, 7168), (1000, 130, 512), (4000, 64, 7168), (4000, 60, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
