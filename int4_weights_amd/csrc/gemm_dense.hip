@@ -126,6 +126,52 @@ __device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v, 
   }
 }
 
+// Eight columns n .. n + 7 of row m as bf16 pairs; align: columns that can be written at once.
+__device__ __forceinline__ void store8(const DenseArgs& a, int m, int n, const v4f v, int align) {
+  if (m >= a.M || n >= a.N) return;
+  uint16_t* d = (uint16_t*)a.D + (int64_t)m * a.ldd + n;
+  if (align == 8 && n + 8 <= a.N) {
+    *(v4f*)d = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t p[2] = {__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1])};
+    if (align >= 4 && n + 4 * i + 4 <= a.N) {
+      *(uint2*)(d + 4 * i) = uint2{p[0], p[1]};
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + 4 * i + e < a.N) d[4 * i + e] = (uint16_t)(p[e >> 1] >> 16 * (e & 1));
+  }
+}
+
+// Lanes 8 .. 15 of each row of 16 get b of lane - 8 in a; lanes 0 .. 7 get a of lane + 8 in b.
+__device__ __forceinline__ void swap8(v4f& a, v4f& b) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int x = __float_as_int(a[e]), y = __float_as_int(b[e]);
+    a[e] = __int_as_float(__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false));  // row_ror:8, lanes 8 .. 15
+    b[e] = __int_as_float(__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false));
+  }
+}
+
+// Of the lanes' 4 columns in two neighbouring 16-column blocks, rounded to bf16: lane group lg gets 8 columns, of block lg & 1,
+// from 8 (lg >> 1) on.
+__device__ __forceinline__ v4f join_columns(const v4f a, const v4f b) {
+  v4f o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t x = f32_to_bf16_rne(a[2 * h]) | (f32_to_bf16_rne(a[2 * h + 1]) << 16);
+    const uint32_t y = f32_to_bf16_rne(b[2 * h]) | (f32_to_bf16_rne(b[2 * h + 1]) << 16);
+    const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);  // x of groups 1, 3 for y of groups 0, 2
+    o[h] = __uint_as_float(r[0]);
+    o[2 + h] = __uint_as_float(r[1]);
+  }
+  return o;
+}
+
 template <int RB, int CB, int WM, int WN, int S>
 struct TileCfg {
   static constexpr int NW = WM * WN;
@@ -255,7 +301,12 @@ struct Tile {
     }
   }
 
+  // A lane's sums are 4 columns of one row per 16x16 block; stored so, an instruction writes 16 rows in pieces of 32 bytes (bf16)
+  // or 64. Lanes exchange columns first, so that it writes whole 128-byte lines of 8 rows (bf16 tiles of 32 columns a wave: 64
+  // bytes of 16 rows); C is read in the same order.  (4096 x 4096 x 128 in bf16: 16.7 -> 15.4 us; 4096 x 7168 x 128
+  // in fp32: 38.4 -> 28.6 us.)
   __device__ __forceinline__ void store(v4f (&acc)[RB][CB]) const {
+    static_assert(CB == 2 || CB == 4, "columns are exchanged in pairs");
     // The sums are whole before any lane's store is masked off: without this the compiler moves the last matrix
     // instructions, and the loads of their operands, under the stores' masks, where the other lanes' operands are stale.
 #pragma unroll
@@ -270,11 +321,35 @@ struct Tile {
       o.ldd = o.N;
       o.D = a.ws + (int64_t)blockIdx.y * a.M * o.N;
     }
-    const bool vec = can_store4(o);
+    const int hi = l16 >> 3, l8 = l16 & 7, m = m0 + wm, n = n0 + wn;
+    if (o.f32) {
+      const bool vec = can_store4(o);
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+      for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int j = 0; j < CB; ++j) store4(o, m0 + wm + 16 * i + l16, n0 + wn + 16 * j + 4 * lg, acc[i][j], vec);
+        for (int j = 0; j < CB; j += 2) {
+          v4f v[2] = {acc[i][j], acc[i][j + 1]};
+          swap8(v[0], v[1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) store4(o, m + 16 * i + 8 * h + l8, n + 16 * (j + hi) + 4 * lg, v[h], vec);
+        }
+      return;
+    }
+    const int align = o.ldd % 8 == 0 && ((uintptr_t)o.D & 15) == 0 ? 8 : o.ldd % 4 == 0 && ((uintptr_t)o.D & 7) == 0 ? 4 : 1;
+    const int n8 = n + 16 * (lg & 1) + 8 * (lg >> 1);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      v4f v[CB / 2];  // 8 columns of bf16 each
+#pragma unroll
+      for (int j = 0; j < CB; j += 2) v[j / 2] = join_columns(acc[i][j], acc[i][j + 1]);
+      if constexpr (CB == 4) {
+        swap8(v[0], v[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) store8(o, m + 16 * i + 8 * h + l8, n8 + 32 * hi, v[h], align);
+      } else {
+        store8(o, m + 16 * i + l16, n8, v[0], align);
+      }
+    }
   }
 };
 
@@ -288,8 +363,9 @@ __device__ __forceinline__ void promote(v4f& acc, const v4f sum, float sa, const
 // Tiles whose fragments fit the registers twice: block kb + 1's fragments and scales are read while block kb is
 // multiplied, and block kb + 4 is copied meanwhile into the slot that block kb left when it was read.  With few matrix
 // instructions per step a wave's time is its instruction count, so the loop is unrolled over the 4 slots (and the 4 blocks of
-// a scale group): slots, offsets and scale positions are constants (64x64 tile: 200 instructions and 0.31 us per K block
-// with computed ones).
+// a scale group): slots, offsets and scale positions are constants.  Measured per K block with the chip full: 64x64 0.33 us
+// (two workgroups on a compute unit 0.57), 64x128 0.50, 128x128 0.69.  131 x 7168 x 2048, 168 tiles of 64x128: 9.0 us, of which
+// 16 steps of 0.5 us each wait for copies out of the L2: with every tile reading the same operands it takes 6.9.
 template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
 __global__ TWO_WAVES void gemm_dense_small_kernel(const DenseArgs a) {
   constexpr int S = 4;
@@ -417,8 +493,14 @@ __global__ TWO_WAVES void gemm_dense_small_kernel(const DenseArgs a) {
 }
 
 // The 256x256 tile (8 waves of 128x64: two per SIMD, so that one wave's promotions run beside the other's matrix
-// instructions; a wave's 128 accumulators leave room for its fragments once).  LDS traffic (64 KB copied in and 192
-// KB read per K block) takes as long as the matrix instructions, so both have to run all the time:
+// instructions; a wave's 128 accumulators leave room for its fragments once), and in bf16 instructions the 128x128 tile (4
+// waves of 64x64, two workgroups per compute unit).  A 256x256 tile copies 64 KB in and reads 192 KB per K block.
+// 4096 x 4096 x 7168: 106 us, 2.26 PFLOP/s; 1.6 us per K block and 13 us at the ends (first copies, stores).  Counters of
+// that run: matrix instructions 47% of the time at 2.07 GHz, other vector instructions 38%, LDS 24%; with every tile reading
+// the same operands it takes 5% less, so what bounds it is the two kinds of vector instructions sharing the issue port (a
+// matrix instruction takes about 8 clocks of it, each other one 4).  4096 x 7168 x 4096 with 1x128 scales, fp32 and an addend:
+// 246 us, 0.98 PFLOP/s, where beside each 16-clock matrix instruction 4.4 others are issued (conversions and promotions).
+// The step:
 //  * row blocks 0 .. RB-3 in turn, their fragments read two blocks ahead;
 //  * then the barrier that publishes block kb + 1, every fragment of block kb being in registers, and the last two row
 //    blocks column by column: after column j's two matrix instructions its weight fragment is read anew for block kb + 1;
