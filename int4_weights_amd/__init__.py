@@ -1,4 +1,5 @@
-"""MoE grouped GEMM on gfx950 (MI355X): FP8 block-scaled, 4-bit weight-only, FP4, INT8 and BF16.
+"""MoE grouped GEMM on gfx950 (MI355X): FP8 block-scaled, 4-bit weight-only, FP4, INT8 and BF16, with the router, a dense
+FP8 product and their gradients.
 
 The compute path is libmoe.so (hand-written HIP kernels behind the C ABI in
 include/moe.h); this package is its thin Python binding.  Build the library

@@ -364,8 +364,8 @@ __device__ __forceinline__ void promote(v4f& acc, const v4f sum, float sa, const
 // multiplied, and block kb + 4 is copied meanwhile into the slot that block kb left when it was read.  With few matrix
 // instructions per step a wave's time is its instruction count, so the loop is unrolled over the 4 slots (and the 4 blocks of
 // a scale group): slots, offsets and scale positions are constants.  Measured per K block with the chip full: 64x64 0.33 us
-// (two workgroups on a compute unit 0.57), 64x128 0.50, 128x128 0.69.  131 x 7168 x 2048, 168 tiles of 64x128: 9.0 us, of which
-// 16 steps of 0.5 us each wait for copies out of the L2: with every tile reading the same operands it takes 6.9.
+// (two workgroups on a compute unit 0.57), 64x128 0.50, 128x128 0.69.  131 x 7168 x 2048, 168 tiles of 64x128, weights from
+// HBM: 11.0 us (9.0 where the caches hold them); the steps wait for copies: with every tile reading the same operands 8.8.
 template <bool WIDE, bool GRAN1, int RB, int CB, int WM, int WN>
 __global__ TWO_WAVES void gemm_dense_small_kernel(const DenseArgs a) {
   constexpr int S = 4;
@@ -496,10 +496,11 @@ __global__ TWO_WAVES void gemm_dense_small_kernel(const DenseArgs a) {
 // instructions; a wave's 128 accumulators leave room for its fragments once), and in bf16 instructions the 128x128 tile (4
 // waves of 64x64, two workgroups per compute unit).  A 256x256 tile copies 64 KB in and reads 192 KB per K block.
 // 4096 x 4096 x 7168: 106 us, 2.26 PFLOP/s; 1.6 us per K block and 13 us at the ends (first copies, stores).  Counters of
-// that run: matrix instructions 47% of the time at 2.07 GHz, other vector instructions 38%, LDS 24%; with every tile reading
-// the same operands it takes 5% less, so what bounds it is the two kinds of vector instructions sharing the issue port (a
-// matrix instruction takes about 8 clocks of it, each other one 4).  4096 x 7168 x 4096 with 1x128 scales, fp32 and an addend:
-// 246 us, 0.98 PFLOP/s, where beside each 16-clock matrix instruction 4.4 others are issued (conversions and promotions).
+// that run: matrix instructions 52% of the time at 2.03 GHz, other vector instructions 35%, LDS 26%: the first two overlap
+// little, although two waves a SIMD that do nothing else overlap them (16 clocks a matrix instruction in bf16, with four others
+// beside it 26).  Memory is not what bounds it: with every tile reading the same operands it takes 5% less.  4096 x 7168 x 4096
+// with 1x128 scales, fp32 output and an addend: 246 to 265 us, 0.91 to 0.98 PFLOP/s; beside each 16-clock matrix instruction 4.4 others are
+// issued (conversions and promotions; 128x128 scales save one: 221 us).
 // The step:
 //  * row blocks 0 .. RB-3 in turn, their fragments read two blocks ahead;
 //  * then the barrier that publishes block kb + 1, every fragment of block kb being in registers, and the last two row

@@ -372,7 +372,8 @@ hipError_t launch_quant_weight_int4(const uint16_t* w, int E, int N, int K, uint
 // One workgroup per 128 rows x 64 columns.  A lane holds 4 consecutive rows of 8 columns (16-byte loads), so
 // each column's 4 codes are one dword of the transposed tile; column maxima meet over the lanes that share
 // columns, then over the 4 waves.  The tile goes through LDS (rows of 132 bytes: the 64 dwords a wave writes at once
-// fall on 64 banks) and leaves as whole 128-byte rows.  HBM-bound: 2 bytes read and 1 written per value.
+// fall on 64 banks) and leaves as whole 128-byte rows.  HBM-bound: 2 bytes read and 1 written per value (4096 x
+// 7168: 19.4 us, 4.6 TB/s; 333 x 1536: 4.7 us, the launch).
 constexpr int kQtCols = 64, kQtStride = 132;
 
 __global__ __launch_bounds__(256) void quant_act_t_kernel(const uint16_t* __restrict__ x, int64_t M, int K,

@@ -27,6 +27,10 @@
 // kernel's tail, with about 12 of them in 4096.)  Without a bias the keys are the logits
 // themselves and need no check.
 //
+// Measured: 4096 x 256, sigmoid, bias, 4 of 8 groups, k 8: 8.6 us; softmax without bias 5.6 us; 16 x 128: 3.8 us, the launch.
+// Memory (4.5 MB, 0.9 us) does not bound it: each of the k rounds waits for a maximum over the wave, seven dependent
+// cross-lane steps.
+//
 // A logit of -inf or NaN marks an expert that this token may not use; slots
 // left over get id -1 and weight 0, which moe_route_pack skips.
 #include "moe_device.h"
@@ -563,7 +567,8 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const RouterArgs a) {
 //   renormalised:       d x_r = w_r (g_r - sum_j g_j w_j / scale), times 1 - s_r for sigmoid scores
 //   sigmoid as it is:   d x_r = scale g_r s_r (1 - s_r)
 //   softmax as it is:   d x_e = scale p_e ([e selected] g_e - sum_j g_j p_j), for every expert
-// One wave per token; slots in lanes, the row assembled in LDS so that it is written once, whole.  An expert
+// One wave per token; slots in lanes, the row assembled in LDS so that it is written once, whole (4096 x 256 in fp32: 5.3 us;
+// 8191 x 128 in bf16, softmax as it is: 6.9 us; the launch takes 4.4 of either).  An expert
 // named by two slots gets the sum over them, in slot order.
 template <typename T, int VPL>
 __global__ __launch_bounds__(256) void router_topk_bwd_kernel(const RouterBwdArgs a) {
