@@ -627,7 +627,8 @@ moe_status moe_gemm_fp8(const uint8_t* A, int64_t lda, const float* SFA,
  *   x [M, K] bf16, rows ldx elements apart.  With Mp = M rounded up to 128:
  *   qt [K, Mp] E4M3FN codes and sft [K, Mp/128] fp32: row k of qt is column k of
  *   x, quantised by the rule of moe_quant_act (power-of-two scale per 128
- *   consecutive m), rows of x past M counting as zeros.
+ *   consecutive m; the same bits as moe_quant_act of the transposed x, infinities
+ *   and quiet NaN included), rows of x past M counting as zeros.
  *   Requires K % 8 == 0, ldx % 8 == 0 and >= K, ceil(M/128) * ceil(K/64) < 2^24,
  *   x and qt 16-byte aligned, sft 4-byte aligned; the outputs must not overlap x.  M == 0 is a no-op. */
 moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx,

@@ -239,6 +239,25 @@ def test_quant_act_t(M, K):
         assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(sf.cpu().numpy(), rs)
 
 
+def test_quant_act_t_is_quant_act_of_the_transpose():
+    """Every bf16 pattern: subnormals, zeros, infinities and quiet NaN in every block."""
+    require_gpu()
+    g = torch.Generator().manual_seed(1)
+    bits = torch.randint(0, 65536, (1280, 256), generator=g, dtype=torch.int32)
+    nan = ((bits & 0x7F80) == 0x7F80) & ((bits & 0x7F) != 0)
+    bits = torch.where(nan, bits | 0x40, bits)
+    bits[:128] &= 0x807F  # subnormals alone
+    bits[128:256] &= 0x8000  # zeros of both signs
+    bits[256:768] = torch.where((bits[256:768] & 0x7F80) == 0x7F80, 0x3F80, bits[256:768])  # finite alone
+    x = bits.to(torch.int16).view(torch.bfloat16).to(DEV)
+    q, sf = torch.empty(256, 1280, dtype=torch.uint8, device=DEV), torch.empty(256, 10, device=DEV)
+    moe.moe_quant_act_t(x, q, sf)
+    q2, sf2 = torch.empty_like(q), torch.empty_like(sf)
+    moe.moe_quant_act(x.t().contiguous(), q2, sf2)
+    torch.cuda.synchronize()
+    assert torch.equal(sf.view(torch.int32), sf2.view(torch.int32)) and torch.equal(q, q2)
+
+
 def test_quant_act_t_refusals():
     require_gpu()
     x = torch.zeros(4, 16, dtype=torch.bfloat16, device=DEV)
