@@ -94,25 +94,22 @@ __device__ __forceinline__ v4f block_sum(const Frag<true>& w, const Frag<true>& 
   return s;
 }
 
-// Whether rows of D (and C) can be accessed 4 columns at a time.
-__device__ __forceinline__ bool can_store4(const DenseArgs& a) {
-  return a.ldd % 4 == 0 && ((uintptr_t)a.D & (a.f32 ? 15 : 7)) == 0 &&
-         (!a.C || (a.ldc % 4 == 0 && ((uintptr_t)a.C & 15) == 0));
-}
+// Vectors of D and C, whose rows begin at any element (global memory takes them at any address).
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t v2u_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// Four consecutive columns n .. n + 3 of row m (vec: they may be accessed as one vector where all four exist).
-__device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v, bool vec) {
+// Four consecutive columns n .. n + 3 of row m.
+__device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v) {
   if (m >= a.M || n >= a.N) return;
   const int64_t at = (int64_t)m * a.ldd + n;
-  if (vec && n + 4 <= a.N) {
+  if (n + 4 <= a.N) {
     if (a.f32) {
-      if (a.C) v += *(const v4f*)(a.C + (int64_t)m * a.ldc + n);
-      __builtin_nontemporal_store(v, (v4f*)((float*)a.D + at));
+      if (a.C) v += *(const v4f_any*)(a.C + (int64_t)m * a.ldc + n);
+      __builtin_nontemporal_store(v, (v4f_any*)((float*)a.D + at));
     } else {
-      uint2 o;
-      o.x = f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16);
-      o.y = f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16);
-      *(uint2*)((uint16_t*)a.D + at) = o;
+      *(v2u_any*)((uint16_t*)a.D + at) = v2u_any{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
+                                                 f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
     }
     return;
   }
@@ -126,25 +123,20 @@ __device__ __forceinline__ void store4(const DenseArgs& a, int m, int n, v4f v, 
   }
 }
 
-// Eight columns n .. n + 7 of row m as bf16 pairs; align: columns that can be written at once.
-__device__ __forceinline__ void store8(const DenseArgs& a, int m, int n, const v4f v, int align) {
+// Eight columns n .. n + 7 of row m as bf16 pairs.
+__device__ __forceinline__ void store8(const DenseArgs& a, int m, int n, const v4f v) {
   if (m >= a.M || n >= a.N) return;
   uint16_t* d = (uint16_t*)a.D + (int64_t)m * a.ldd + n;
-  if (align == 8 && n + 8 <= a.N) {
-    *(v4f*)d = v;
+  v4u_any p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = __float_as_uint(v[i]);
+  if (n + 8 <= a.N) {
+    *(v4u_any*)d = p;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t p[2] = {__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1])};
-    if (align >= 4 && n + 4 * i + 4 <= a.N) {
-      *(uint2*)(d + 4 * i) = uint2{p[0], p[1]};
-      continue;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + 4 * i + e < a.N) d[4 * i + e] = (uint16_t)(p[e >> 1] >> 16 * (e & 1));
-  }
+  for (int e = 0; e < 8; ++e)
+    if (n + e < a.N) d[e] = (uint16_t)(p[e >> 1] >> 16 * (e & 1));
 }
 
 // Lanes 8 .. 15 of each row of 16 get b of lane - 8 in a; lanes 0 .. 7 get a of lane + 8 in b.
@@ -323,7 +315,6 @@ struct Tile {
     }
     const int hi = l16 >> 3, l8 = l16 & 7, m = m0 + wm, n = n0 + wn;
     if (o.f32) {
-      const bool vec = can_store4(o);
 #pragma unroll
       for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -331,11 +322,10 @@ struct Tile {
           v4f v[2] = {acc[i][j], acc[i][j + 1]};
           swap8(v[0], v[1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) store4(o, m + 16 * i + 8 * h + l8, n + 16 * (j + hi) + 4 * lg, v[h], vec);
+          for (int h = 0; h < 2; ++h) store4(o, m + 16 * i + 8 * h + l8, n + 16 * (j + hi) + 4 * lg, v[h]);
         }
       return;
     }
-    const int align = o.ldd % 8 == 0 && ((uintptr_t)o.D & 15) == 0 ? 8 : o.ldd % 4 == 0 && ((uintptr_t)o.D & 7) == 0 ? 4 : 1;
     const int n8 = n + 16 * (lg & 1) + 8 * (lg >> 1);
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
@@ -345,9 +335,9 @@ struct Tile {
       if constexpr (CB == 4) {
         swap8(v[0], v[1]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) store8(o, m + 16 * i + 8 * h + l8, n8 + 32 * hi, v[h], align);
+        for (int h = 0; h < 2; ++h) store8(o, m + 16 * i + 8 * h + l8, n8 + 32 * hi, v[h]);
       } else {
-        store8(o, m + 16 * i + l16, n8, v[0], align);
+        store8(o, m + 16 * i + l16, n8, v[0]);
       }
     }
   }
@@ -628,11 +618,10 @@ __global__ TWO_WAVES void gemm_dense_kernel(const DenseArgs a) {
 __global__ __launch_bounds__(256) void gemm_dense_join_kernel(const DenseArgs a) {
   const int np = (a.N + 3) / 4;
   const int64_t total = (int64_t)a.M * np;
-  const bool vec = can_store4(a);
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
     v4f v = *(const v4f*)(a.ws + 4 * q);
     for (int k = 1; k < a.splits; ++k) v += *(const v4f*)(a.ws + 4 * (q + k * total));
-    store4(a, (int)(q / np), 4 * (int)(q % np), v, vec);
+    store4(a, (int)(q / np), 4 * (int)(q % np), v);
   }
 }
 
@@ -779,13 +768,12 @@ __global__ TWO_WAVES void gemm_stream_kernel(const DenseArgs a) {
 #pragma unroll
     for (int j = 0; j < CB; ++j) *(v4f*)(part + (16 * i + l16) * (kCols + 4) + 16 * j + 4 * lg) = acc[i][j];
   __syncthreads();
-  const bool vec = can_store4(a);
   for (int q = threadIdx.x; q < kRows * kCols / 4; q += KS * 64) {
     const int m = q / (kCols / 4), n = 4 * (q % (kCols / 4));
     v4f v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KS; ++k) v += *(const v4f*)((const float*)(sm + k * C::kWave) + m * (kCols + 4) + n);
-    store4(a, m0 + m, n0 + n, v, vec);
+    store4(a, m0 + m, n0 + n, v);
   }
 }
 
