@@ -148,9 +148,11 @@ __device__ __forceinline__ void shared_row(const CombineBwdArgs& a, int p, int o
   }
 }
 
-// NT threads per B slots of a token: 256 and 8 where there are tokens enough to fill the chip, so that dZ is read once;
-// else 1024 and 2, so that a row (up to 8192 columns) is in flight at once and the slots spread over more compute
-// units.
+// NT threads per B slots of a token.  Pairs of slots while the chip holds all of them at once: 1024 threads each (a row of
+// up to 8192 columns in flight) where every one has a compute unit, 512 where four share one; beyond that 256 threads and 4
+// slots, or 8 where a second batch of 4 would hold one or two.  us, k x N, 1024 and 2, 512 and 2, 256 and 4, 256 and 8:
+// 61 x 8 x 7168 7.4, 7.8, 14.1, 22.7; 128 x 8 x 4096 10.4, 8.1, 10.9, 17.2; 451 x 8 x 4096 34.8, 22.8, 18.4, 23.2;
+// 4096 x 8 x 4096 257, 164, 122, 128; 4096 x 5 x 6560 228, 160, 152, 135; 2166 x 2 x 1312 34.7, 23.3, 20.5, 29.0.
 template <int NT, int B>
 __global__ __launch_bounds__(NT) void combine_bwd_kernel(const CombineBwdArgs a) {
   constexpr int kScan = (kRouteSmallMax + NT - 1) / NT;
@@ -282,11 +284,17 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.T < 2 * device_info().cus) {
-    combine_bwd_kernel<1024, 2><<<(unsigned)((int64_t)a.T * ((a.k + 1) / 2)), 1024, 0, s>>>(a);
-  } else {
+  const int64_t pairs = (int64_t)a.T * ((a.k + 1) / 2), cus = device_info().cus;
+  if (pairs <= cus) {
+    combine_bwd_kernel<1024, 2><<<(unsigned)pairs, 1024, 0, s>>>(a);
+  } else if (pairs <= 4 * cus) {
+    combine_bwd_kernel<512, 2><<<(unsigned)pairs, 512, 0, s>>>(a);
+  } else if (a.k % 8 == 5 || a.k % 8 == 6) {
     const int64_t total = (int64_t)a.T * ((a.k + 7) / 8);
     combine_bwd_kernel<256, 8><<<(unsigned)(total < cap ? total : cap), 256, 0, s>>>(a);
+  } else {
+    const int64_t total = (int64_t)a.T * ((a.k + 3) / 4);
+    combine_bwd_kernel<256, 4><<<(unsigned)(total < cap ? total : cap), 256, 0, s>>>(a);
   }
   return hipGetLastError();
 }

@@ -62,6 +62,7 @@ def _inputs(T, k, N, rows, seed, unique=True):
     (1, 1, 8, 1), (1, 8, 7168, 8), (5, 3, 2056, 40), (61, 8, 520, 500), (3, 64, 136, 200), (7, 9, 4096, 70),
     (513, 8, 64, 4200),  # more than 4096 routes: the workspace path
     (700, 6, 8, 4300), (4097, 1, 16, 4097),
+    (130, 8, 4104, 1100), (300, 7, 1032, 2200), (450, 5, 2056, 2300), (300, 13, 264, 4000), (1500, 3, 72, 4600),
 ])
 def test_against_oracle(T, k, N, rows):
     require_gpu()
