@@ -113,8 +113,7 @@ __device__ __forceinline__ v4i pack8(const float (&f)[8]) {
 }
 
 // dY of a row named by `cnt` slots, the lowest of them `own`: the whole workgroup sums them in route order, searching
-// the table NT entries at a time (a thread searching alone: R / 2 dependent loads per row, 10 s where 2^20 routes name
-// half as many rows).
+// the table NT entries at a time (a thread searching alone would take R / 2 dependent loads for a row named twice).
 template <int NT>
 __device__ __forceinline__ void shared_row(const CombineBwdArgs& a, int p, int own, int cnt) {
   __shared__ uint64_t s_hit[NT / 64];
