@@ -515,7 +515,7 @@ moe_status moe_unpermute_combine(const uint16_t* Y, int64_t y_rows,
                                  uint16_t* Z, void* stream);
 
 /* moe_unpermute_combine_bwd: the gradient of moe_unpermute_combine.
- *     dweights[t, r] = sum_n dZ[t, n] * Y[output_index[t, r], n]     (fp32; 0 for a skipped slot)
+ *     dweights[t, r] = sum_n dZ[t, n] * Y[output_index[t, r], n]     (fp32; 0 for a skipped slot, whatever dZ holds)
  *     dY[p, n]       = bf16_rne( sum over the slots (t, r) that name row p, in route order
  *                                t*k + r, of topk_weights[t, r] * dZ[t, n] )
  *   Slots with output_index < 0 or >= y_rows are skipped.  Rows of dY that no

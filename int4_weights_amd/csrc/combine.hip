@@ -253,6 +253,7 @@ __global__ __launch_bounds__(NT) void combine_bwd_kernel(const CombineBwdArgs a)
     if (a.dw) {
 #pragma unroll
       for (int j = 0; j < B; ++j) {
+        if (p[j] < 0) dot[j] = 0.0f;  // a skipped slot's zeros met dZ, which may hold Inf or NaN
 #pragma unroll
         for (int off = 32; off; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
         if (lane == 0) s_sum[wv][j] = dot[j];
