@@ -21,14 +21,13 @@
 // publishes block kb + 1 sits before the promotion of the step's last row block, when every wave holds its last
 // fragments of block kb in registers, so the next block's first fragments are read behind matrix instructions and
 // promotions.  Scales come 4 K blocks at a time (one 16-byte copy per row).
+#include "dense_plan.h"
 #include "moe_device.h"
 #include "moe_internal.h"
 
 namespace moe {
 
 namespace {
-
-constexpr int kXcd = 8;
 
 // Workgroups of up to 512 threads are declared as 512: at two waves per SIMD a wave has 256 registers.  Given 512, the
 // compiler takes every K block's sums through the same four accumulation registers, each matrix instruction waiting for
@@ -206,7 +205,7 @@ struct Tile {
     lds0 = lds_offset(sm);
     KB = a.K / 128;
     // this workgroup's K blocks (split K: a multiple of 4 per split)
-    const int per_split = ((KB + 3) / 4 + a.splits - 1) / a.splits * 4;
+    const int per_split = split_blocks(KB, a.splits);
     kb0 = uniform(min((int)blockIdx.y * per_split, KB));
     kb1 = uniform(min(kb0 + per_split, KB));
     // Workgroup b runs on XCD b % 8: consecutive tiles go to one XCD, and consecutive tiles are blocks of up to 8
@@ -791,71 +790,6 @@ hipError_t launch_stream(const DenseArgs& a, hipStream_t s) {
   const dim3 grid((a.N + 16 * CB - 1) / (16 * CB), (a.M + 16 * RB - 1) / (16 * RB));
   gemm_stream_kernel<WIDE, GRAN1, RB, CB, KS, S><<<grid, KS * 64, 0, s>>>(a);
   return hipGetLastError();
-}
-
-// Which kernel, by sizes alone.  Times in us per K block of one round of tiles over the 256 compute units, as
-// measured with the whole chip busy (first: one workgroup per compute unit; second, where two fit: both); the tile with
-// the smallest sum of rounds is taken.  Measured (us, N x K = 4096 x 7168, bf16 output): 256 rows 64x64 22.2, 64x128
-// 29.7, 128x128 40.0; 512 rows 34.3, 30.4, 39.6; 1024 rows 58.9, 51.1, 40.8; 2048 rows 128x128 72.7, 256x256 86; 4096
-// rows 141, 111.
-enum Kind { kStream16, kStream32, kStream64, k64x64, k64x128, k128x128, k128x128two, k256x256 };
-struct Plan {
-  Kind kind;
-  int splits;
-};
-struct TileCost {
-  Kind kind;
-  int bm, bn;
-  float one, two;  // two = 0: one workgroup per compute unit
-};
-constexpr int kCus = 256;
-
-Plan plan_dense(int M, int N, int K, bool wide) {
-  if (M <= 16) return {kStream16, 1};
-  if (M <= 32) return {kStream32, 1};
-  if (M <= 64) return {kStream64, 1};
-  constexpr TileCost narrow_t[] = {{k64x64, 64, 64, 0.33f, 0.57f},
-                                   {k64x128, 64, 128, 0.5f, 0.0f},
-                                   {k128x128, 128, 128, 0.69f, 0.0f},
-                                   {k256x256, 256, 256, 1.9f, 0.0f}};
-  constexpr TileCost wide_t[] = {{k64x64, 64, 64, 0.5f, 0.76f},
-                                 {k64x128, 64, 128, 0.74f, 0.0f},
-                                 {k128x128, 128, 128, 1.3f, 0.0f},
-                                 {k128x128two, 128, 128, 1.7f, 2.05f}};
-  Plan best{k64x64, 1};
-  float least = 0.0f;
-  int64_t best_tiles = 0;
-  auto consider = [&](const TileCost& c) {
-    const int64_t t = (int64_t)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-    const float f = c.two == 0.0f ? c.one * (float)((t + kCus - 1) / kCus)
-                                  : (t <= kCus ? c.one : c.two * (float)((t + 2 * kCus - 1) / (2 * kCus)));
-    if (best_tiles == 0 || f < least) {
-      least = f;
-      best.kind = c.kind;
-      best_tiles = t;
-    }
-  };
-  if (wide)
-    for (const TileCost& c : wide_t) consider(c);
-  else
-    for (const TileCost& c : narrow_t) consider(c);
-  // Few tiles and a long K: split it so that the chip fills, at least 8 blocks each, where that saves more than the second
-  // launch takes (131 x 1000 x 7168, 48 tiles: 14.7 us whole, 12.1 in two, 11.9 in five).
-  const int KB = K / 128;
-  int s = (int)(kCus / best_tiles);
-  if (s > KB / 8) s = KB / 8;
-  if (s > 8) s = 8;
-  if (s > 1 && (float)KB * least * (1.0f - 1.0f / (float)s) > 5.0f) best.splits = s;
-  // Where its workgroups of 64 x 16 outputs fit the chip once, the streaming kernel, whose waves split K among themselves (0.14
-  // us per K block, in fp32 0.18), unless splitting tiles is faster or the activations, which the columns' workgroups on every
-  // XCD read anew, take longer (6 TB/s).  us, tiles and streams: 192 x 1000 x 2048 6.9, 5.1, in fp32 10.3, 6.3; 131 x 512 x
-  // 7168 (tiles in seven splits) 10.1, 10.9; 4096 x 64 x 7168 12.8, 19.8; more than one round, 300 x 1000 x 2048: 7.0, 8.7.
-  const int64_t cols = (N + 15) / 16;
-  const float tiles_us = (float)KB * least / (float)best.splits + (best.splits > 1 ? 5.0f : 0.0f);
-  const float stream_us = (float)KB * (wide ? 0.18f : 0.14f);
-  const float reread_us = (float)M * (float)K * (float)(cols < kXcd ? cols : kXcd) / 6e6f;
-  if ((M + 63) / 64 * cols <= kCus && stream_us < tiles_us && reread_us < tiles_us) return {kStream64, 1};
-  return best;
 }
 
 template <bool WIDE, bool GRAN1>
