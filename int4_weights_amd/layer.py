@@ -268,6 +268,8 @@ class DenseFP8Linear:
 
     def grad_weight(self, dy, x, dw, accumulate=True):
         """dw float32 [N, K] (+)= dy^T x of dy bf16 [T, N] and x bf16 [T, K], both quantised along the tokens."""
+        if dy.shape[0] != x.shape[0]:
+            raise ValueError(f"dy has {dy.shape[0]} tokens, x {x.shape[0]}")
         mb = (x.shape[0] + 127) // 128
         if mb == 0:
             return dw if accumulate else dw.zero_()
