@@ -198,7 +198,10 @@ class MoeInt4Layer:
 class MoeRouter:
     """The router before a layer: gate logits -> (topk_ids, topk_weights), with the gradient back to the logits.
 
-    Holds the balance bias and the output buffers for up to max_tokens tokens; a call allocates nothing."""
+    Holds the balance bias and output buffers for up to max_tokens tokens; a call allocates nothing.  forward() without
+    buffers of the caller's writes those: its result lasts until the next such forward, so the gradient comes before that,
+    and such calls that overlap in time must not run on two streams.  Where several batches are under way (micro-batches, a
+    graph beside eager work), give each topk_ids and topk_weights of its own."""
 
     def __init__(self, E: int, topk: int, max_tokens: int, score: str = "softmax", bias: torch.Tensor | None = None,
                  n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
@@ -209,16 +212,21 @@ class MoeRouter:
         self.topk_ids = torch.empty(max_tokens, topk, dtype=torch.int32, device=device)
         self.topk_weights = torch.empty(max_tokens, topk, dtype=torch.float32, device=device)
 
-    def forward(self, logits):
-        """logits float32 or bf16 [T, E] -> this router's topk_ids and topk_weights, [T, topk] each."""
+    def forward(self, logits, topk_ids=None, topk_weights=None):
+        """logits float32 or bf16 [T, E] -> topk_ids int32 and topk_weights float32, [T, topk] each: the caller's if given
+        (both, of any T), else this router's."""
+        if (topk_ids is None) != (topk_weights is None):
+            raise ValueError("topk_ids and topk_weights come together")
         T = logits.shape[0]
-        ids, w = self.topk_ids[:T], self.topk_weights[:T]
+        ids, w = (self.topk_ids[:T], self.topk_weights[:T]) if topk_ids is None else (topk_ids, topk_weights)
+        if ids.shape != (T, self.topk):
+            raise ValueError(f"topk_ids is {tuple(ids.shape)}, needs {(T, self.topk)}")
         L.moe_router_topk(logits, ids, w, score=self.score, bias=self.bias, renormalize=self.renormalize,
                           scale=self.scale, **self.groups)
         return ids, w
 
     def backward(self, logits, topk_ids, dweights, dlogits):
-        """d logits of the weights that forward(logits) gave for topk_ids."""
+        """d logits of the weights that forward(logits) gave for topk_ids (which must still hold that choice)."""
         L.moe_router_topk_bwd(logits, topk_ids, dweights, dlogits, score=self.score, renormalize=self.renormalize,
                               scale=self.scale)
         return dlogits
