@@ -597,7 +597,8 @@ def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
 def moe_gemm_fp8(A, SFA, W, SFW, D, C=None, workspace=None, stream=None):
     """D = C + A W^T of E4M3 codes: A uint8 [M, K] with SFA float32 [M, K/128], W uint8 [N, K] with SFW float32
     [ceil(N/128), K/128] or [N, K/128]; D bf16 or float32 [M, N], C float32 [M, N] (float32 D only; may be D).  Rows of A, W, D
-    and C may be strided.  workspace: moe_gemm_fp8_workspace_bytes(M, N, K) bytes."""
+    and C may be strided.  float32 D counts every product in full; bf16 D is up to 7 * 2^-13 of the sum of magnitudes
+    off before its rounding (1.5e-5 of the result on normal data).  workspace: moe_gemm_fp8_workspace_bytes(M, N, K) bytes."""
     fn = "moe_gemm_fp8"
     M, K, dev = _shape2(A, "A")
     N = W.shape[0]

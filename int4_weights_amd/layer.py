@@ -265,7 +265,7 @@ class DenseFP8Linear:
         return self._gemm(q, sf, w, sfw, out)
 
     def forward(self, x, out):
-        """x bf16 [T, K] -> out bf16 or float32 [T, N]."""
+        """x bf16 [T, K] -> out bf16 or float32 [T, N] (float32: every product in full, at half the rate)."""
         return self._product(x, self.w, self.sfw, out)
 
     def grad_input(self, dy, dx):

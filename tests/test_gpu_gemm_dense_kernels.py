@@ -73,6 +73,37 @@ def test_scales_that_cannot_be_copied_as_vectors(M, N, K, f32, kind, splits):
     _check(M, N, K, f32, 1, offset=1)
 
 
+ONE_EACH = list({(s[3], s[4], s[5] > 1): s for s in dense_shapes.ALL if s[2] >= 2048}.values())
+
+
+@pytest.mark.parametrize("M,N,K,f32,kind,splits", ONE_EACH)
+def test_nan_and_infinite_scales_stay_in_their_row_and_column(M, N, K, f32, kind, splits):
+    require_gpu()
+    a, sa, w, sw = _inputs(M, N, K, 1, M + N)
+    out = torch.float32 if f32 else torch.bfloat16
+
+    def run():
+        D = torch.empty(M, N, dtype=out, device=DEV)
+        moe.moe_gemm_fp8(a, sa, w, sw, D, workspace=_ws(M, N, K, 0xFF))
+        return D
+
+    clean = run()
+    rows, cols = [0, M // 2, M - 1], [1, N // 2, N - 1]
+    a[rows[0], K - 1] = 0x7F  # NaN codes, of either sign, in the first and last block
+    a[rows[1], 3] = 0xFF
+    w[cols[0], K - 130] = 0xFF
+    w[cols[1], 0] = 0x7F
+    sa[rows[2], K // 128 - 1] = float("inf")
+    sw[cols[2], 5] = float("nan")
+    d = run()
+    torch.cuda.synchronize()
+    keep_r = torch.ones(M, dtype=torch.bool, device=DEV)
+    keep_c = torch.ones(N, dtype=torch.bool, device=DEV)
+    keep_r[rows], keep_c[cols] = False, False
+    assert not torch.isfinite(d[~keep_r]).any() and torch.isnan(d[:, ~keep_c]).all()
+    assert torch.equal(d[keep_r][:, keep_c], clean[keep_r][:, keep_c])
+
+
 @pytest.mark.parametrize("M", [9, 131, 300, 1100])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 def test_products_that_cancel(M, out):
