@@ -13,8 +13,8 @@
 // and dp[t,r] = <dZ[t], Y[output_index[t,r]]>.
 // One workgroup per token and batch of slots: the token's dZ row is read once per
 // batch, every named row of Y is streamed once and its gradient row written
-// once (nontemporal).  HBM-bound: 8192 x 8 slots x 4096 230 us, 4.96 TB/s, of which 9 us are the table's two kernels
-// (clear, claim); 61 x 8 x 7168 6.7 us, two trips to memory and the launch.
+// once (nontemporal).  HBM-bound: 8192 x 8 slots x 4096 232 us, 4.92 TB/s, of which 10 us are the table's two kernels
+// (clear, claim); 61 x 8 x 7168 6.9 us, two trips to memory and the launch.
 // A row is normally named by one slot (moe_route_pack gives every route a row
 // of its own).  A row named by several slots gets the sum over them in route
 // order: its lowest slot writes it, in fp32 until the one rounding.  Who names a row is

@@ -11,11 +11,10 @@ constexpr int kXcd = 8;
 // K blocks of a workgroup when K is split: whole groups of 4 (a group's scales are copied at once).
 constexpr int split_blocks(int KB, int splits) { return ((KB + 3) / 4 + splits - 1) / splits * 4; }
 
-// Times in us per K block of one round of tiles over the 256 compute units, as
-// measured with the whole chip busy (first: one workgroup per compute unit; second, where two fit: both); the tile with
-// the smallest sum of rounds is taken.  Measured (us, N x K = 4096 x 7168, bf16 output): 256 rows 64x64 22.2, 64x128
-// 29.7, 128x128 40.0; 512 rows 34.3, 30.4, 39.6; 1024 rows 58.9, 51.1, 40.8; 2048 rows 128x128 72.7, 256x256 86; 4096
-// rows 141, 111.
+// Times in us per K block of one round of tiles over the 256 compute units, as measured with the whole chip busy (first: one
+// workgroup per compute unit; second, where two fit: both); the tile with the smallest sum of rounds is taken.  Measured
+// (us, N x K = 4096 x 7168, bf16 output; 64x64, 64x128, 128x128): 256 rows 16.5, 19.4, 26.4; 512 rows 26.5, 22.1, 26.7;
+// 1024 rows 48.3, 42.7, 34.5; 64x128, 128x128, 256x256: 2048 rows 84, 69, 82; 4096 rows 128x128 137, 256x256 104.
 enum Kind { kStream16, kStream32, kStream64, k64x64, k64x128, k128x128, k128x128two, k256x256 };
 struct Plan {
   Kind kind;
