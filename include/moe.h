@@ -641,6 +641,46 @@ moe_status moe_gemm_fp8(const uint8_t* A, int64_t lda, const float* SFA,
 moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx,
                            uint8_t* qt, float* sft, void* stream);
 
+/* ------------------------------------------------------------------------- */
+/* moe_experts_decode: the whole expert layer for a few tokens, in two kernels:
+ * up-projection with SwiGLU, then down-projection with the weighted sum over a
+ * token's slots.  For decode steps, where the reading of the active experts'
+ * weights is all there is: nothing is packed, requantised or sorted in memory.
+ *     h[t,r,j] = silu(sum_k W13[e,j,k] x[t,k]) * (sum_k W13[e,I+j,k] x[t,k]),  e = topk_ids[t,r]
+ *     Z[t,n]   = bf16_rne( sum_r topk_weights[t,r] * (sum_j W2[e,n,j] h[t,r,j]) + C[t,n] )
+ *   accumulated in fp32, the sum over r as an fma chain in slot order; h is
+ *   rounded to bf16 (nearest even) once, as the second product's operand.
+ *   Activations are not quantised.  topk_ids < 0 are skipped silently, ids >= E
+ *   are skipped and flag MOE_DEV_ID_RANGE in *dev_status (NULL: not reported); a
+ *   token whose slots are all skipped gets C, or 0.  An expert named twice by a
+ *   token counts twice.
+ *     x [T, H] bf16; topk_ids [T, k] int32; topk_weights [T, k] fp32;
+ *     C [T, H] bf16 or NULL (a residual, a shared expert's result); Z [T, H]
+ *     bf16, which may be C (or x).
+ *     W13 [E, 2I, H] (gate rows 0..I-1, up rows I..2I-1) and W2 [E, H, I] in
+ *     weight_format:
+ *       MOE_WEIGHTS_BF16  bf16; S13 and S2 NULL
+ *       MOE_WEIGHTS_FP8   E4M3FN codes, S13 [E, 2I/128, H/128] and S2
+ *                         [E, H/128, I/128] fp32, any values (128x128 blocks)
+ *       MOE_WEIGHTS_INT4  4-bit codes as moe_grouped_gemm_int4 takes them,
+ *                         S13 [E, 2I, H/128] and S2 [E, H, I/128] fp16
+ *     weight_format | MOE_WEIGHTS_PACKED: in the orders written by
+ *     moe_pack_weight_bf16 / _fp8 / _int4 (the 4-bit scales too).
+ *   1 <= E <= 1024, 1 <= k <= 64, T <= MOE_DECODE_MAX_TOKENS and
+ *   T * k <= MOE_DECODE_MAX_ROUTES (more: route, pack and use the grouped
+ *   GEMMs); H and I multiples of 128, at most 32768.  x, W13, W2 16-byte, scales
+ *   4-byte aligned.  T == 0 is a no-op.
+ *   workspace: moe_experts_decode_workspace_bytes(T, k, I) bytes (h), 16-byte
+ *   aligned; calls that overlap in time must not share it. */
+enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8 = 1, MOE_WEIGHTS_INT4 = 2 };
+enum { MOE_DECODE_MAX_TOKENS = 128, MOE_DECODE_MAX_ROUTES = 1024 };
+int64_t moe_experts_decode_workspace_bytes(int T, int k, int I);
+moe_status moe_experts_decode(int weight_format, const uint16_t* x, const int32_t* topk_ids,
+                              const float* topk_weights, int T, int k, int E, int H, int I,
+                              const void* W13, const void* S13, const void* W2, const void* S2,
+                              const uint16_t* C, uint16_t* Z, int32_t* dev_status,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
 /* moe_stream_read: a measurement helper, not a step of the method.  Reads the
  * `bytes` bytes at `buf` once with 16-byte nontemporal loads (eight in
  * flight per lane, one 256-lane workgroup per compute unit) and writes an XOR fold

@@ -22,6 +22,10 @@ LAYOUT_MASKED = 1
 WEIGHTS_PACKED = 0x10  # flag for moe_grouped_gemm_fp8's layout: W in moe_pack_weight_fp8 order
 F32, BF16 = 0, 1
 SCORES = {"softmax": 0, "sigmoid": 1}
+# weight formats of moe_experts_decode: (number, type, values per element, type of the scales)
+WEIGHT_FORMATS = {"bf16": (0, torch.bfloat16, 1, None), "fp8": (1, torch.uint8, 1, torch.float32),
+                  "int4": (2, torch.uint8, 2, torch.float16)}
+DECODE_MAX_TOKENS, DECODE_MAX_ROUTES = 128, 1024
 _FLOATS = (torch.float32, torch.bfloat16)
 _CODES = (torch.uint8,)
 DEV_ID_RANGE = 1
@@ -82,6 +86,9 @@ SIGNATURES = {
     "moe_gemm_fp8": (_c_i32, [_vp, _c_i64, _vp, _vp, _c_i64, _vp, ctypes.c_int, _vp, ctypes.c_int, _c_i64,
                               _vp, _c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _c_i64, _vp]),
     "moe_quant_act_t": (_c_i32, [_vp, _c_i64, ctypes.c_int, _c_i64, _vp, _vp, _vp]),
+    "moe_experts_decode_workspace_bytes": (_c_i64, [ctypes.c_int] * 3),
+    "moe_experts_decode": (_c_i32, [ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                    ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
     "moe_stream_read_words": (ctypes.c_int, []),
     "moe_stream_read": (_c_i32, [_vp, _c_i64, _vp, _vp]),
 }
@@ -625,6 +632,46 @@ def moe_quant_act_t(x, q, sf, stream=None):
     qp = _whole(fn, dev, q, "q", torch.uint8, (K, 128 * mb))
     sp = _whole(fn, dev, sf, "sf", torch.float32, (K, mb))
     _check(load().moe_quant_act_t(x.data_ptr(), M, K, ldx, qp, sp, _queue(fn, dev, stream)), fn)
+
+
+def moe_experts_decode_workspace_bytes(T: int, k: int, I: int) -> int:
+    return int(load().moe_experts_decode_workspace_bytes(T, k, I))
+
+
+def moe_experts_decode(x, topk_ids, topk_weights, w13, w2, z, weights: str = "fp8", s13=None, s2=None,
+                       packed: bool = False, residual=None, dev_status=None, workspace=None, stream=None):
+    """The expert layer of a few tokens in two kernels: x bf16 [T, H], topk_ids int32 and topk_weights float32 [T, k] ->
+    z bf16 [T, H] (+ residual, bf16 [T, H], which may be z).  w13 [E, 2I, H] (gate rows, then up rows) and w2 [E, H, I]:
+    weights "bf16"; "fp8", uint8 codes with s13 float32 [E, 2I/128, H/128] and s2 [E, H/128, I/128]; "int4", uint8
+    [..., /2] with s13 float16 [E, 2I, H/128] and s2 [E, H, I/128]; packed: in moe_pack_weight_*'s order.  At most
+    DECODE_MAX_TOKENS tokens and DECODE_MAX_ROUTES routes.  workspace: moe_experts_decode_workspace_bytes(T, k, I) bytes."""
+    fn = "moe_experts_decode"
+    if weights not in WEIGHT_FORMATS:
+        raise ValueError(f"{fn}: weights must be one of {', '.join(WEIGHT_FORMATS)}, got {weights!r}")
+    fmt, wtype, per, stype = WEIGHT_FORMATS[weights]
+    T, H, dev = _shape2(x, "x")
+    k, (E, I2), bf16 = topk_ids.shape[-1], w13.shape[:2], torch.bfloat16
+    I = I2 // 2
+    xp = _whole(fn, dev, x, "x", bf16, (T, H))
+    ids = _whole(fn, dev, topk_ids, "topk_ids", torch.int32, (T, k))
+    p = _whole(fn, dev, topk_weights, "topk_weights", torch.float32, (T, k))
+    a = _whole(fn, dev, w13, "w13", wtype, (E, 2 * I, H // per))
+    b = _whole(fn, dev, w2, "w2", wtype, (E, H, I // per))
+    sa = sb = None
+    if stype is not None:
+        if s13 is None or s2 is None:
+            raise ValueError(f"{fn}: {weights} weights need s13 and s2")
+        gran = 128 if per == 1 else 1
+        sa = _whole(fn, dev, s13, "s13", stype, (E, 2 * I // gran, H // 128))
+        sb = _whole(fn, dev, s2, "s2", stype, (E, H // gran, I // 128))
+    elif s13 is not None or s2 is not None:
+        raise ValueError(f"{fn}: bf16 weights have no scales")
+    zp = _whole(fn, dev, z, "z", bf16, (T, H))
+    c = None if residual is None else _whole(fn, dev, residual, "residual", bf16, (T, H))
+    st = None if dev_status is None else _whole(fn, dev, dev_status, "dev_status", torch.int32, (1,))
+    ws, ws_bytes = _scratch(fn, dev, workspace)
+    _check(load().moe_experts_decode(fmt | (WEIGHTS_PACKED if packed else 0), xp, ids, p, T, k, E, H, I, a, sa, b, sb, c,
+                                     zp, st, ws, ws_bytes, _queue(fn, dev, stream)), fn)
 
 
 def moe_stream_read_words() -> int:

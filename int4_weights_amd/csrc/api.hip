@@ -827,6 +827,65 @@ moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx, uin
   return hip_status(launch_quant_act_t(x, M, K, ldx, qt, sft, (hipStream_t)stream), fn);
 }
 
+int64_t moe_experts_decode_workspace_bytes(int T, int k, int I) {
+  if (T < 0 || T > MOE_DECODE_MAX_TOKENS || k < 1 || k > MOE_MAX_TOPK || T * k > MOE_DECODE_MAX_ROUTES || I < 1 ||
+      I > 32768)
+    return -1;
+  return decode_workspace_bytes(T, k, I);
+}
+
+moe_status moe_experts_decode(int weight_format, const uint16_t* x, const int32_t* topk_ids, const float* topk_weights,
+                              int T, int k, int E, int H, int I, const void* W13, const void* S13, const void* W2,
+                              const void* S2, const uint16_t* C, uint16_t* Z, int32_t* dev_status, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_experts_decode";
+  static_assert(MOE_DECODE_MAX_TOKENS == kDecodeMaxTokens && MOE_DECODE_MAX_ROUTES == kDecodeMaxRoutes, "limits");
+  const int format = weight_format & ~MOE_WEIGHTS_PACKED;
+  if (format < MOE_WEIGHTS_BF16 || format > MOE_WEIGHTS_INT4)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown weight format %d", fn, weight_format);
+  if (T < 0 || k < 1 || k > MOE_MAX_TOPK || E < 1 || E > MOE_MAX_EXPERTS || H < 1 || I < 1)
+    return fail(MOE_ERR_SHAPE, "%s: T=%d k=%d E=%d H=%d I=%d", fn, T, k, E, H, I);
+  if (T > MOE_DECODE_MAX_TOKENS || T * k > MOE_DECODE_MAX_ROUTES)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d tokens of k=%d are more than %d tokens or %d routes: pack them for the grouped GEMMs",
+                fn, T, k, MOE_DECODE_MAX_TOKENS, MOE_DECODE_MAX_ROUTES);
+  if (H % 128 || I % 128 || H > 32768 || I > 32768)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d and I=%d must be multiples of 128, at most 32768", fn, H, I);
+  if (T == 0) return MOE_OK;
+  if (!x || !topk_ids || !topk_weights || !W13 || !W2 || !Z) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (format != MOE_WEIGHTS_BF16 && (!S13 || !S2)) return fail(MOE_ERR_NULL, "%s: this weight format needs S13 and S2", fn);
+  if (format == MOE_WEIGHTS_BF16 && (S13 || S2)) return fail(MOE_ERR_UNSUPPORTED, "%s: bf16 weights have no scales", fn);
+  if (!aligned(x, 16) || !aligned(W13, 16) || !aligned(W2, 16))
+    return fail(MOE_ERR_ALIGN, "%s: x, W13 and W2 must be 16-byte aligned", fn);
+  if (!aligned(S13, 4) || !aligned(S2, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(C, 2) ||
+      !aligned(Z, 2) || !aligned(dev_status, 4))
+    return fail(MOE_ERR_ALIGN, "%s: scales, topk_ids, topk_weights, dev_status, C or Z misaligned", fn);
+  const int64_t need = decode_workspace_bytes(T, k, I);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(MOE_ERR_WORKSPACE, "%s: needs %lld workspace bytes (16-byte aligned), got %lld", fn, (long long)need,
+                (long long)workspace_bytes);
+  DecodeArgs a{};
+  a.format = format;
+  a.packed = (weight_format & MOE_WEIGHTS_PACKED) != 0;
+  a.x = x;
+  a.ids = topk_ids;
+  a.p = topk_weights;
+  a.W13 = W13;
+  a.S13 = S13;
+  a.W2 = W2;
+  a.S2 = S2;
+  a.C = C;
+  a.Z = Z;
+  a.h = (uint16_t*)workspace;
+  a.status = dev_status;
+  a.T = T;
+  a.k = k;
+  a.E = E;
+  a.H = H;
+  a.I = I;
+  return hip_status(launch_experts_decode(a, (hipStream_t)stream), fn);
+}
+
 int moe_stream_read_words(void) { return stream_read_grid(); }
 
 moe_status moe_stream_read(const void* buf, int64_t bytes, uint32_t* out, void* stream) {

@@ -167,4 +167,23 @@ struct DenseArgs {
 int64_t dense_workspace_bytes(int M, int N, int K);
 hipError_t launch_gemm_dense(const DenseArgs& a, hipStream_t s);
 
+constexpr int kDecodeMaxTokens = 128, kDecodeMaxRoutes = 1024;
+struct DecodeArgs {
+  int format;            // 0 bf16, 1 FP8, 2 4-bit
+  int packed;            // weights (and 4-bit scales) in the fragment-packed orders
+  const uint16_t* x;     // bf16 [T, H]
+  const int32_t* ids;    // [T, k]
+  const float* p;        // [T, k]
+  const void *W13, *S13; // [E, 2I, H]: gate rows, then up rows
+  const void *W2, *S2;   // [E, H, I]
+  const uint16_t* C;     // bf16 [T, H] or nullptr
+  uint16_t* Z;           // bf16 [T, H]
+  uint16_t* h;           // workspace: bf16 [T * k, I]
+  int32_t* status;       // or nullptr
+  int T, k, E, H, I;
+  int ksplit;            // shares of I in the down-projection
+};
+int64_t decode_workspace_bytes(int T, int k, int I);
+hipError_t launch_experts_decode(const DecodeArgs& a, hipStream_t s);
+
 }  // namespace moe
