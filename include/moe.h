@@ -21,6 +21,9 @@
  * uses, or of any projection; arbitrary fp32 block scales); and for training
  * the gradients moe_unpermute_combine_bwd, moe_router_topk_bwd, and
  * moe_quant_act_t, which prepares the operands of moe_gemm_fp8's weight gradient;
+ * moe_gemm_bf16, a dense bf16 product with bias, activation and residual in its
+ * epilogue, with moe_act_bwd for its gradient; and for decode steps
+ * moe_experts_decode, the whole expert layer of a few tokens in two kernels;
  *
  * plus weight-preparation calls (moe_quant_weight_fp8 / _int4 / _fp4 / _int8,
  * moe_pack_weight_fp8 / _int4 / _fp4 / _bf16) that turn bf16 expert weights
@@ -680,6 +683,74 @@ moe_status moe_experts_decode(int weight_format, const uint16_t* x, const int32_
                               const void* W13, const void* S13, const void* W2, const void* S2,
                               const uint16_t* C, uint16_t* Z, int32_t* dev_status,
                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Activations, each with its fp32 formula; MOE_ACT_GATED is ORed to one. */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,      /* v / (1 + exp(-v)); gated: SwiGLU            */
+  MOE_ACT_GELU = 3,      /* v * Phi(v), Phi the normal distribution     */
+  MOE_ACT_GELU_TANH = 4, /* v / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3) */
+  MOE_ACT_GATED = 0x10   /* the product's first N/2 columns are gates, the others what they gate */
+};
+
+/* moe_gemm_bf16: dense bf16 product with bias, activation and residual in its
+ * epilogue, each value rounded once; the products of its gradient; and products
+ * in general.  (A router's gate projection with fp32 logits for
+ * moe_router_topk; the expert that every token uses, added to the routed ones'
+ * result; projections.)
+ *     v[m, n] = sum_k a[m, k] w[n, k] + bias[n],  fp32
+ *     D[m, n] = act(v[m, n]) + C[m, n]                                    n < N
+ *     gated:  D[m, j] = act(v[m, j]) * v[m, N/2 + j] + C[m, j]            j < N/2
+ *     pre[m, n] = bf16_rne(v[m, n])      (for moe_act_bwd; NULL: not kept)
+ *     A [M, K] bf16, or with transpose MOE_TRANS_A stored as [K, M]; W [N, K],
+ *       or with MOE_TRANS_W stored as [K, N]; rows lda, ldw elements apart.
+ *       Forward: transpose 0.  Input gradient dX [M, K] = dP W: A dP, W the
+ *       weight as it is stored, MOE_TRANS_W.  Weight gradient dW [N, K] += dP^T X:
+ *       A dP, W X, MOE_TRANS_A | MOE_TRANS_W, C and D the fp32 gradient.
+ *       MOE_TRANS_A comes with MOE_TRANS_W only, a gated epilogue with neither.
+ *     D bf16 or fp32 (out_type), rows ldd apart; nothing past its last column is
+ *       written.  bias [N] fp32 or bf16 (bias_type) or NULL.  C of D's shape,
+ *       fp32 or bf16 (c_type), rows ldc apart, or NULL; C may be D itself (with
+ *       the same type and stride).  pre [M, N] bf16, rows ldp apart.
+ *   Requires lda and ldw multiples of 8 and below 2^22, A and W 16-byte aligned,
+ *   the others aligned to their type; the contiguous dimension of each operand a
+ *   multiple of 8 (K; with MOE_TRANS_A M, with MOE_TRANS_W N), the others any;
+ *   gated: N even, N/2 * ldw < 2^30 - 2^28; M and N <= 2^26 and ceil(M/64) * ceil(N/64) <
+ *   2^24.  M == 0 is a no-op; K == 0 is a product of zeros (A and W are
+ *   not looked at).
+ *   D and pre must not overlap the inputs (but D = C) or each other.
+ *   workspace: at least moe_gemm_bf16_workspace_bytes(M, N, K) bytes, 16-byte
+ *   aligned (may be NULL when that is 0; it is not 0 only where few output tiles
+ *   make it pay to split K); calls that overlap in time must not share it. */
+enum { MOE_TRANS_A = 1, MOE_TRANS_W = 2 };
+int64_t moe_gemm_bf16_workspace_bytes(int M, int N, int K);
+moe_status moe_gemm_bf16(const uint16_t* A, int64_t lda, const uint16_t* W, int64_t ldw, int transpose,
+                         void* D, int out_type, int64_t ldd, const void* bias, int bias_type, int act,
+                         const void* C, int c_type, int64_t ldc, uint16_t* pre, int64_t ldp,
+                         int M, int N, int K, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* moe_act_bwd: the gradient of moe_gemm_bf16's activation and bias (C's is dD).
+ *     dP[m, n]  = bf16_rne( dD[m, n] * act'(pre[m, n]) )
+ *     gated:      dP[m, j] = dD[m, j] * act'(pre[m, j]) * pre[m, N/2 + j],
+ *                 dP[m, N/2 + j] = dD[m, j] * act(pre[m, j])
+ *     dbias[n] (+)= sum_m of dP's column n before its rounding, in fp32
+ *   dP is what the input's and weight's gradients start from (moe_gemm_bf16).
+ *     dD [M, N] (gated [M, N/2]), pre and dP [M, N] bf16, rows ldd, ldp, ldo
+ *     elements apart; dbias [N] fp32, added to what it holds if accumulate.
+ *   dP or dbias may be NULL, but not both; pre is not read (may be NULL) for
+ *   MOE_ACT_NONE without MOE_ACT_GATED.  dP may be dD (not gated, same stride)
+ *   or pre (same stride).  ReLU's slope at 0 is 0.
+ *   Requires N % 8 == 0 (gated: N % 16 == 0), strides multiples of 8, dD, pre and
+ *   dP 16-byte, dbias 4-byte aligned; M, N <= 2^26.  M == 0 writes dbias = 0 (unless
+ *   accumulate).  workspace: moe_act_bwd_workspace_bytes(M, N) bytes, 16-byte
+ *   aligned (NULL when that is 0, or when dbias is); calls that overlap in time
+ *   must not share it. */
+int64_t moe_act_bwd_workspace_bytes(int M, int N);
+moe_status moe_act_bwd(const uint16_t* dD, int64_t ldd, const uint16_t* pre, int64_t ldp, int act,
+                       uint16_t* dP, int64_t ldo, float* dbias, int accumulate, int M, int N,
+                       void* workspace, int64_t workspace_bytes, void* stream);
 
 /* moe_stream_read: a measurement helper, not a step of the method.  Reads the
  * `bytes` bytes at `buf` once with 16-byte nontemporal loads (eight in

@@ -25,6 +25,9 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 # weight formats of moe_experts_decode: (number, type, values per element, type of the scales)
 WEIGHT_FORMATS = {"bf16": (0, torch.bfloat16, 1, None), "fp8": (1, torch.uint8, 1, torch.float32),
                   "int4": (2, torch.uint8, 2, torch.float16)}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_GATED, _TRANS_A, _TRANS_W = 0x10, 1, 2
+_BF16S = (torch.bfloat16,)
 DECODE_MAX_TOKENS, DECODE_MAX_ROUTES = 128, 1024
 _FLOATS = (torch.float32, torch.bfloat16)
 _CODES = (torch.uint8,)
@@ -89,6 +92,13 @@ SIGNATURES = {
     "moe_experts_decode_workspace_bytes": (_c_i64, [ctypes.c_int] * 3),
     "moe_experts_decode": (_c_i32, [ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                     ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
+    "moe_gemm_bf16_workspace_bytes": (_c_i64, [ctypes.c_int] * 3),
+    "moe_gemm_bf16": (_c_i32, [_vp, _c_i64, _vp, _c_i64, ctypes.c_int, _vp, ctypes.c_int, _c_i64, _vp, ctypes.c_int,
+                               ctypes.c_int, _vp, ctypes.c_int, _c_i64, _vp, _c_i64, ctypes.c_int, ctypes.c_int,
+                               ctypes.c_int, _vp, _c_i64, _vp]),
+    "moe_act_bwd_workspace_bytes": (_c_i64, [ctypes.c_int] * 2),
+    "moe_act_bwd": (_c_i32, [_vp, _c_i64, _vp, _c_i64, ctypes.c_int, _vp, _c_i64, _vp, ctypes.c_int, ctypes.c_int,
+                             ctypes.c_int, _vp, _c_i64, _vp]),
     "moe_stream_read_words": (ctypes.c_int, []),
     "moe_stream_read": (_c_i32, [_vp, _c_i64, _vp, _vp]),
 }
@@ -672,6 +682,71 @@ def moe_experts_decode(x, topk_ids, topk_weights, w13, w2, z, weights: str = "fp
     ws, ws_bytes = _scratch(fn, dev, workspace)
     _check(load().moe_experts_decode(fmt | (WEIGHTS_PACKED if packed else 0), xp, ids, p, T, k, E, H, I, a, sa, b, sb, c,
                                      zp, st, ws, ws_bytes, _queue(fn, dev, stream)), fn)
+
+
+def _act(fn, act, gated) -> int:
+    if act not in ACTS:
+        raise ValueError(f"{fn}: act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act] | (_GATED if gated else 0)
+
+
+def moe_gemm_bf16_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().moe_gemm_bf16_workspace_bytes(M, N, K))
+
+
+def moe_gemm_bf16(A, W, D, bias=None, act: str = "none", gated: bool = False, C=None, pre=None, trans_a: bool = False,
+                  trans_w: bool = False, workspace=None, stream=None):
+    """D = C + act(A W^T + bias): A bf16 [M, K] (trans_a: stored as [K, M]), W bf16 [N, K] (trans_w: [K, N]), D bf16 or
+    float32 [M, N], bias float32 or bf16 [N], C of D's shape, float32 or bf16 (may be D), pre bf16 [M, N] receives the
+    product plus bias.  act "none", "relu", "silu", "gelu" or "gelu_tanh"; gated: W's rows are gates, then what they gate,
+    D = C + act(v[:, :N/2]) * v[:, N/2:], of N/2 columns.  Rows may be strided.  Input gradient: moe_gemm_bf16(dP, W, dX,
+    trans_w=True); weight gradient: moe_gemm_bf16(dP, X, dW, C=dW, trans_a=True, trans_w=True).  workspace:
+    moe_gemm_bf16_workspace_bytes(M, N, K) bytes."""
+    fn = "moe_gemm_bf16"
+    a0, a1, dev = _shape2(A, "A")
+    w0, w1 = W.shape
+    (M, K), N = ((a1, a0) if trans_a else (a0, a1)), (w1 if trans_w else w0)
+    lda = _rows(fn, dev, A, "A", _BF16S, (a0, a1))
+    ldw = _rows(fn, dev, W, "W", _BF16S, (K, N) if trans_w else (N, K))
+    out = (M, N // 2 if gated else N)
+    ldd = _rows(fn, dev, D, "D", _FLOATS, out)
+    b, btype = (None, 0)
+    if bias is not None:
+        b, btype = _whole(fn, dev, bias, "bias", bias.dtype, (N,)), _float_type("bias", bias)
+    c, ctype, ldc = (None, 0, 0) if C is None else (C.data_ptr(), _float_type("C", C), _rows(fn, dev, C, "C", _FLOATS, out))
+    p, ldp = (None, 0) if pre is None else (pre.data_ptr(), _rows(fn, dev, pre, "pre", _BF16S, (M, N)))
+    ws, ws_bytes = _scratch(fn, dev, workspace)
+    _check(load().moe_gemm_bf16(A.data_ptr(), lda, W.data_ptr(), ldw, (_TRANS_A if trans_a else 0) | (_TRANS_W if trans_w else 0),
+                                D.data_ptr(), _float_type("D", D), ldd, b, btype, _act(fn, act, gated), c, ctype, ldc, p,
+                                ldp, M, N, K, ws, ws_bytes, _queue(fn, dev, stream)), fn)
+
+
+def _float_type(name, t) -> int:
+    if t.dtype not in _FLOATS:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return BF16 if t.dtype is torch.bfloat16 else F32
+
+
+def moe_act_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(load().moe_act_bwd_workspace_bytes(M, N))
+
+
+def moe_act_bwd(dD, pre, dP, dbias=None, act: str = "none", gated: bool = False, accumulate: bool = False, workspace=None,
+                stream=None):
+    """The gradient of moe_gemm_bf16's activation and bias: dD bf16 [M, N] (gated [M, N/2]) and pre bf16 [M, N] -> dP bf16
+    [M, N] and dbias float32 [N] (added to, if accumulate); either may be None.  pre may be None for act "none" without
+    gated.  Rows may be strided.  workspace: moe_act_bwd_workspace_bytes(M, N) bytes (with dbias)."""
+    fn = "moe_act_bwd"
+    M, half, dev = _shape2(dD, "dD")
+    N = 2 * half if gated else half
+    code = _act(fn, act, gated)
+    ldd = _rows(fn, dev, dD, "dD", _BF16S, (M, half))
+    p, ldp = (None, 0) if pre is None else (pre.data_ptr(), _rows(fn, dev, pre, "pre", _BF16S, (M, N)))
+    o, ldo = (None, 0) if dP is None else (dP.data_ptr(), _rows(fn, dev, dP, "dP", _BF16S, (M, N)))
+    b = None if dbias is None else _whole(fn, dev, dbias, "dbias", torch.float32, (N,))
+    ws, ws_bytes = _scratch(fn, dev, workspace)
+    _check(load().moe_act_bwd(dD.data_ptr(), ldd, p, ldp, code, o, ldo, b, int(accumulate), M, N, ws, ws_bytes,
+                              _queue(fn, dev, stream)), fn)
 
 
 def moe_stream_read_words() -> int:

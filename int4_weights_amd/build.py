@@ -17,7 +17,7 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.hip", "quant.hip", "route.hip", "gemm_fp8.hip", "gemm_int4.hip", "gemm_bf16.hip", "gemm_fp4.hip",
            "gemm_int8.hip", "swiglu.hip", "combine.hip", "router.hip", "gemm_dense.hip", "stream.hip",
-           "decode.hip"]
+           "decode.hip", "gemm_linear.hip", "act_bwd.hip"]
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 

@@ -886,6 +886,131 @@ moe_status moe_experts_decode(int weight_format, const uint16_t* x, const int32_
   return hip_status(launch_experts_decode(a, (hipStream_t)stream), fn);
 }
 
+static bool act_ok(int act) {
+  const int f = act & ~MOE_ACT_GATED;
+  return f >= MOE_ACT_NONE && f <= MOE_ACT_GELU_TANH;
+}
+// A launch has fewer than 2^32 threads: tiles of 64x64 or more have 256 threads, or 512 for twice the area; few rows take 512
+// threads per 16 columns.
+static bool linear_size_ok(int M, int N, int K) {
+  return M >= 0 && M <= (1 << 26) && N >= 1 && N <= (1 << 26) && K >= 0 && K <= (1 << 30) &&
+         (int64_t)((M + 63) / 64) * ((N + 63) / 64) < (1 << 24);
+}
+
+int64_t moe_gemm_bf16_workspace_bytes(int M, int N, int K) {
+  return linear_size_ok(M, N, K) ? linear_workspace_bytes(M, N, K) : -1;
+}
+
+moe_status moe_gemm_bf16(const uint16_t* A, int64_t lda, const uint16_t* W, int64_t ldw, int transpose, void* D,
+                         int out_type, int64_t ldd, const void* bias, int bias_type, int act, const void* C, int c_type,
+                         int64_t ldc, uint16_t* pre, int64_t ldp, int M, int N, int K, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_gemm_bf16";
+  if (M < 0 || N < 1 || K < 0) return fail(MOE_ERR_SHAPE, "%s: M=%d N=%d K=%d", fn, M, N, K);
+  if (!linear_size_ok(M, N, K)) return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d x N=%d (K=%d) is too large", fn, M, N, K);
+  if (transpose != 0 && transpose != MOE_TRANS_W && transpose != (MOE_TRANS_A | MOE_TRANS_W))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: transpose=%d must be 0, MOE_TRANS_W or MOE_TRANS_A | MOE_TRANS_W", fn, transpose);
+  const bool ta = transpose & MOE_TRANS_A, tw = transpose & MOE_TRANS_W, gated = act & MOE_ACT_GATED;
+  if (!act_ok(act)) return fail(MOE_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, act);
+  if (gated && (tw || N % 2))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: a gated activation needs an even N (%d) and operands as in the forward product", fn, N);
+  for (int t : {out_type, bias ? bias_type : 0, C ? c_type : 0})
+    if (t != MOE_F32 && t != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: unknown element type %d", fn, t);
+  if ((!ta || !tw) && K % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 8", fn, K);
+  if (ta && M % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d is not a multiple of 8 (transposed A)", fn, M);
+  if (tw && N % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d is not a multiple of 8 (transposed W)", fn, N);
+  const int NO = gated ? N / 2 : N;
+  if ((K > 0 && (lda < (ta ? M : K) || ldw < (tw ? N : K))) || ldd < NO || (C && ldc < NO) || (pre && ldp < N))
+    return fail(MOE_ERR_SHAPE, "%s: a row stride is shorter than its row", fn);
+  if (K > 0 && (lda >= (1 << 22) || ldw >= (1 << 22)))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: lda and ldw must be below 2^22", fn);
+  if (gated && K > 0 && (int64_t)NO * ldw >= (1 << 30) - (1 << 28))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: a gated product's weight is too large", fn);
+  if (M == 0) return MOE_OK;
+  if ((K > 0 && (!A || !W)) || !D) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (K > 0 && (!aligned(A, 16) || !aligned(W, 16) || lda % 8 || ldw % 8))
+    return fail(MOE_ERR_ALIGN, "%s: A and W must be 16-byte aligned, lda and ldw multiples of 8", fn);
+  if (!aligned(D, out_type == MOE_F32 ? 4 : 2) || !aligned(bias, bias_type == MOE_F32 ? 4 : 2) ||
+      !aligned(C, c_type == MOE_F32 ? 4 : 2) || !aligned(pre, 2))
+    return fail(MOE_ERR_ALIGN, "%s: D, bias, C and pre must be aligned to their type", fn);
+  if (C == D && (ldc != ldd || c_type != out_type)) return fail(MOE_ERR_SHAPE, "%s: C is D but of another type or stride", fn);
+  const int64_t need = linear_workspace_bytes(M, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(MOE_ERR_WORKSPACE, "%s: needs %lld workspace bytes (16-byte aligned), got %lld", fn, (long long)need,
+                (long long)workspace_bytes);
+  LinearArgs a{};
+  a.A = A;
+  a.lda = lda;
+  a.W = W;
+  a.ldw = ldw;
+  a.ta = ta;
+  a.tw = tw;
+  a.D = D;
+  a.ldd = ldd;
+  a.d_f32 = out_type == MOE_F32;
+  a.bias = bias;
+  a.bias_f32 = bias_type == MOE_F32;
+  a.act = act & ~MOE_ACT_GATED;
+  a.gated = gated;
+  a.C = C;
+  a.ldc = ldc;
+  a.c_f32 = c_type == MOE_F32;
+  a.pre = pre;
+  a.ldp = ldp;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.ws = need > 0 ? (float*)workspace : nullptr;
+  return hip_status(launch_linear(a, (hipStream_t)stream), fn);
+}
+
+int64_t moe_act_bwd_workspace_bytes(int M, int N) {
+  if (M < 0 || M > (1 << 26) || N < 1 || N > (1 << 26)) return -1;
+  return act_bwd_workspace_bytes(M, N);
+}
+
+moe_status moe_act_bwd(const uint16_t* dD, int64_t ldd, const uint16_t* pre, int64_t ldp, int act, uint16_t* dP,
+                       int64_t ldo, float* dbias, int accumulate, int M, int N, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "moe_act_bwd";
+  if (M < 0 || N < 1) return fail(MOE_ERR_SHAPE, "%s: M=%d N=%d", fn, M, N);
+  if (M > (1 << 26) || N > (1 << 26)) return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d x N=%d is too large", fn, M, N);
+  if (!act_ok(act)) return fail(MOE_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, act);
+  const bool gated = act & MOE_ACT_GATED, reads = act != MOE_ACT_NONE;
+  if (N % (gated ? 16 : 8)) return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d is not a multiple of %d", fn, N, gated ? 16 : 8);
+  if (!dP && !dbias) return fail(MOE_ERR_NULL, "%s: neither dP nor dbias", fn);
+  if (M > 0 && (!dD || (reads && !pre))) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
+  if (ldd < (gated ? N / 2 : N) || (reads && ldp < N) || (dP && ldo < N))
+    return fail(MOE_ERR_SHAPE, "%s: a row stride is shorter than its row", fn);
+  if (!aligned(dD, 16) || !aligned(dP, 16) || !aligned(dbias, 4) || ldd % 8 || (dP && ldo % 8) ||
+      (reads && (!aligned(pre, 16) || ldp % 8)))
+    return fail(MOE_ERR_ALIGN, "%s: dD, pre and dP (and their strides) must be 16-byte, dbias 4-byte aligned", fn);
+  if ((dP == dD && dP && (gated || ldo != ldd)) || (reads && dP == pre && dP && ldo != ldp))
+    return fail(MOE_ERR_SHAPE, "%s: dP is an input of another shape or stride", fn);
+  const int64_t need = dbias ? act_bwd_workspace_bytes(M, N) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(MOE_ERR_WORKSPACE, "%s: needs %lld workspace bytes (16-byte aligned), got %lld", fn, (long long)need,
+                (long long)workspace_bytes);
+  if (M == 0 && (!dbias || accumulate)) return MOE_OK;
+  ActBwdArgs a{};
+  a.dD = dD;
+  a.ldd = ldd;
+  a.pre = pre;
+  a.ldp = ldp;
+  a.dP = dP;
+  a.ldo = ldo;
+  a.dbias = dbias;
+  a.accumulate = accumulate != 0;
+  a.act = act & ~MOE_ACT_GATED;
+  a.gated = gated;
+  a.M = M;
+  a.N = N;
+  a.ws = need > 0 ? (float*)workspace : nullptr;
+  return hip_status(launch_act_bwd(a, (hipStream_t)stream), fn);
+}
+
 int moe_stream_read_words(void) { return stream_read_grid(); }
 
 moe_status moe_stream_read(const void* buf, int64_t bytes, uint32_t* out, void* stream) {

@@ -17,6 +17,7 @@
 // waves share; persistent workgroups walk over the units.  Down-projection: a workgroup owns 16 columns of Z and takes every
 // job, its waves in turn; the rows' sums meet in LDS as one line per route, so the sum over a token's slots runs in slot order
 // whatever wave was first, and no partial result goes through memory.
+#include "linear_act.h"
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void decode_up_kernel(const DecodeAr
           g += part[buf][v][row][c];
           up += part[buf][v][row][kCols + c];
         }
-        a.h[(int64_t)clist[row] * a.I + col + c] = (uint16_t)f32_to_bf16_rne(silu_f32(g) * up);
+        a.h[(int64_t)clist[row] * a.I + col + c] = (uint16_t)f32_to_bf16_rne(silu_any(g) * up);
       }
     }
   }

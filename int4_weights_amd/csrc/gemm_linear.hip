@@ -1,0 +1,498 @@
+// gemm_linear.hip -- moe_gemm_bf16: a dense bf16 product with bias, activation and residual in its epilogue, and the
+// products of its gradient.
+//
+//   D[m, n] = C[m, n] + act( sum_k a[m, k] w[n, k] + bias[n] )
+//   gated:    D[m, j] = C[m, j] + act(v[m, j]) * v[m, N/2 + j],   v = the product plus bias, w's rows gate then up
+//
+// Operands come in the order they are stored in: rows with K contiguous, or (ta, tw) rows of one k with m (n) contiguous, as
+// the gradients' products need them: dX = dP W has W's n as its k, dW = dP^T X contracts over the tokens.  No transpose goes
+// through memory: both orders are copied global -> LDS as they lie, and a fragment of the second order is read with
+// ds_read_b64_tr_b16, which hands 16 lanes the columns of 4 rows.
+//
+// Tile.  A workgroup of WM x WN waves computes 16 RB WM rows x 16 CB WN columns, 64 K values a step.  w is the matrix
+// instruction's A operand (output columns), a its B operand (rows), so a lane holds 4 consecutive columns of one row, and the
+// epilogue sees each value in fp32 once.  Copies are buffer loads into the LDS, whose range check turns what lies outside the
+// matrices (rows, columns, the last K block's rest) into zeros.
+#include "linear_act.h"
+#include "linear_plan.h"
+#include "moe_device.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer: its copy writes zeros
+constexpr int kXcds8 = 8;
+
+__device__ __forceinline__ void barrier_reads() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), which the compiler sees
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// 64 lanes x 16 bytes global -> LDS, lane i's from base + voff to lds + 16 i; offsets from 2^31 on write zeros.
+__device__ __forceinline__ void copy16(uint32_t voff, const void* base, uint32_t lds) {
+  const uint64_t b = (uint64_t)base;
+  const v4i r = {(int)(uint32_t)b, (int)(uint32_t)(b >> 32) & 0xffff, 0x7fffffff, 0x00020000};
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r), "{m0}"(lds) : "memory");
+}
+
+__device__ __forceinline__ v4f mma(const v8bf w, const v8bf x, const v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
+}
+
+// -------------------------------------------------------------- epilogue --
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t v2u_any __attribute__((ext_vector_type(2), aligned(2)));
+
+__device__ __forceinline__ v2u_any bf16x4(const v4f v) {
+  return v2u_any{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16), f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
+}
+// Elements at .. at + 3 (cnt of them are there) of an fp32 or bf16 row.
+__device__ __forceinline__ v4f load4(const void* p, bool f32, int64_t at, int cnt) {
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  if (f32) {
+    const float* q = (const float*)p + at;
+    if (cnt == 4) return *(const v4f_any*)q;
+    for (int i = 0; i < cnt; ++i) v[i] = q[i];
+  } else {
+    const uint16_t* q = (const uint16_t*)p + at;
+    if (cnt == 4) {
+      const v2u_any u = *(const v2u_any*)q;
+      return v4f{bf16_to_f32(u[0] & 0xffffu), bf16_to_f32(u[0] >> 16), bf16_to_f32(u[1] & 0xffffu), bf16_to_f32(u[1] >> 16)};
+    }
+    for (int i = 0; i < cnt; ++i) v[i] = bf16_to_f32(q[i]);
+  }
+  return v;
+}
+__device__ __forceinline__ void store4(void* p, bool f32, int64_t at, int cnt, const v4f v) {
+  if (f32) {
+    float* q = (float*)p + at;
+    if (cnt == 4) *(v4f_any*)q = v;
+    else
+      for (int i = 0; i < cnt; ++i) q[i] = v[i];
+  } else {
+    uint16_t* q = (uint16_t*)p + at;
+    if (cnt == 4) *(v2u_any*)q = bf16x4(v);
+    else
+      for (int i = 0; i < cnt; ++i) q[i] = (uint16_t)f32_to_bf16_rne(v[i]);
+  }
+}
+
+// Columns n .. n + 3 of row m; NO: how many columns D has.  v: the product (gated: gate and up).
+template <bool GATED>
+__device__ __forceinline__ void epilogue4(const LinearArgs& a, int m, int n, v4f v, v4f up) {
+  const int NO = GATED ? a.N / 2 : a.N;
+  if (m >= a.M || n >= NO) return;
+  const int cnt = min(4, NO - n);
+  if (a.bias) {
+    v += load4(a.bias, a.bias_f32, n, cnt);
+    if (GATED) up += load4(a.bias, a.bias_f32, NO + n, cnt);
+  }
+  if (a.pre) {
+    store4(a.pre, false, (int64_t)m * a.ldp + n, cnt, v);
+    if (GATED) store4(a.pre, false, (int64_t)m * a.ldp + NO + n, cnt, up);
+  }
+  v = act4(a.act, v);
+  if (GATED) v *= up;
+  if (a.C) v += load4(a.C, a.c_f32, (int64_t)m * a.ldc + n, cnt);
+  store4(a.D, a.d_f32, (int64_t)m * a.ldd + n, cnt, v);
+}
+
+// Split K: this share's sums, in rows of ws_cols() floats (gated: the up columns begin at half of them).
+__host__ __device__ inline int ws_half(const LinearArgs& a) { return ((a.gated ? a.N / 2 : a.N) + 3) & ~3; }
+__host__ __device__ inline int ws_cols(const LinearArgs& a) { return a.gated ? 2 * ws_half(a) : ws_half(a); }
+
+template <bool GATED>
+__device__ __forceinline__ void finish4(const LinearArgs& a, int m, int n, const v4f v, const v4f up) {
+  if (a.splits == 1) return epilogue4<GATED>(a, m, n, v, up);
+  const int half = ws_half(a);
+  if (m >= a.M || n >= half) return;
+  float* w = a.ws + ((int64_t)blockIdx.y * a.M + m) * ws_cols(a) + n;
+  *(v4f*)w = v;
+  if (GATED) *(v4f*)(w + half) = up;
+}
+
+// ---------------------------------------------------------------- operand --
+// One operand's B rows (m or n) x 64 K values in LDS, B * 128 bytes, and its copies.
+// K contiguous: row r at 128 r, its 16-byte chunk c at position c ^ ((r >> 1) & 7).
+// TR: row k at 2 B k, its 32-byte segment s at position s ^ f(k); f takes the 8 rows that 32 lanes read at once to 8 places.
+template <bool TR, int B>
+struct Operand {
+  static constexpr int kRowsPerCopy = TR ? 512 / B : 8;
+  __device__ static __forceinline__ int f(int k) {
+    return B == 64 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
+  }
+  // this lane's place in copy q: k offset within the step, and the row (m or n) in the tile
+  __device__ static __forceinline__ void place(int q, int lane, int& k, int& row) {
+    if (TR) {
+      k = kRowsPerCopy * q + lane / (B / 8);
+      const int pos = lane % (B / 8);
+      row = ((pos >> 1) ^ f(k)) * 16 + (pos & 1) * 8;
+    } else {
+      row = 8 * q + (lane >> 3);
+      k = 8 * ((lane & 7) ^ ((row >> 1) & 7));
+    }
+  }
+  // byte offset of that place from the tile's first element
+  __device__ static __forceinline__ uint32_t offset(int k, int row, int64_t ld) {
+    return 2u * (TR ? (uint32_t)k * (uint32_t)ld + (uint32_t)row : (uint32_t)row * (uint32_t)ld + (uint32_t)k);
+  }
+  // fragment reads: block blk of 16 rows, half h of the step
+  int o0, o1;
+  __device__ __forceinline__ void init(int lane, int first_blk) {
+    const int i = lane & 15, g = lane >> 4;
+    if (TR) {
+      const int k = 8 * g + (i >> 2);
+      o0 = k * 2 * B + 8 * (i & 3);
+      o1 = (first_blk ^ f(k)) * 32;
+    } else {
+      const int sw = (i >> 1) & 7;
+      o0 = first_blk * 2048 + i * 128 + 16 * (g ^ sw);
+      o1 = first_blk * 2048 + i * 128 + 16 * ((4 + g) ^ sw);
+    }
+  }
+  // blk counts from first_blk, which is a multiple of the wave's blocks (a power of two), so that it can be xor-ed
+  __device__ __forceinline__ v8bf frag(const uint8_t* s, int blk, int h) const {
+    if constexpr (TR) {
+      typedef short v4s __attribute__((ext_vector_type(4)));
+      typedef short v8s __attribute__((ext_vector_type(8)));
+      const uint8_t* p = s + o0 + (o1 ^ (blk * 32)) + h * 64 * B;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p + 8 * B));
+      return __builtin_bit_cast(v8bf, v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    } else {
+      return __builtin_bit_cast(v8bf, *(const v4i*)(s + (h ? o1 : o0) + blk * 2048));
+    }
+  }
+};
+
+// ------------------------------------------------------------------- tile --
+template <int RB, int CB, int WM, int WN, int S>
+struct LinCfg {
+  static constexpr int NW = WM * WN, BM = 16 * RB * WM, BN = 16 * CB * WN;
+  static constexpr int kCopies = (BM + BN) / 8, kPw = kCopies / NW;
+  static constexpr int kSlot = (BM + BN) * 128, kLds = S * kSlot;
+  static_assert(kCopies % NW == 0 && kLds <= 160 * 1024 && (S - 1) * kPw < 64, "copies in equal shares; LDS; vmcnt");
+};
+
+template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN, int S>
+struct LinTileT {
+  using C = LinCfg<RB, CB, WM, WN, S>;
+  static_assert(!GATED || (!TW && CB % 2 == 0), "gate and up blocks in turn");
+  const LinearArgs& a;
+  uint8_t* sm;
+  uint32_t lds0;
+  int lane, wv, l16, lg, KB, kb0, kb1, m0, n0, wm, wn;  // n0: first column of D
+  const uint8_t *abase, *wbase;
+  uint32_t voff[C::kPw];
+  Operand<TA, C::BM> xa;
+  Operand<TW, C::BN> xw;
+
+  __device__ __forceinline__ LinTileT(const LinearArgs& args, uint8_t* smem) : a(args), sm(smem) {
+    lane = lane_id();
+    wv = uniform(threadIdx.x >> 6);
+    l16 = lane & 15;
+    lg = lane >> 4;
+    lds0 = lds_offset(sm);
+    KB = (a.K + 63) / 64;
+    const int per = lin_split_blocks(KB, a.splits);
+    kb0 = uniform(min((int)blockIdx.y * per, KB));
+    kb1 = uniform(min(kb0 + per, KB));
+    // Workgroup b runs on XCD b % 8: consecutive tiles go to one XCD, and consecutive tiles are blocks of up to 8 column
+    // tiles by a few row tiles, so an XCD's workgroups share both operands in its L2.
+    const int NO = GATED ? a.N / 2 : a.N, BNO = GATED ? C::BN / 2 : C::BN;
+    const int mt = (a.M + C::BM - 1) / C::BM, nt = (NO + BNO - 1) / BNO, tiles = mt * nt;
+    const int share = tiles / kXcds8, rem = tiles % kXcds8, x = blockIdx.x % kXcds8;
+    const int t = x * share + min(x, rem) + blockIdx.x / kXcds8;
+    const int gn = 8, g = t / (mt * gn), gw = min(gn, nt - g * gn), r = t - g * mt * gn;
+    m0 = uniform(r / gw * C::BM);
+    n0 = uniform((g * gn + r % gw) * BNO);
+    wm = (wv / WN) * 16 * RB;
+    wn = (wv % WN) * 16 * CB;
+    abase = (const uint8_t*)(a.A + (TA ? (int64_t)m0 : m0 * a.lda)) + (int64_t)kb0 * astep();
+    wbase = (const uint8_t*)(a.W + (TW ? (int64_t)n0 : n0 * a.ldw)) + (int64_t)kb0 * wstep();
+#pragma unroll
+    for (int i = 0; i < C::kPw; ++i) {
+      int k, row;
+      voff[i] = where(i, k, row);
+    }
+    xa.init(lane, wm / 16);
+    xw.init(lane, wn / 16);
+  }
+  __device__ __forceinline__ int64_t astep() const { return TA ? 128 * a.lda : 128; }
+  __device__ __forceinline__ int64_t wstep() const { return TW ? 128 * a.ldw : 128; }
+  // copy i of this wave: this lane's k and row, and its offset (kOut where the matrix has no such row)
+  __device__ __forceinline__ uint32_t where(int i, int& k, int& row) const {
+    const int q = wv + C::NW * i;
+    if (8 * q < C::BM) {
+      Operand<TA, C::BM>::place(q, lane, k, row);
+      return m0 + row < a.M ? Operand<TA, C::BM>::offset(k, row, a.lda) : kOut;
+    }
+    Operand<TW, C::BN>::place(q - C::BM / 8, lane, k, row);
+    if (GATED) {  // 16 gate rows, then the 16 up rows of the same outputs
+      const int j = (row >> 5) * 16 + (row & 15);
+      row = j + (row & 16 ? a.N / 2 : 0);
+      return n0 + j < a.N / 2 ? Operand<TW, C::BN>::offset(k, row, a.ldw) : kOut;
+    }
+    return n0 + row < a.N ? Operand<TW, C::BN>::offset(k, row, a.ldw) : kOut;
+  }
+  __device__ __forceinline__ void copy(int kb, int i) {
+    const int q = wv + C::NW * i;
+    uint32_t v = voff[i];
+    if (64 * kb + 64 > a.K) {  // the last block's rest: zeros
+      int k, row;
+      where(i, k, row);
+      if (64 * kb + k >= a.K) v = kOut;
+    }
+    copy16(v, 8 * q < C::BM ? abase : wbase, (uint32_t)uniform((int)(lds0 + (kb % S) * C::kSlot + 1024 * q)));
+  }
+  __device__ __forceinline__ void copied() {  // the next block's copies come from the next K values
+    abase += astep();
+    wbase += wstep();
+  }
+  __device__ __forceinline__ void store(v4f (&acc)[RB][CB]) const {
+    // The sums are whole before any lane's store is masked off.
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j) asm volatile("" : "+v"(acc[i][j]));
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int m = m0 + wm + 16 * i + l16;
+      if constexpr (GATED) {
+#pragma unroll
+        for (int j = 0; j < CB; j += 2) finish4<true>(a, m, n0 + wn / 2 + 8 * j + 4 * lg, acc[i][j], acc[i][j + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < CB; ++j) finish4<false>(a, m, n0 + wn + 16 * j + 4 * lg, acc[i][j], v4f{0.f, 0.f, 0.f, 0.f});
+      }
+    }
+  }
+};
+
+// S slots: block kb + S - 1 is copied while block kb is multiplied; one barrier a step.
+template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN, int S>
+__global__ __launch_bounds__(512) void gemm_linear_kernel(const LinearArgs a) {
+  using C = LinCfg<RB, CB, WM, WN, S>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
+  LinTileT<TA, TW, GATED, RB, CB, WM, WN, S> T(a, sm);
+  const int kb0 = T.kb0, kb1 = T.kb1;
+  v4f acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto issue = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < C::kPw; ++i) T.copy(kb, i);
+    T.copied();
+  };
+  for (int b = 0; b < S - 1; ++b)
+    if (kb0 + b < kb1) issue(kb0 + b);
+  for (int kb = kb0; kb < kb1; ++kb) {
+    if (kb + S - 2 < kb1) wait_vmcnt<(S - 2) * C::kPw>();
+    else wait_vmcnt<0>();
+    barrier_reads();
+    if (kb + S - 1 < kb1) issue(kb + S - 1);
+    const uint8_t* sa = sm + (kb % S) * C::kSlot;
+    const uint8_t* sw = sa + C::BM * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v8bf w[CB];
+#pragma unroll
+      for (int j = 0; j < CB; ++j) w[j] = T.xw.frag(sw, j, h);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const v8bf x = T.xa.frag(sa, i, h);
+#pragma unroll
+        for (int j = 0; j < CB; ++j) acc[i][j] = mma(w[j], x, acc[i][j]);
+      }
+    }
+  }
+  T.store(acc);
+}
+
+// Split K: the shares' sums, added in order, then the epilogue.
+template <bool GATED>
+__global__ __launch_bounds__(256) void gemm_linear_join_kernel(const LinearArgs a) {
+  const int half = ws_half(a), cols = ws_cols(a), np = half / 4;
+  const int64_t total = (int64_t)a.M * np, plane = (int64_t)a.M * cols;
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
+    const int m = (int)(q / np), n = 4 * (int)(q % np);
+    const float* w = a.ws + (int64_t)m * cols + n;
+    v4f v = *(const v4f*)w, up = {0.f, 0.f, 0.f, 0.f};
+    if (GATED) up = *(const v4f*)(w + half);
+    for (int k = 1; k < a.splits; ++k) {
+      v += *(const v4f*)(w + k * plane);
+      if (GATED) up += *(const v4f*)(w + k * plane + half);
+    }
+    epilogue4<GATED>(a, m, n, v, up);
+  }
+}
+
+template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN, int S>
+hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
+  using C = LinCfg<RB, CB, WM, WN, S>;
+  const int NO = GATED ? a.N / 2 : a.N, BNO = GATED ? C::BN / 2 : C::BN;
+  const dim3 grid(((a.M + C::BM - 1) / C::BM) * ((NO + BNO - 1) / BNO), a.splits);
+  gemm_linear_kernel<TA, TW, GATED, RB, CB, WM, WN, S><<<grid, WM * WN * 64, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t need = ((int64_t)a.M * (ws_half(a) / 4) + 255) / 256, cap = (int64_t)device_info().cus * 16;
+  gemm_linear_join_kernel<GATED><<<(unsigned)(need < cap ? need : cap), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// ----------------------------------------------------------------- stream --
+// Few rows (a decode step): every weight byte is used by one wave, so waves need nothing from one another.  A workgroup takes
+// 16 CB columns (gated: 8 CB outputs) and all 16 RB rows; its KS waves split K, each with a ring of S blocks of its own in LDS
+// (no barrier in the loop), and meet once at the end, where the partial sums are added in wave order.
+template <int RB, int CB, int KS, int S>
+struct LinStreamCfg {
+  static constexpr int kBlock = (RB + CB) * 2048, kCopies = 2 * (RB + CB), kWave = S * kBlock;
+  static constexpr int kPart = 16 * RB * (16 * CB + 4) * 4;  // a wave's partial sums, over its ring
+  static constexpr int kLds = KS * kWave;
+  static_assert(kPart <= kWave && kLds <= 160 * 1024 && (S - 1) * kCopies < 64, "LDS; vmcnt");
+};
+
+template <bool GATED, int RB, int CB, int KS, int S>
+__global__ __launch_bounds__(KS * 64) void gemm_linear_stream_kernel(const LinearArgs a) {
+  using C = LinStreamCfg<RB, CB, KS, S>;
+  constexpr int kRows = 16 * RB, kCols = 16 * CB, kOuts = GATED ? kCols / 2 : kCols;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
+  const int lane = lane_id(), wv = uniform(threadIdx.x >> 6), l16 = lane & 15, lg = lane >> 4;
+  const int KB = (a.K + 63) / 64, NO = GATED ? a.N / 2 : a.N;
+  const int n0 = blockIdx.x * kOuts;
+  const int kb0 = wv * KB / KS, nb = (wv + 1) * KB / KS - kb0;
+  uint8_t* ring = sm + wv * C::kWave;
+  const uint32_t lds0 = (uint32_t)uniform((int)lds_offset(ring));
+  const uint8_t* abase = (const uint8_t*)a.A + (int64_t)kb0 * 128;
+  const uint8_t* wbase = (const uint8_t*)(a.W + (int64_t)n0 * a.ldw) + (int64_t)kb0 * 128;
+  uint32_t voff[C::kCopies];
+  const int ck = 8 * ((lane & 7) ^ (lane >> 4));  // this lane's k in even copies; odd ones: ^ 32
+#pragma unroll
+  for (int q = 0; q < C::kCopies; ++q) {
+    const int row = 8 * q + (lane >> 3), k = q & 1 ? ck ^ 32 : ck;
+    if (8 * q < kRows) {
+      voff[q] = row < a.M ? Operand<false, 64>::offset(k, row, a.lda) : kOut;
+    } else {
+      int n = row - kRows;
+      bool in = n0 + n < NO;
+      if (GATED) {
+        const int j = (n >> 5) * 16 + (n & 15);
+        in = n0 + j < NO;
+        n = j + (n & 16 ? NO : 0);
+      }
+      voff[q] = in ? Operand<false, 64>::offset(k, n, a.ldw) : kOut;
+    }
+  }
+  int slot = 0;
+  auto issue = [&](int b) {
+    const bool rest = 64 * (kb0 + b) + 64 > a.K;
+#pragma unroll
+    for (int q = 0; q < C::kCopies; ++q) {
+      uint32_t v = voff[q];
+      if (rest && 64 * (kb0 + b) + (q & 1 ? ck ^ 32 : ck) >= a.K) v = kOut;
+      copy16(v, 8 * q < kRows ? abase : wbase, (uint32_t)uniform((int)(lds0 + slot * C::kBlock + 1024 * q)));
+    }
+    abase += 128;
+    wbase += 128;
+    slot = slot + 1 == S ? 0 : slot + 1;
+  };
+  Operand<false, 64> op;
+  op.init(lane, 0);
+  v4f acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int b = 0; b < S - 1; ++b)
+    if (b < nb) issue(b);
+  int cs = 0;
+  for (int b = 0; b < nb; ++b) {
+    if (b + S - 1 < nb) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot's last reads are in registers
+      issue(b + S - 1);
+      wait_vmcnt<(S - 1) * C::kCopies>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    asm volatile("" ::: "memory");
+    const uint8_t* blk = ring + cs * C::kBlock;
+    cs = cs + 1 == S ? 0 : cs + 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v8bf x[RB];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) x[i] = op.frag(blk, i, h);
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        const v8bf w = op.frag(blk, RB + j, h);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) acc[i][j] = mma(w, x[i], acc[i][j]);
+      }
+    }
+  }
+  // over the wave's own ring, whose copies have all landed and been read; lane: columns 4 lg .. + 3 of row l16
+  float* part = (float*)ring;
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) *(v4f*)(part + (16 * i + l16) * (kCols + 4) + 16 * j + 4 * lg) = acc[i][j];
+  __syncthreads();
+  for (int q = threadIdx.x; q < kRows * kOuts / 4; q += KS * 64) {
+    const int m = q / (kOuts / 4), n = 4 * (q % (kOuts / 4));
+    const int c = GATED ? (n >> 4) * 32 + (n & 15) : n;
+    v4f v = {0.f, 0.f, 0.f, 0.f}, up = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const float* p = (const float*)(sm + k * C::kWave) + m * (kCols + 4) + c;
+      v += *(const v4f*)p;
+      if (GATED) up += *(const v4f*)(p + 16);
+    }
+    epilogue4<GATED>(a, m, n0 + n, v, up);
+  }
+}
+
+template <bool GATED, int RB, int CB, int KS, int S>
+hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
+  const int NO = GATED ? a.N / 2 : a.N, outs = GATED ? 8 * CB : 16 * CB;
+  gemm_linear_stream_kernel<GATED, RB, CB, KS, S><<<(NO + outs - 1) / outs, KS * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool TA, bool TW, bool GATED>
+hipError_t launch_order(LinearArgs a, hipStream_t s) {
+  const LinPlan p = plan_linear(a.M, a.N, a.K, TA || TW);
+  a.splits = p.splits;
+  if constexpr (!TA && !TW) {
+    if (p.kind == kLinStream16) return launch_stream<GATED, 1, GATED ? 2 : 1, 8, GATED ? 3 : 4>(a, s);
+    if (p.kind == kLinStream32) return launch_stream<GATED, 2, GATED ? 2 : 1, 8, GATED ? 2 : 3>(a, s);
+    if (p.kind == kLinStream64) return launch_stream<GATED, 4, GATED ? 2 : 1, 4, 3>(a, s);
+  }
+  switch (p.kind) {
+    case kLin64x64: return launch_tile<TA, TW, GATED, 2, 2, 2, 2, 4>(a, s);
+    case kLin64x128: return launch_tile<TA, TW, GATED, 2, 2, 2, 4, 4>(a, s);
+    case kLin128x128: return launch_tile<TA, TW, GATED, 4, 4, 2, 2, 2>(a, s);
+    default: return launch_tile<TA, TW, GATED, 8, 4, 2, 4, 2>(a, s);
+  }
+}
+
+}  // namespace
+
+int64_t linear_workspace_bytes(int M, int N, int K) {
+  // any order and a gated epilogue may be asked for: the largest need
+  const int x = plan_linear(M, N, K, false).splits, y = plan_linear(M, N, K, true).splits, s = x > y ? x : y;
+  return s > 1 ? 4ll * s * M * (((N + 3) & ~3) + 4) : 0;
+}
+
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
+  if (a.gated) return launch_order<false, false, true>(a, s);
+  if (!a.ta) return a.tw ? launch_order<false, true, false>(a, s) : launch_order<false, false, false>(a, s);
+  return launch_order<true, true, false>(a, s);
+}
+
+}  // namespace moe

@@ -186,4 +186,45 @@ struct DecodeArgs {
 int64_t decode_workspace_bytes(int T, int k, int I);
 hipError_t launch_experts_decode(const DecodeArgs& a, hipStream_t s);
 
+struct LinearArgs {
+  const uint16_t* A;     // bf16 [M, K], or [K, M] (ta), rows lda apart
+  int64_t lda;
+  const uint16_t* W;     // bf16 [N, K], or [K, N] (tw), rows ldw apart
+  int64_t ldw;
+  int ta, tw;
+  void* D;               // bf16 or fp32 [M, N] (gated: [M, N/2]), rows ldd apart
+  int64_t ldd;
+  int d_f32;
+  const void* bias;      // [N], or nullptr
+  int bias_f32;
+  int act, gated;
+  const void* C;         // addend of D's shape, rows ldc apart, or nullptr
+  int64_t ldc;
+  int c_f32;
+  uint16_t* pre;         // bf16 [M, N], rows ldp apart, or nullptr
+  int64_t ldp;
+  int M, N, K;
+  float* ws;             // split K: partial sums
+  int splits;
+};
+int64_t linear_workspace_bytes(int M, int N, int K);
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+
+struct ActBwdArgs {
+  const uint16_t* dD;    // bf16 [M, N] (gated: [M, N/2]), rows ldd apart
+  int64_t ldd;
+  const uint16_t* pre;   // bf16 [M, N], rows ldp apart, or nullptr
+  int64_t ldp;
+  uint16_t* dP;          // bf16 [M, N], rows ldo apart, or nullptr
+  int64_t ldo;
+  float* dbias;          // [N] or nullptr
+  int accumulate;
+  int act, gated;
+  int M, N;
+  float* ws;             // column sums of the row chunks
+  int rows;              // of a chunk
+};
+int64_t act_bwd_workspace_bytes(int M, int N);
+hipError_t launch_act_bwd(const ActBwdArgs& a, hipStream_t s);
+
 }  // namespace moe

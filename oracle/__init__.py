@@ -76,6 +76,7 @@ from .combine import combine, combine_bwd, combine_fp32, f32_to_bf16_bits
 from .router import router_scores, router_topk, router_topk_bwd, router_weights
 from .activation import quant_act_values, silu, swiglu, swiglu_quant
 from .decode import experts_decode
+from .linear import act, act_bwd, act_slope, linear
 from .metrics import calc_diff, elementwise_ok, elementwise_excess
 
 __all__ = [
@@ -92,6 +93,6 @@ __all__ = [
     "silu", "swiglu", "quant_act_values", "swiglu_quant",
     "INT8_MAX", "quant_int8", "dequant_int8", "grouped_gemm_int8",
     "quant_act_t", "dense_gemm_fp8", "combine_bwd",
-    "experts_decode",
+    "experts_decode", "act", "act_bwd", "act_slope", "linear",
     "router_scores", "router_topk", "router_topk_bwd", "router_weights",
 ]

@@ -1,6 +1,6 @@
-"""The expert layer of a few tokens and the dense product with its epilogue, in float64.  TEST INFRASTRUCTURE ONLY.
+"""The expert layer of a few tokens, in float64.  TEST INFRASTRUCTURE ONLY.
 
-Written from the definitions (include/moe.h: moe_experts_decode, moe_gemm_bf16, moe_act_bwd), on values, not codes.
+Written from the definition in include/moe.h (moe_experts_decode), on values, not codes.
 """
 
 from __future__ import annotations
