@@ -46,7 +46,7 @@ inline LinPlan plan_linear(int M, int N, int K, bool transposed) {
       best_tiles = t;
     }
   }
-  int s = (int)(kLinCus / best_tiles);
+  int s = best_tiles > 0 ? (int)(kLinCus / best_tiles) : 1;
   if (s > KB / 8) s = KB / 8;
   if (s > 8) s = 8;
   if (s > 1 && (float)KB * least * (1.0f - 1.0f / (float)s) > 5.0f) {
