@@ -54,28 +54,40 @@ __device__ __forceinline__ v4f load4(const void* p, bool f32, int64_t at, int cn
   if (f32) {
     const float* q = (const float*)p + at;
     if (cnt == 4) return *(const v4f_any*)q;
-    for (int i = 0; i < cnt; ++i) v[i] = q[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) v[i] = q[i];
   } else {
     const uint16_t* q = (const uint16_t*)p + at;
     if (cnt == 4) {
       const v2u_any u = *(const v2u_any*)q;
       return v4f{bf16_to_f32(u[0] & 0xffffu), bf16_to_f32(u[0] >> 16), bf16_to_f32(u[1] & 0xffffu), bf16_to_f32(u[1] >> 16)};
     }
-    for (int i = 0; i < cnt; ++i) v[i] = bf16_to_f32(q[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) v[i] = bf16_to_f32(q[i]);
   }
   return v;
 }
 __device__ __forceinline__ void store4(void* p, bool f32, int64_t at, int cnt, const v4f v) {
   if (f32) {
     float* q = (float*)p + at;
-    if (cnt == 4) *(v4f_any*)q = v;
-    else
-      for (int i = 0; i < cnt; ++i) q[i] = v[i];
+    if (cnt == 4) {
+      *(v4f_any*)q = v;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) q[i] = v[i];
   } else {
     uint16_t* q = (uint16_t*)p + at;
-    if (cnt == 4) *(v2u_any*)q = bf16x4(v);
-    else
-      for (int i = 0; i < cnt; ++i) q[i] = (uint16_t)f32_to_bf16_rne(v[i]);
+    if (cnt == 4) {
+      *(v2u_any*)q = bf16x4(v);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) q[i] = (uint16_t)f32_to_bf16_rne(v[i]);
   }
 }
 
@@ -237,19 +249,22 @@ struct LinTileT {
     }
     return n0 + row < a.N ? Operand<TW, C::BN>::offset(k, row, a.ldw) : kOut;
   }
-  __device__ __forceinline__ void copy(int kb, int i) {
-    const int q = wv + C::NW * i;
-    uint32_t v = voff[i];
-    if (64 * kb + 64 > a.K) {  // the last block's rest: zeros
+  // before the copies of block kb: if K ends inside it, what lies behind becomes zeros (it is the last block that is copied)
+  // (of one operand: of_a, else of w)
+  template <bool of_a>
+  __device__ __forceinline__ void end_of_k(int kb) {
+    if (64 * kb + 64 <= a.K) return;
+#pragma unroll
+    for (int i = 0; i < C::kPw; ++i) {
+      if ((8 * (wv + C::NW * i) < C::BM) != of_a) continue;
       int k, row;
       where(i, k, row);
-      if (64 * kb + k >= a.K) v = kOut;
+      if (64 * kb + k >= a.K) voff[i] = kOut;
     }
-    copy16(v, 8 * q < C::BM ? abase : wbase, (uint32_t)uniform((int)(lds0 + (kb % S) * C::kSlot + 1024 * q)));
   }
-  __device__ __forceinline__ void copied() {  // the next block's copies come from the next K values
-    abase += astep();
-    wbase += wstep();
+  // copy i of a block to `at` in the LDS; base: abase or wbase of the block
+  __device__ __forceinline__ void copy_to(int i, const uint8_t* base, int at) const {
+    copy16(voff[i], base, (uint32_t)uniform((int)lds0 + at));
   }
   __device__ __forceinline__ void store(v4f (&acc)[RB][CB]) const {
     // The sums are whole before any lane's store is masked off.
@@ -284,9 +299,15 @@ __global__ __launch_bounds__(512) void gemm_linear_kernel(const LinearArgs a) {
 #pragma unroll
     for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   auto issue = [&](int kb) {
+    T.template end_of_k<true>(kb);
+    T.template end_of_k<false>(kb);
 #pragma unroll
-    for (int i = 0; i < C::kPw; ++i) T.copy(kb, i);
-    T.copied();
+    for (int i = 0; i < C::kPw; ++i) {
+      const int q = T.wv + C::NW * i;
+      T.copy_to(i, 8 * q < C::BM ? T.abase : T.wbase, kb % S * C::kSlot + 1024 * q);
+    }
+    T.abase += T.astep();
+    T.wbase += T.wstep();
   };
   for (int b = 0; b < S - 1; ++b)
     if (kb0 + b < kb1) issue(kb0 + b);
@@ -309,6 +330,129 @@ __global__ __launch_bounds__(512) void gemm_linear_kernel(const LinearArgs a) {
         for (int j = 0; j < CB; ++j) acc[i][j] = mma(w[j], x, acc[i][j]);
       }
     }
+  }
+  T.store(acc);
+}
+
+// The large tiles (256x256: 8 waves of 128x64, two per SIMD; 128x128: 4 waves of 64x64, two workgroups per compute unit), with the
+// other work of a step laid out between the matrix instructions of its own wave:
+//  * row blocks 0 .. RB-3 in turn, their fragments read two ahead;
+//  * then the barrier that publishes block kb + 1, every fragment of block kb being in registers, and the last two row blocks
+//    column by column: after column j's matrix instructions its weight fragment is read anew for block kb + 1;
+//  * three slots for rows, two for weights (all of the LDS): a slot of rows is free from that barrier on, so block kb + 3's rows
+//    are copied behind it and have two steps to arrive; weights stay in registers from there on, so block kb + 2's are copied from the
+//    second row block of step kb on (a barrier says that every wave has read block kb's) and have one and a half.
+template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN>
+__global__ __launch_bounds__(512) void gemm_linear_big_kernel(const LinearArgs a) {
+  using C = LinCfg<RB, CB, WM, WN, 2>;
+  constexpr int kA = C::BM * 128, kW = C::BN * 128;
+  static_assert(RB >= 4 && RB % 4 == 0 && C::kPw == 2 * CB && C::BM == 8 * C::NW * CB,
+                "fragment ring; a wave's first CB copies are of A, its last CB of W");
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[3 * kA + 2 * kW];
+  LinTileT<TA, TW, GATED, RB, CB, WM, WN, 2> T(a, sm);
+  const int kb0 = T.kb0, kb1 = T.kb1;
+  v4f acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  v8bf w[CB][2], x[4][2];
+  auto read_x = [&](int slot, int i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x[i & 3][h] = T.xa.frag(sm + slot * kA, i, h);
+  };
+  auto read_w = [&](int kb, int j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[j][h] = T.xw.frag(sm + 3 * kA + (kb & 1) * kW, j, h);
+  };
+  auto copy_x = [&](int slot, int i) { T.copy_to(i, T.abase, slot * kA + 1024 * (T.wv + C::NW * i)); };
+  auto copy_w = [&](int kb, int i) {
+    T.copy_to(CB + i, T.wbase, 3 * kA + (kb & 1) * kW + 1024 * (T.wv + C::NW * (CB + i)) - kA);
+  };
+  int s0 = 0, s1 = 1, s2 = 2;  // the slots of the rows of blocks kb, kb + 1, kb + 2
+  // ahead: how many blocks follow block kb, at most 3
+  auto step = [&](int kb, auto ahead_c) {
+    constexpr int ahead = decltype(ahead_c)::value;
+    if constexpr (ahead >= 2) T.template end_of_k<false>(kb + 2);
+#pragma unroll
+    for (int i = 0; i < RB - 2; ++i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+          acc[i][j] = mma(w[j][h], x[i & 3][h], acc[i][j]);
+          if (h == 0 && j == 0) read_x(s0, i + 2);
+          if constexpr (ahead >= 2) {  // the weights of block kb + 2
+            const int c = RB >= 8 ? (h == 1 && j == 1 ? i - 1 : -1) : (i == 1 && h == 1 ? j : -1);
+            if (c >= 0 && c < CB) copy_w(kb, c);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      if constexpr (ahead >= 2)
+        if (i == 0) asm volatile("s_barrier" ::: "memory");
+    }
+    if constexpr (ahead > 0) {
+      wait_vmcnt<ahead >= 2 ? 2 * CB : 0>();  // all but block kb + 2
+      barrier_reads();
+    }
+    if constexpr (ahead >= 2) T.wbase += T.wstep();
+    if constexpr (ahead == 3) T.template end_of_k<true>(kb + 3);
+    v8bf xl[2] = {x[(RB - 2) & 3][0], x[(RB - 2) & 3][1]}, xm[2] = {x[(RB - 1) & 3][0], x[(RB - 1) & 3][1]};
+    if constexpr (ahead > 0) {
+      read_x(s1, 0);
+      read_x(s1, 1);
+    }
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        acc[RB - 2][j] = mma(w[j][h], xl[h], acc[RB - 2][j]);
+        acc[RB - 1][j] = mma(w[j][h], xm[h], acc[RB - 1][j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (ahead > 0) read_w(kb + 1, j);
+      if constexpr (ahead == 3) copy_x(s0, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (ahead == 3) T.abase += T.astep();
+    const int s = s0;
+    s0 = s1;
+    s1 = s2;
+    s2 = s;
+  };
+  if (kb0 < kb1) {
+    const int n = kb1 - kb0;
+    auto issue_x = [&](int kb, int slot) {
+      T.template end_of_k<true>(kb);
+#pragma unroll
+      for (int i = 0; i < CB; ++i) copy_x(slot, i);
+      T.abase += T.astep();
+    };
+    auto issue_w = [&](int kb) {
+      T.template end_of_k<false>(kb);
+#pragma unroll
+      for (int i = 0; i < CB; ++i) copy_w(kb, i);
+      T.wbase += T.wstep();
+    };
+    // in the loop's order: rows are copied before the weights of the block before
+    issue_x(kb0, 0);
+    issue_w(kb0);
+    if (n > 1) issue_x(kb0 + 1, 1);
+    if (n > 1) issue_w(kb0 + 1);
+    if (n > 2) issue_x(kb0 + 2, 2);
+    if (n > 2) wait_vmcnt<3 * CB>();
+    else if (n > 1) wait_vmcnt<2 * CB>();
+    else wait_vmcnt<0>();
+    barrier_reads();
+    read_x(0, 0);
+    read_x(0, 1);
+#pragma unroll
+    for (int j = 0; j < CB; ++j) read_w(kb0, j);
+    int kb = kb0;
+    for (; kb + 3 < kb1; ++kb) step(kb, IntC<3>{});
+    if (kb + 2 < kb1) step(kb++, IntC<2>{});
+    if (kb + 1 < kb1) step(kb++, IntC<1>{});
+    step(kb, IntC<0>{});
   }
   T.store(acc);
 }
@@ -336,7 +480,8 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
   using C = LinCfg<RB, CB, WM, WN, S>;
   const int NO = GATED ? a.N / 2 : a.N, BNO = GATED ? C::BN / 2 : C::BN;
   const dim3 grid(((a.M + C::BM - 1) / C::BM) * ((NO + BNO - 1) / BNO), a.splits);
-  gemm_linear_kernel<TA, TW, GATED, RB, CB, WM, WN, S><<<grid, WM * WN * 64, 0, s>>>(a);
+  if constexpr (RB >= 4) gemm_linear_big_kernel<TA, TW, GATED, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
+  else gemm_linear_kernel<TA, TW, GATED, RB, CB, WM, WN, S><<<grid, WM * WN * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t need = ((int64_t)a.M * (ws_half(a) / 4) + 255) / 256, cap = (int64_t)device_info().cus * 16;
