@@ -4,8 +4,10 @@
 //   gated:     dP[m, j] = dD[m, j] * up * act'(gate),   dP[m, N/2 + j] = dD[m, j] * act(gate)
 //   dbias[n] (+)= sum_m dP[m, n], of the fp32 values before dP's rounding
 //
-// One pass: 8 columns per lane (16-byte loads and stores), rows in turn; a workgroup's column sums stay in registers, meet in
-// LDS, and one line per workgroup goes to the workspace, where a second launch adds the lines in order.
+// One pass: 8 columns per lane (16-byte loads and stores), kRowsAhead rows' loads in flight per lane; the column sums stay in
+// registers, meet across lanes and waves in a fixed order, and where the rows are cut into several chunks one line of sums per
+// chunk goes to the workspace, where a second launch adds the lines.  A launch costs more than a few hundred rows do, so up to
+// kOneChunk rows are one chunk: narrow strips, 16 waves each, no second launch.
 #include "linear_act.h"
 #include "moe_internal.h"
 
@@ -13,7 +15,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kStrip = 512;  // columns of a workgroup: 64 lanes x 8
+constexpr int kOneChunk = 1024;   // rows
+constexpr int kRowsAhead = 4;
+constexpr int kJoinCols = 64, kJoinParts = 16;
 
 struct Eight {
   float v[8];
@@ -34,84 +38,120 @@ __device__ __forceinline__ v4i pack8(const Eight& e) {
   return w;
 }
 
-template <int ACT, bool GATED>
-__global__ __launch_bounds__(256) void act_bwd_kernel(const ActBwdArgs a) {
-  __shared__ float part[4][GATED ? 2 : 1][kStrip];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int half = GATED ? a.N / 2 : a.N, n = blockIdx.x * kStrip + 8 * lane;
+// LPR lanes per row: a workgroup of TPB threads owns 8 LPR columns (of each half, if gated) and the rows of chunk blockIdx.y.
+template <int ACT, bool GATED, int LPR, int TPB>
+__global__ __launch_bounds__(TPB) void act_bwd_kernel(const ActBwdArgs a) {
+  constexpr int kCols = 8 * LPR, kWaves = TPB / 64, kRows = TPB / LPR, H = GATED ? 2 : 1;
+  __shared__ float part[kWaves][H][kCols];
+  const int lr = threadIdx.x % LPR, wv = threadIdx.x >> 6;
+  const int half = GATED ? a.N / 2 : a.N, n = blockIdx.x * kCols + 8 * lr;
   const int r0 = blockIdx.y * a.rows, r1 = min(r0 + a.rows, a.M);
-  float s0[8], s1[8];
+  float s[H][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s0[i] = s1[i] = 0.f;
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int h = 0; h < H; ++h) s[h][i] = 0.f;
   if (n < half) {
-    for (int m = r0 + wv; m < r1; m += 4) {
-      const Eight d = unpack8(*(const v4i*)(a.dD + (int64_t)m * a.ldd + n));
-      Eight g{}, u{}, o, p;
-      if (GATED || ACT != kActNone) g = unpack8(*(const v4i*)(a.pre + (int64_t)m * a.ldp + n));
-      if (GATED) u = unpack8(*(const v4i*)(a.pre + (int64_t)m * a.ldp + half + n));
+    for (int m0 = r0 + threadIdx.x / LPR; m0 < r1; m0 += kRowsAhead * kRows) {
+      v4i d[kRowsAhead], g[kRowsAhead], u[kRowsAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o.v[i] = d.v[i] * slope1(ACT, g.v[i]);
-        if (GATED) {
-          o.v[i] *= u.v[i];
-          p.v[i] = d.v[i] * act1(ACT, g.v[i]);
-          s1[i] += p.v[i];
-        }
-        s0[i] += o.v[i];
+      for (int j = 0; j < kRowsAhead; ++j) {
+        const int64_t m = min(m0 + j * kRows, r1 - 1);
+        d[j] = *(const v4i*)(a.dD + m * a.ldd + n);
+        if (GATED || ACT != kActNone) g[j] = *(const v4i*)(a.pre + m * a.ldp + n);
+        if (GATED) u[j] = *(const v4i*)(a.pre + m * a.ldp + half + n);
       }
-      if (a.dP) {
-        *(v4i*)(a.dP + (int64_t)m * a.ldo + n) = pack8(o);
-        if (GATED) *(v4i*)(a.dP + (int64_t)m * a.ldo + half + n) = pack8(p);
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j) {
+        const int64_t m = m0 + j * kRows;
+        if (m >= r1) break;
+        const Eight dv = unpack8(d[j]);
+        Eight gv{}, uv{}, o, p;
+        if (GATED || ACT != kActNone) gv = unpack8(g[j]);
+        if (GATED) uv = unpack8(u[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float act = 0.f;
+          o.v[i] = dv.v[i] * (GATED ? act_and_slope(ACT, gv.v[i], act) * uv.v[i] : slope1(ACT, gv.v[i]));
+          s[0][i] += o.v[i];
+          if (GATED) {
+            p.v[i] = dv.v[i] * act;
+            s[H - 1][i] += p.v[i];
+          }
+        }
+        if (a.dP) {
+          *(v4i*)(a.dP + m * a.ldo + n) = pack8(o);
+          if (GATED) *(v4i*)(a.dP + m * a.ldo + half + n) = pack8(p);
+        }
       }
     }
   }
   if (!a.dbias) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    part[wv][0][8 * lane + i] = s0[i];
-    if (GATED) part[wv][GATED ? 1 : 0][8 * lane + i] = s1[i];
+  for (int h = 0; h < H; ++h) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int x = LPR; x < 64; x <<= 1) s[h][i] += __shfl_xor(s[h][i], x);
+      if ((threadIdx.x & 63) < LPR) part[wv][h][8 * lr + i] = s[h][i];
+    }
   }
   __syncthreads();
-  for (int q = threadIdx.x; q < (GATED ? 2 : 1) * kStrip; q += 256) {
-    const int which = q / kStrip, c = q % kStrip, col = blockIdx.x * kStrip + c;
+  for (int q = threadIdx.x; q < H * kCols; q += TPB) {
+    const int h = q / kCols, c = q % kCols, col = blockIdx.x * kCols + c;
     if (col >= half) continue;
-    const float s = (part[0][which][c] + part[1][which][c]) + (part[2][which][c] + part[3][which][c]);
-    const int at = which * half + col;
-    if (gridDim.y > 1) a.ws[(int64_t)blockIdx.y * a.N + at] = s;
-    else a.dbias[at] = a.accumulate ? a.dbias[at] + s : s;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += part[w][h][c];
+    const int at = h * half + col;
+    if (gridDim.y > 1) a.ws[(int64_t)blockIdx.y * a.N + at] = sum;
+    else a.dbias[at] = a.accumulate ? a.dbias[at] + sum : sum;
   }
 }
 
-// dbias from the workgroups' lines, in order.
-__global__ __launch_bounds__(256) void act_bwd_join_kernel(const ActBwdArgs a, int lines) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= a.N) return;
+// dbias from the chunks' lines: kJoinParts threads per column take the lines in turn, then meet in order.
+__global__ __launch_bounds__(kJoinCols* kJoinParts) void act_bwd_join_kernel(const ActBwdArgs a, int lines) {
+  __shared__ float part[kJoinParts][kJoinCols];
+  const int c = threadIdx.x % kJoinCols, p = threadIdx.x / kJoinCols, n = blockIdx.x * kJoinCols + c;
   float s = 0.f;
-  for (int i = 0; i < lines; ++i) s += a.ws[(int64_t)i * a.N + n];
+  if (n < a.N) {
+#pragma unroll 4
+    for (int i = p; i < lines; i += kJoinParts) s += a.ws[(int64_t)i * a.N + n];
+  }
+  part[p][c] = s;
+  __syncthreads();
+  if (p || n >= a.N) return;
+#pragma unroll
+  for (int i = 1; i < kJoinParts; ++i) s += part[i][c];
   a.dbias[n] = a.accumulate ? a.dbias[n] + s : s;
 }
 
-// Row chunks: enough workgroups for the chip, at least 16 rows each.
+// Row chunks: one up to kOneChunk rows; else chunks that give the chip two workgroups per compute unit, of 32 rows at least.
+// (By the columns of dP, so that gated calls have half as many workgroups.)
 int chunks(int M, int N) {
-  const int strips = (N + kStrip - 1) / kStrip;
-  int c = (2048 + strips - 1) / strips;
-  const int most = M > 16 ? (M + 15) / 16 : 1;
+  if (M <= kOneChunk) return 1;
+  const int strips = (N + 511) / 512, c = (1024 + strips - 1) / strips, most = (M + 31) / 32;
   return c < most ? c : most;
 }
 
-template <int ACT>
-hipError_t launch_act(ActBwdArgs a, hipStream_t s) {
-  const int half = a.gated ? a.N / 2 : a.N;
-  const int c = chunks(a.M, a.N);
+template <int ACT, bool GATED>
+hipError_t launch_gated(ActBwdArgs a, hipStream_t s) {
+  const int half = GATED ? a.N / 2 : a.N, c = chunks(a.M, a.N);
   a.rows = a.M > c ? (a.M + c - 1) / c : 1;
-  const int lines = a.M > a.rows ? (a.M + a.rows - 1) / a.rows : 1;
-  const dim3 grid((half + kStrip - 1) / kStrip, lines);
-  if (a.gated) act_bwd_kernel<ACT, true><<<grid, 256, 0, s>>>(a);
-  else act_bwd_kernel<ACT, false><<<grid, 256, 0, s>>>(a);
+  if (c == 1) {
+    act_bwd_kernel<ACT, GATED, 4, 1024><<<(half + 31) / 32, 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int lines = (a.M + a.rows - 1) / a.rows;
+  act_bwd_kernel<ACT, GATED, 64, 256><<<dim3((half + 511) / 512, lines), 256, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.dbias || lines == 1) return e;
-  act_bwd_join_kernel<<<(a.N + 255) / 256, 256, 0, s>>>(a, lines);
+  if (e != hipSuccess || !a.dbias) return e;
+  act_bwd_join_kernel<<<(a.N + kJoinCols - 1) / kJoinCols, kJoinCols * kJoinParts, 0, s>>>(a, lines);
   return hipGetLastError();
+}
+template <int ACT>
+hipError_t launch_act(const ActBwdArgs& a, hipStream_t s) {
+  return a.gated ? launch_gated<ACT, true>(a, s) : launch_gated<ACT, false>(a, s);
 }
 
 }  // namespace

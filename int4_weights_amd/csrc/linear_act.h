@@ -51,4 +51,28 @@ __device__ __forceinline__ float slope1(int act, float v) {
   }
 }
 
+// Both, from one evaluation of their common part: returns the slope.
+__device__ __forceinline__ float act_and_slope(int act, float v, float& value) {
+  switch (act) {
+    case kActSilu: {
+      const float s = 1.0f / (1.0f + expf(-v));
+      value = v * s;
+      return s * __builtin_fmaf(v, 1.0f - s, 1.0f);
+    }
+    case kActGelu: {
+      const float c = normal_cdf(v);
+      value = v * c;
+      return __builtin_fmaf(v * 0.3989422804014327f, expf(-0.5f * v * v), c);
+    }
+    case kActGeluTanh: {
+      const float s = gelu_gate(v);
+      value = v * s;
+      return __builtin_fmaf(v * s * (1.0f - s) * 1.5957691216057308f, __builtin_fmaf(0.134145f * v, v, 1.0f), s);
+    }
+    default:
+      value = act1(act, v);
+      return slope1(act, v);
+  }
+}
+
 }  // namespace moe

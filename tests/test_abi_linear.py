@@ -54,8 +54,8 @@ def test_product_refusals(kw, status):
     (dict(pre=None), NULL), (dict(pre=None, act=GATED), NULL), (dict(ldd=248), SHAPE), (dict(ldp=248), SHAPE), (dict(ldo=248), SHAPE),
     (dict(act=GATED | 2, ldd=120), SHAPE), (dict(dD=P + 8), ALIGN), (dict(pre=P + 2), ALIGN), (dict(dP=P + 4), ALIGN), (dict(db=P + 2), ALIGN),
     (dict(ldd=260), ALIGN), (dict(ldp=258), ALIGN), (dict(ldo=257), ALIGN), (dict(dD=P, dP=P, ldo=264), SHAPE),
-    (dict(dD=P, dP=P, act=GATED | 2), SHAPE), (dict(dP=P + 65536, pre=P + 65536, ldp=264), SHAPE), (dict(ws=None), WORKSPACE),
-    (dict(wsb=16), WORKSPACE), (dict(ws=P + 4), WORKSPACE), (dict(M=0, dD=None, pre=None, dP=P, db=None), OK),
+    (dict(dD=P, dP=P, act=GATED | 2), SHAPE), (dict(dP=P + 65536, pre=P + 65536, ldp=264), SHAPE), (dict(M=2000, ws=None), WORKSPACE),
+    (dict(M=2000, wsb=16), WORKSPACE), (dict(M=2000, ws=P + 4), WORKSPACE), (dict(M=0, dD=None, pre=None, dP=P, db=None), OK),
     (dict(M=0, dD=None, pre=None, dP=None, db=P, acc=1), OK),
 ])
 def test_gradient_refusals(kw, status):
@@ -71,7 +71,7 @@ def test_workspace_sizes():
     f, g = moe.moe_gemm_bf16_workspace_bytes, moe.moe_act_bwd_workspace_bytes
     assert f(-1, 8, 8) == f(8, 0, 8) == f(8, 8, -1) == f(1 << 27, 8, 8) == f(1 << 20, 1 << 20, 8) == -1
     assert f(0, 8, 8) == 0 and f(8192, 8192, 4096) == 0 and f(131, 200, 4096) > 0
-    assert g(-1, 8) == g(8, 0) == g(1 << 27, 8) == -1 and g(0, 8) == g(16, 1024) == 0 and g(33, 8) == 3 * 8 * 4
+    assert g(-1, 8) == g(8, 0) == g(1 << 27, 8) == -1 and g(0, 8) == g(1024, 8) == 0 and g(1025, 8) == 33 * 8 * 4
 
 
 def test_binding_refuses():
