@@ -71,8 +71,9 @@ __global__ __launch_bounds__(TPB) void act_bwd_kernel(const ActBwdArgs a) {
         if (GATED) uv = unpack8(u[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float act = 0.f;
-          o.v[i] = dv.v[i] * (GATED ? act_and_slope(ACT, gv.v[i], act) * uv.v[i] : slope1(ACT, gv.v[i]));
+          float slope;
+          const float act = act_and_slope(ACT, gv.v[i], slope);
+          o.v[i] = dv.v[i] * (GATED ? slope * uv.v[i] : slope);
           s[0][i] += o.v[i];
           if (GATED) {
             p.v[i] = dv.v[i] * act;

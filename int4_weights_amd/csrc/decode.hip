@@ -391,7 +391,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void decode_up_kernel(const DecodeAr
           g += part[buf][v][row][c];
           up += part[buf][v][row][kCols + c];
         }
-        a.h[(int64_t)clist[row] * a.I + col + c] = (uint16_t)f32_to_bf16_rne(silu_any(g) * up);
+        a.h[(int64_t)clist[row] * a.I + col + c] = (uint16_t)f32_to_bf16_rne(g * sigmoid_f32(g) * up);
       }
     }
   }

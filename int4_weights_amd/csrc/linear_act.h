@@ -7,72 +7,84 @@ namespace moe {
 
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-// Phi(v) = erfc(-v / sqrt 2) / 2: no cancellation for negative v.
-__device__ __forceinline__ float normal_cdf(float v) { return 0.5f * erfcf(v * -0.70710678118654752f); }
-// 1 / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3): gelu_tanh(v) = v times it.
-__device__ __forceinline__ float gelu_gate(float v) {
-  const float u2 = 1.5957691216057308f * v * __builtin_fmaf(0.044715f * v, v, 1.0f);
-  return 1.0f / (1.0f + expf(-u2));
+// v within [lo, hi]; NaN stays.
+__device__ __forceinline__ float clamp_nan(float v, float lo, float hi) { return v > hi ? hi : (v < lo ? lo : v); }
+
+// exp(a + a_lo): the hardware exp2 of the rounded product with log2(e), times 1 + its error (and a_lo) to first order.
+__device__ __forceinline__ float exp_f32(float a, float a_lo) {
+  constexpr float kLog2e = 1.44269504088896341f, kLog2eLo = 1.92596299e-08f, kLn2 = 0.693147180559945309f;
+  const float hi = a * kLog2e;
+  const float lo = __builtin_fmaf(a, kLog2e, -hi) + __builtin_fmaf(a, kLog2eLo, a_lo * kLog2e);
+  return __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.0f);
 }
 
-// silu_f32 for any finite v: its exponent overflows past 2.3e38, and from 64 on silu(v) is v in fp32.
-__device__ __forceinline__ float silu_any(float v) { return v > 64.0f ? v : silu_f32(v); }
+// 1 / (1 + exp(-v)): 0 from -88 down, 1 from 17 up, nothing overflows to NaN.
+__device__ __forceinline__ float sigmoid_f32(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_f32(-clamp_nan(v, -128.0f, 64.0f), 0.0f));
+}
 
-__device__ __forceinline__ float act1(int act, float v) {
+// Phi(v) and exp(-v^2 / 2).  Phi(-|v|) = exp(-v^2 / 2) t P(t), t = 1 / (1 + 0.31 |v|), P the polynomial of degree 9 with the
+// smallest relative error (1.2e-8 for |v| <= 41; 3e-7 as evaluated in fp32), fitted to erfcx(|v| / sqrt 2) / (2 t): no cancellation
+// for negative v, and one exponential for the function and its slope.
+__device__ __forceinline__ float normal_cdf(float v, float& e) {
+  const float x = fabsf(clamp_nan(v, -40.0f, 40.0f)), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, x, 1.0f));
+  const float xx = x * x;
+  e = exp_f32(-0.5f * xx, -0.5f * __builtin_fmaf(x, x, -xx));
+  float p = -0.02082189917564392f;
+  p = __builtin_fmaf(p, t, 0.10342404991388321f);
+  p = __builtin_fmaf(p, t, -0.1837586760520935f);
+  p = __builtin_fmaf(p, t, 0.11884111911058426f);
+  p = __builtin_fmaf(p, t, -0.034121375530958176f);
+  p = __builtin_fmaf(p, t, 0.07190302759408951f);
+  p = __builtin_fmaf(p, t, 0.08510398119688034f);
+  p = __builtin_fmaf(p, t, 0.11210367828607559f);
+  p = __builtin_fmaf(p, t, 0.12365353852510452f);
+  p = __builtin_fmaf(p, t, 0.12367255240678787f);
+  const float tail = e * t * p;
+  return v > 0.0f ? 1.0f - tail : tail;
+}
+
+// sqrt(2/pi) (v + 0.044715 v^3), doubled: gelu_tanh(v) = v sigmoid of it.
+__device__ __forceinline__ float gelu_arg(float v) {
+  return 1.5957691216057308f * v * __builtin_fmaf(0.044715f * v, v, 1.0f);
+}
+
+// The activation's value, and its slope (ReLU's at 0: 0).  act: the same for every lane.
+__device__ __forceinline__ float act_and_slope(int act, float v, float& slope) {
   switch (act) {
-    case kActRelu: return v < 0.0f ? 0.0f : v;
-    case kActSilu: return silu_any(v);
-    case kActGelu: return v * normal_cdf(v);
-    case kActGeluTanh: return v * gelu_gate(v);
-    default: return v;
+    case kActRelu:
+      slope = v > 0.0f ? 1.0f : 0.0f;
+      return v < 0.0f ? 0.0f : v;
+    case kActSilu: {
+      const float s = sigmoid_f32(v);
+      slope = s * __builtin_fmaf(v, 1.0f - s, 1.0f);
+      return v * s;
+    }
+    case kActGelu: {
+      float e;
+      const float c = normal_cdf(v, e);
+      slope = __builtin_fmaf(clamp_nan(v, -40.0f, 40.0f) * 0.3989422804014327f, e, c);
+      return v * c;
+    }
+    case kActGeluTanh: {
+      const float w = clamp_nan(v, -16.0f, 16.0f), s = sigmoid_f32(gelu_arg(w));  // its gate is 0 or 1 from there on
+      slope = __builtin_fmaf(w * s * (1.0f - s) * 1.5957691216057308f, __builtin_fmaf(0.134145f * w, w, 1.0f), s);
+      return v * s;
+    }
+    default:
+      slope = 1.0f;
+      return v;
   }
 }
-__device__ __forceinline__ v4f act4(int act, v4f v) {  // act: the same for every lane
+__device__ __forceinline__ float act1(int act, float v) {
+  float slope;
+  return act_and_slope(act, v, slope);
+}
+__device__ __forceinline__ v4f act4(int act, v4f v) {
   if (act == kActNone) return v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = act1(act, v[i]);
   return v;
-}
-
-// The derivative (ReLU's at 0: 0).
-__device__ __forceinline__ float slope1(int act, float v) {
-  switch (act) {
-    case kActRelu: return v > 0.0f ? 1.0f : 0.0f;
-    case kActSilu: {
-      const float s = 1.0f / (1.0f + expf(-v));
-      return s * __builtin_fmaf(v, 1.0f - s, 1.0f);
-    }
-    case kActGelu: return __builtin_fmaf(v * 0.3989422804014327f, expf(-0.5f * v * v), normal_cdf(v));
-    case kActGeluTanh: {
-      const float s = gelu_gate(v);
-      return __builtin_fmaf(v * s * (1.0f - s) * 1.5957691216057308f, __builtin_fmaf(0.134145f * v, v, 1.0f), s);
-    }
-    default: return 1.0f;
-  }
-}
-
-// Both, from one evaluation of their common part: returns the slope.
-__device__ __forceinline__ float act_and_slope(int act, float v, float& value) {
-  switch (act) {
-    case kActSilu: {
-      const float s = 1.0f / (1.0f + expf(-v));
-      value = v * s;
-      return s * __builtin_fmaf(v, 1.0f - s, 1.0f);
-    }
-    case kActGelu: {
-      const float c = normal_cdf(v);
-      value = v * c;
-      return __builtin_fmaf(v * 0.3989422804014327f, expf(-0.5f * v * v), c);
-    }
-    case kActGeluTanh: {
-      const float s = gelu_gate(v);
-      value = v * s;
-      return __builtin_fmaf(v * s * (1.0f - s) * 1.5957691216057308f, __builtin_fmaf(0.134145f * v, v, 1.0f), s);
-    }
-    default:
-      value = act1(act, v);
-      return slope1(act, v);
-  }
 }
 
 }  // namespace moe
