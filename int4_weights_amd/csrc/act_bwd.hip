@@ -34,7 +34,7 @@ __device__ __forceinline__ Eight unpack8(const v4i w) {
 __device__ __forceinline__ v4i pack8(const Eight& e) {
   v4i w;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = (int)(f32_to_bf16_rne(e.v[2 * i]) | (f32_to_bf16_rne(e.v[2 * i + 1]) << 16));
+  for (int i = 0; i < 4; ++i) w[i] = (int)bf16_pair(e.v[2 * i], e.v[2 * i + 1]);
   return w;
 }
 

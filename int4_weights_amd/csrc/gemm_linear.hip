@@ -46,7 +46,7 @@ typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t v2u_any __attribute__((ext_vector_type(2), aligned(2)));
 
 __device__ __forceinline__ v2u_any bf16x4(const v4f v) {
-  return v2u_any{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16), f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
+  return v2u_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 // Elements at .. at + 3 (cnt of them are there) of an fp32 or bf16 row.
 __device__ __forceinline__ v4f load4(const void* p, bool f32, int64_t at, int cnt) {
@@ -87,7 +87,7 @@ __device__ __forceinline__ void store4(void* p, bool f32, int64_t at, int cnt, c
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < cnt) q[i] = (uint16_t)f32_to_bf16_rne(v[i]);
+      if (i < cnt) q[i] = (uint16_t)bf16_pair(v[i], 0.f);
   }
 }
 

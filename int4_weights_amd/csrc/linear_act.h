@@ -7,29 +7,28 @@ namespace moe {
 
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-// v within [lo, hi]; NaN stays.
-__device__ __forceinline__ float clamp_nan(float v, float lo, float hi) { return v > hi ? hi : (v < lo ? lo : v); }
+// v within [lo, hi].  (NaN becomes lo: the callers multiply by v itself, so that NaN comes out all the same.)
+__device__ __forceinline__ float within(float v, float lo, float hi) { return __builtin_amdgcn_fmed3f(v, lo, hi); }
 
-// exp(a + a_lo): the hardware exp2 of the rounded product with log2(e), times 1 + its error (and a_lo) to first order.
-__device__ __forceinline__ float exp_f32(float a, float a_lo) {
+// exp(a): the hardware exp2 of the rounded product with log2(e), times 1 + the product's error to first order.
+__device__ __forceinline__ float exp_f32(float a) {
   constexpr float kLog2e = 1.44269504088896341f, kLog2eLo = 1.92596299e-08f, kLn2 = 0.693147180559945309f;
   const float hi = a * kLog2e;
-  const float lo = __builtin_fmaf(a, kLog2e, -hi) + __builtin_fmaf(a, kLog2eLo, a_lo * kLog2e);
+  const float lo = __builtin_fmaf(a, kLog2eLo, __builtin_fmaf(a, kLog2e, -hi));
   return __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.0f);
 }
 
-// 1 / (1 + exp(-v)): 0 from -88 down, 1 from 17 up, nothing overflows to NaN.
+// 1 / (1 + exp(-v)): 0 from -88 down, 1 from 17 up; the bounds keep what overflows from becoming NaN.
 __device__ __forceinline__ float sigmoid_f32(float v) {
-  return __builtin_amdgcn_rcpf(1.0f + exp_f32(-clamp_nan(v, -128.0f, 64.0f), 0.0f));
+  return __builtin_amdgcn_rcpf(1.0f + exp_f32(within(-v, -64.0f, 128.0f)));
 }
 
 // Phi(v) and exp(-v^2 / 2).  Phi(-|v|) = exp(-v^2 / 2) t P(t), t = 1 / (1 + 0.31 |v|), P the polynomial of degree 9 with the
 // smallest relative error (1.2e-8 for |v| <= 41; 3e-7 as evaluated in fp32), fitted to erfcx(|v| / sqrt 2) / (2 t): no cancellation
 // for negative v, and one exponential for the function and its slope.
 __device__ __forceinline__ float normal_cdf(float v, float& e) {
-  const float x = fabsf(clamp_nan(v, -40.0f, 40.0f)), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, x, 1.0f));
-  const float xx = x * x;
-  e = exp_f32(-0.5f * xx, -0.5f * __builtin_fmaf(x, x, -xx));
+  const float x = fabsf(v), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, x, 1.0f));
+  e = exp_f32(fmaxf(-0.5f * x * x, -200.0f));
   float p = -0.02082189917564392f;
   p = __builtin_fmaf(p, t, 0.10342404991388321f);
   p = __builtin_fmaf(p, t, -0.1837586760520935f);
@@ -49,6 +48,13 @@ __device__ __forceinline__ float gelu_arg(float v) {
   return 1.5957691216057308f * v * __builtin_fmaf(0.044715f * v, v, 1.0f);
 }
 
+// Two fp32 values as bf16, rounded to nearest even by the hardware (NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // The activation's value, and its slope (ReLU's at 0: 0).  act: the same for every lane.
 __device__ __forceinline__ float act_and_slope(int act, float v, float& slope) {
   switch (act) {
@@ -63,12 +69,13 @@ __device__ __forceinline__ float act_and_slope(int act, float v, float& slope) {
     case kActGelu: {
       float e;
       const float c = normal_cdf(v, e);
-      slope = __builtin_fmaf(clamp_nan(v, -40.0f, 40.0f) * 0.3989422804014327f, e, c);
+      slope = __builtin_fmaf(v * 0.3989422804014327f, e, c);
       return v * c;
     }
     case kActGeluTanh: {
-      const float w = clamp_nan(v, -16.0f, 16.0f), s = sigmoid_f32(gelu_arg(w));  // its gate is 0 or 1 from there on
+      const float w = within(v, -16.0f, 16.0f), s = sigmoid_f32(gelu_arg(w));  // its gate is 0 or 1 from there on
       slope = __builtin_fmaf(w * s * (1.0f - s) * 1.5957691216057308f, __builtin_fmaf(0.134145f * w, w, 1.0f), s);
+      slope = v == v ? slope : v;  // NaN stays
       return v * s;
     }
     default:
