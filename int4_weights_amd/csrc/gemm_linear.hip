@@ -91,6 +91,34 @@ __device__ __forceinline__ void store4(void* p, bool f32, int64_t at, int cnt, c
   }
 }
 
+// Eight bf16 columns.
+__device__ __forceinline__ void store8(uint16_t* p, const v4f v) {
+  typedef float v4b_any __attribute__((ext_vector_type(4), aligned(2)));
+  *(v4b_any*)p = v;
+}
+// Lanes 8 .. 15 of each row of 16 get b of lane - 8 in a; lanes 0 .. 7 get a of lane + 8 in b.
+__device__ __forceinline__ void swap8(v4f& a, v4f& b) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int x = __float_as_int(a[e]), y = __float_as_int(b[e]);
+    a[e] = __int_as_float(__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false));  // row_ror:8, lanes 8 .. 15
+    b[e] = __int_as_float(__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false));
+  }
+}
+// Of the lanes' 4 columns in two neighbouring 16-column blocks, rounded to bf16: lane group lg gets 8 columns, of block lg & 1,
+// from 8 (lg >> 1) on.
+__device__ __forceinline__ v4f join_columns(const v4f a, const v4f b) {
+  v4f o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const auto r = __builtin_amdgcn_permlane16_swap(bf16_pair(a[2 * h], a[2 * h + 1]), bf16_pair(b[2 * h], b[2 * h + 1]),
+                                                    false, false);  // the first of groups 1, 3 for the second of groups 0, 2
+    o[h] = __uint_as_float(r[0]);
+    o[2 + h] = __uint_as_float(r[1]);
+  }
+  return o;
+}
+
 // Columns n .. n + 3 of row m; NO: how many columns D has.  v: the product (gated: gate and up).
 template <bool GATED>
 __device__ __forceinline__ void epilogue4(const LinearArgs& a, int m, int n, v4f v, v4f up) {
@@ -272,6 +300,8 @@ struct LinTileT {
     for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int j = 0; j < CB; ++j) asm volatile("" : "+v"(acc[i][j]));
+    const int NO = GATED ? a.N / 2 : a.N;
+    if (a.splits == 1 && m0 + C::BM <= a.M && n0 + (GATED ? C::BN / 2 : C::BN) <= NO) return store_whole(acc);
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
       const int m = m0 + wm + 16 * i + l16;
@@ -281,6 +311,83 @@ struct LinTileT {
       } else {
 #pragma unroll
         for (int j = 0; j < CB; ++j) finish4<false>(a, m, n0 + wn + 16 * j + 4 * lg, acc[i][j], v4f{0.f, 0.f, 0.f, 0.f});
+      }
+    }
+  }
+  // A tile inside the matrix: no lane is masked; the bias is read once per column block, a row block's addends before they are
+  // needed, and lanes exchange columns so that stores write whole lines.
+  __device__ __forceinline__ void store_whole(v4f (&acc)[RB][CB]) const {
+    constexpr int OB = GATED ? CB / 2 : CB;  // column blocks of D
+    const int NO = GATED ? a.N / 2 : a.N, n = n0 + (GATED ? wn / 2 : wn);
+    v4f bias[CB];
+    if (a.bias) {
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+        bias[j] = load4(a.bias, a.bias_f32, GATED ? n + 8 * (j & ~1) + 4 * lg + (j & 1 ? NO : 0) : n + 16 * j + 4 * lg, 4);
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int m = m0 + wm + 16 * i;
+      v4f c[OB], o[OB];
+      if (a.C) {
+#pragma unroll
+        for (int j = 0; j < OB; ++j) c[j] = load4(a.C, a.c_f32, (int64_t)(m + l16) * a.ldc + n + 16 * j + 4 * lg, 4);
+      }
+      if (a.bias) {
+#pragma unroll
+        for (int j = 0; j < CB; ++j) acc[i][j] += bias[j];
+      }
+#pragma unroll
+      for (int j = 0; j < OB; ++j) o[j] = acc[i][GATED ? 2 * j : j];
+      if (a.pre) {
+        put<OB>(a.pre, false, a.ldp, m, n, o);
+        if constexpr (GATED) {
+          v4f up[OB];
+#pragma unroll
+          for (int j = 0; j < OB; ++j) up[j] = acc[i][2 * j + 1];
+          put<OB>(a.pre, false, a.ldp, m, NO + n, up);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < OB; ++j) {
+        o[j] = act4(a.act, o[j]);
+        if (GATED) o[j] *= acc[i][GATED ? 2 * j + 1 : 0];
+        if (a.C) o[j] += c[j];
+      }
+      put<OB>(a.D, a.d_f32, a.ldd, m, n, o);
+    }
+  }
+  // 16 rows from m on of B 16-column blocks from n on; v[j]: columns 4 lg .. + 3 of block j of row l16.  As they are, an
+  // instruction would write 16 rows in pieces of 32 bytes (bf16) or 64.
+  template <int B>
+  __device__ __forceinline__ void put(void* p, bool f32, int64_t ld, int m, int n, const v4f (&v)[B]) const {
+    const int hi = l16 >> 3, l8 = l16 & 7;
+    if constexpr (B == 1) {
+      store4(p, f32, (int64_t)(m + l16) * ld + n + 4 * lg, 4, v[0]);
+    } else if (f32) {
+#pragma unroll
+      for (int j = 0; j < B; j += 2) {
+        v4f x[2] = {v[j], v[j + 1]};
+        swap8(x[0], x[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v4f_any* q = (v4f_any*)((float*)p + (int64_t)(m + 8 * h + l8) * ld + n + 16 * (j + hi) + 4 * lg);
+          // past the caches where whole lines are written; rows that share lines with their neighbours meet them in the L2
+          if (ld % 4 == 0) __builtin_nontemporal_store(x[h], q);
+          else *q = x[h];
+        }
+      }
+    } else {
+      v4f x[B / 2];  // 8 columns of bf16 each
+#pragma unroll
+      for (int j = 0; j < B; j += 2) x[j / 2] = join_columns(v[j], v[j + 1]);
+      const int n8 = n + 16 * (lg & 1) + 8 * (lg >> 1);
+      if constexpr (B == 4) {
+        swap8(x[0], x[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) store8((uint16_t*)p + (int64_t)(m + 8 * h + l8) * ld + n8 + 32 * hi, x[h]);
+      } else {
+        store8((uint16_t*)p + (int64_t)(m + l16) * ld + n8, x[0]);
       }
     }
   }
