@@ -393,9 +393,13 @@ struct LinTileT {
   }
 };
 
-// S slots: block kb + S - 1 is copied while block kb is multiplied; one barrier a step.
-template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN, int S>
-__global__ __launch_bounds__(512) void gemm_linear_kernel(const LinearArgs a) {
+// Smaller tiles: fragments fit the registers twice, so block kb + 1's are read while block kb is multiplied, and block kb + 4 is copied
+// meanwhile into the slot that block kb left when it was read.  The loop is unrolled over the 4 slots, so that slots and offsets are
+// constants; reads and copies are laid out between the matrix instructions (in one go each, they take turns instead of
+// overlapping: 64x64 0.34 us a step).
+template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN>
+__global__ __launch_bounds__(512) void gemm_linear_small_kernel(const LinearArgs a) {
+  constexpr int S = 4;
   using C = LinCfg<RB, CB, WM, WN, S>;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
   LinTileT<TA, TW, GATED, RB, CB, WM, WN, S> T(a, sm);
@@ -405,38 +409,83 @@ __global__ __launch_bounds__(512) void gemm_linear_kernel(const LinearArgs a) {
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  auto issue = [&](int kb) {
-    T.template end_of_k<true>(kb);
-    T.template end_of_k<false>(kb);
-#pragma unroll
-    for (int i = 0; i < C::kPw; ++i) {
-      const int q = T.wv + C::NW * i;
-      T.copy_to(i, 8 * q < C::BM ? T.abase : T.wbase, kb % S * C::kSlot + 1024 * q);
-    }
+  struct Regs {
+    v8bf w[CB][2], x[RB][2];
+  } reg[2];
+  // read r of a block in slot `slot`: halves of the weights' fragments, then of the rows'
+  auto read = [&](Regs& to, int slot, int r) {
+    const uint8_t* p = sm + slot * C::kSlot;
+    if (r < 2 * CB) to.w[r < 2 * CB ? r / 2 : 0][r & 1] = T.xw.frag(p + C::BM * 128, r / 2, r & 1);
+    else to.x[r < 2 * CB ? 0 : r / 2 - CB][r & 1] = T.xa.frag(p, r / 2 - CB, r & 1);
+  };
+  auto copy = [&](int slot, int i) {
+    const int q = T.wv + C::NW * i;
+    T.copy_to(i, 8 * q < C::BM ? T.abase : T.wbase, slot * C::kSlot + 1024 * q);
+  };
+  auto next_block = [&]() {
     T.abase += T.astep();
     T.wbase += T.wstep();
   };
-  for (int b = 0; b < S - 1; ++b)
-    if (kb0 + b < kb1) issue(kb0 + b);
-  for (int kb = kb0; kb < kb1; ++kb) {
-    if (kb + S - 2 < kb1) wait_vmcnt<(S - 2) * C::kPw>();
+  // block k in slot u (k - kb0 = u mod 4).  kind 2: block k + 4 is copied; 1: no more copies, but a next block; 0: the last block
+  auto step = [&](int k, auto uc, auto kind) {
+    constexpr int u = decltype(uc)::value, kd = decltype(kind)::value;
+    constexpr int NM = 2 * RB * CB, NF = 2 * (RB + CB);
+    const Regs& r = reg[u & 1];
+    Regs& next = reg[(u + 1) & 1];
+    if constexpr (kd == 2) {
+      T.template end_of_k<true>(k + S);
+      T.template end_of_k<false>(k + S);
+    }
+    static_for<0, NM>([&](auto mc) {
+      constexpr int m = decltype(mc)::value, h = m / (RB * CB), i = m / CB % RB, j = m % CB;
+      acc[i][j] = mma(r.w[j][h], r.x[i][h], acc[i][j]);
+      if constexpr (kd > 0) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+          if (f * NM / NF == m) read(next, (u + 1) & 3, f);
+      }
+      if constexpr (kd == 2) {
+#pragma unroll
+        for (int c = 0; c < C::kPw; ++c)
+          if (c * NM / C::kPw == m) copy(u, c);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (kd == 2) next_block();
+    if constexpr (kd > 0) {
+      wait_vmcnt<kd == 2 ? C::kPw*(S - 2) : 0>();  // block k + 2 is in the LDS
+      barrier_reads();                              // and block k + 1 in registers
+    }
+  };
+  if (kb0 < kb1) {
+    static_for<0, S>([&](auto u) {
+      const int k = kb0 + decltype(u)::value;
+      if (k < kb1) {
+        T.template end_of_k<true>(k);
+        T.template end_of_k<false>(k);
+#pragma unroll
+        for (int c = 0; c < C::kPw; ++c) copy(decltype(u)::value, c);
+        next_block();
+      }
+    });
+    const bool full = kb0 + S <= kb1;
+    if (full) wait_vmcnt<C::kPw*(S - 1)>();
     else wait_vmcnt<0>();
     barrier_reads();
-    if (kb + S - 1 < kb1) issue(kb + S - 1);
-    const uint8_t* sa = sm + (kb % S) * C::kSlot;
-    const uint8_t* sw = sa + C::BM * 128;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v8bf w[CB];
-#pragma unroll
-      for (int j = 0; j < CB; ++j) w[j] = T.xw.frag(sw, j, h);
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const v8bf x = T.xa.frag(sa, i, h);
-#pragma unroll
-        for (int j = 0; j < CB; ++j) acc[i][j] = mma(w[j], x, acc[i][j]);
-      }
-    }
+    for (int f = 0; f < 2 * (RB + CB); ++f) read(reg[0], 0, f);
+    if (full) wait_vmcnt<C::kPw*(S - 2)>();
+    barrier_reads();  // block kb0 is in registers, block kb0 + 1 in the LDS
+    int kb = kb0;
+    for (; kb + 2 * S <= kb1; kb += S)  // whole rounds of the ring
+      static_for<0, S>([&](auto u) { step(kb + decltype(u)::value, u, IntC<2>{}); });
+    for (; kb < kb1; kb += S)
+      static_for<0, S>([&](auto u) {
+        const int k = kb + decltype(u)::value;
+        if (k + S < kb1) step(k, u, IntC<2>{});
+        else if (k + 1 < kb1) step(k, u, IntC<1>{});
+        else if (k < kb1) step(k, u, IntC<0>{});
+      });
   }
   T.store(acc);
 }
@@ -582,13 +631,13 @@ __global__ __launch_bounds__(256) void gemm_linear_join_kernel(const LinearArgs 
   }
 }
 
-template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN, int S>
+template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN, bool BIG = false>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
-  using C = LinCfg<RB, CB, WM, WN, S>;
+  using C = LinCfg<RB, CB, WM, WN, 2>;
   const int NO = GATED ? a.N / 2 : a.N, BNO = GATED ? C::BN / 2 : C::BN;
   const dim3 grid(((a.M + C::BM - 1) / C::BM) * ((NO + BNO - 1) / BNO), a.splits);
-  if constexpr (RB >= 4) gemm_linear_big_kernel<TA, TW, GATED, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
-  else gemm_linear_kernel<TA, TW, GATED, RB, CB, WM, WN, S><<<grid, WM * WN * 64, 0, s>>>(a);
+  if constexpr (BIG) gemm_linear_big_kernel<TA, TW, GATED, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
+  else gemm_linear_small_kernel<TA, TW, GATED, RB, CB, WM, WN><<<grid, WM * WN * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t need = ((int64_t)a.M * (ws_half(a) / 4) + 255) / 256, cap = (int64_t)device_info().cus * 16;
@@ -598,8 +647,8 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
 
 // ----------------------------------------------------------------- stream --
 // Few rows (a decode step): every weight byte is used by one wave, so waves need nothing from one another.  A workgroup takes
-// 16 CB columns (gated: 8 CB outputs) and all 16 RB rows; its KS waves split K, each with a ring of S blocks of its own in LDS
-// (no barrier in the loop), and meet once at the end, where the partial sums are added in wave order.
+// 16 CB columns (gated: blocks of 8 gates and their 8 ups) and all 16 RB rows; its KS waves split K, each with a ring of S blocks
+// of its own in LDS (no barrier in the loop), and meet once at the end, where the partial sums are added in wave order.
 template <int RB, int CB, int KS, int S>
 struct LinStreamCfg {
   static constexpr int kBlock = (RB + CB) * 2048, kCopies = 2 * (RB + CB), kWave = S * kBlock;
@@ -632,9 +681,9 @@ __global__ __launch_bounds__(KS * 64) void gemm_linear_stream_kernel(const Linea
       int n = row - kRows;
       bool in = n0 + n < NO;
       if (GATED) {
-        const int j = (n >> 5) * 16 + (n & 15);
+        const int j = (n >> 4) * 8 + (n & 7);
         in = n0 + j < NO;
-        n = j + (n & 16 ? NO : 0);
+        n = j + (n & 8 ? NO : 0);
       }
       voff[q] = in ? Operand<false, 64>::offset(k, n, a.ldw) : kOut;
     }
@@ -697,13 +746,13 @@ __global__ __launch_bounds__(KS * 64) void gemm_linear_stream_kernel(const Linea
   __syncthreads();
   for (int q = threadIdx.x; q < kRows * kOuts / 4; q += KS * 64) {
     const int m = q / (kOuts / 4), n = 4 * (q % (kOuts / 4));
-    const int c = GATED ? (n >> 4) * 32 + (n & 15) : n;
+    const int c = GATED ? (n >> 3) * 16 + (n & 7) : n;
     v4f v = {0.f, 0.f, 0.f, 0.f}, up = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const float* p = (const float*)(sm + k * C::kWave) + m * (kCols + 4) + c;
       v += *(const v4f*)p;
-      if (GATED) up += *(const v4f*)(p + 16);
+      if (GATED) up += *(const v4f*)(p + 8);
     }
     epilogue4<GATED>(a, m, n0 + n, v, up);
   }
@@ -721,15 +770,17 @@ hipError_t launch_order(LinearArgs a, hipStream_t s) {
   const LinPlan p = plan_linear(a.M, a.N, a.K, TA || TW);
   a.splits = p.splits;
   if constexpr (!TA && !TW) {
-    if (p.kind == kLinStream16) return launch_stream<GATED, 1, GATED ? 2 : 1, 8, GATED ? 3 : 4>(a, s);
-    if (p.kind == kLinStream32) return launch_stream<GATED, 2, GATED ? 2 : 1, 8, GATED ? 2 : 3>(a, s);
-    if (p.kind == kLinStream64) return launch_stream<GATED, 4, GATED ? 2 : 1, 4, 3>(a, s);
+    const bool many = a.N > 16 * kLinCus;
+    if (p.kind == kLinStream16) return many ? launch_stream<GATED, 1, 2, 4, 5>(a, s) : launch_stream<GATED, 1, 1, 8, 4>(a, s);
+    if (p.kind == kLinStream32) return many ? launch_stream<GATED, 2, 2, 4, 4>(a, s) : launch_stream<GATED, 2, 1, 8, 3>(a, s);
+    if (p.kind == kLinStream64) return many ? launch_stream<GATED, 4, 2, 4, 3>(a, s) : launch_stream<GATED, 4, 1, 4, 3>(a, s);
   }
   switch (p.kind) {
-    case kLin64x64: return launch_tile<TA, TW, GATED, 2, 2, 2, 2, 4>(a, s);
-    case kLin64x128: return launch_tile<TA, TW, GATED, 2, 2, 2, 4, 4>(a, s);
-    case kLin128x128: return launch_tile<TA, TW, GATED, 4, 4, 2, 2, 2>(a, s);
-    default: return launch_tile<TA, TW, GATED, 8, 4, 2, 4, 2>(a, s);
+    case kLin64x64: return launch_tile<TA, TW, GATED, 2, 2, 2, 2>(a, s);
+    case kLin64x128: return launch_tile<TA, TW, GATED, 2, 2, 2, 4>(a, s);
+    case kLin128x128: return launch_tile<TA, TW, GATED, 4, 2, 2, 4>(a, s);
+    case kLin128x128two: return launch_tile<TA, TW, GATED, 4, 4, 2, 2, true>(a, s);
+    default: return launch_tile<TA, TW, GATED, 8, 4, 2, 4, true>(a, s);
   }
 }
 

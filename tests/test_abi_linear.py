@@ -32,9 +32,9 @@ def _p(v):
     (dict(D=None), NULL), (dict(A=P + 8), ALIGN), (dict(W=P + 2), ALIGN), (dict(lda=132), ALIGN), (dict(ldw=130), ALIGN),
     (dict(D=P + 1), ALIGN), (dict(D=P + 2, out=F32), ALIGN), (dict(bias=P + 2, btype=F32), ALIGN), (dict(bias=P + 1, btype=BF16), ALIGN),
     (dict(C=P + 2, ctype=F32), ALIGN), (dict(pre=P + 1), ALIGN), (dict(C=P + 4096, D=P + 4096, ldc=264), SHAPE),
-    (dict(C=P + 4096, D=P + 4096, ctype=F32), SHAPE), (dict(M=131, N=200, ldd=200, K=4096, lda=4096, ldw=4096, ws=None), WORKSPACE),
-    (dict(M=131, N=200, ldd=200, K=4096, lda=4096, ldw=4096, wsb=1024), WORKSPACE),
-    (dict(M=131, N=200, ldd=200, K=4096, lda=4096, ldw=4096, ws=P + 8), WORKSPACE), (EMPTY, OK), (dict(EMPTY, act=GATED | 2, ws=None), OK),
+    (dict(C=P + 4096, D=P + 4096, ctype=F32), SHAPE), (dict(M=131, N=200, ldd=200, K=8192, lda=8192, ldw=8192, ws=None), WORKSPACE),
+    (dict(M=131, N=200, ldd=200, K=8192, lda=8192, ldw=8192, wsb=1024), WORKSPACE),
+    (dict(M=131, N=200, ldd=200, K=8192, lda=8192, ldw=8192, ws=P + 8), WORKSPACE), (EMPTY, OK), (dict(EMPTY, act=GATED | 2, ws=None), OK),
 ])
 def test_product_refusals(kw, status):
     a = dict(A=P, lda=128, W=P, ldw=128, tr=0, D=P, out=BF16, ldd=256, bias=None, btype=F32, act=0, C=None, ctype=BF16, ldc=256,
@@ -70,7 +70,7 @@ def test_gradient_refusals(kw, status):
 def test_workspace_sizes():
     f, g = moe.moe_gemm_bf16_workspace_bytes, moe.moe_act_bwd_workspace_bytes
     assert f(-1, 8, 8) == f(8, 0, 8) == f(8, 8, -1) == f(1 << 27, 8, 8) == f(1 << 20, 1 << 20, 8) == -1
-    assert f(0, 8, 8) == 0 and f(8192, 8192, 4096) == 0 and f(131, 200, 4096) > 0
+    assert f(0, 8, 8) == 0 and f(8192, 8192, 4096) == 0 and f(131, 200, 8192) > 0
     assert g(-1, 8) == g(8, 0) == g(1 << 27, 8) == -1 and g(0, 8) == g(1024, 8) == 0 and g(1025, 8) == 33 * 8 * 4
 
 

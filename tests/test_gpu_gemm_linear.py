@@ -8,6 +8,7 @@ import torch
 import int4_weights_amd as moe
 import oracle
 from gpu_helpers import DEV, require_gpu
+from linear_shapes import REACHED
 
 pytestmark = pytest.mark.gpu
 
@@ -63,14 +64,7 @@ def make(order, M, N, K, seed=0, scale=0.3):
     return A, W, f64(A).T if ta else f64(A), f64(W).T if tw else f64(W)
 
 
-# sizes that reach every kernel (test_linear_plan.py), with rows, columns and K that end inside a tile, a copy and a block
-SHAPES = {
-    "nt": [(1, 1, 8), (1, 256, 7168), (16, 17, 72), (17, 130, 1000), (33, 64, 520), (64, 1000, 264), (5, 4099, 128), (65, 64, 64),
-           (131, 200, 2048), (100, 1000, 1032), (333, 1536, 512), (1024, 4096, 96), (1500, 1300, 200), (4100, 4090, 136)],
-    "nn": [(1, 8, 8), (3, 264, 712), (65, 64, 64), (131, 200, 2048), (333, 1536, 520), (1024, 4096, 96), (4100, 4088, 136)],
-    "tn": [(8, 8, 1), (64, 72, 3), (72, 264, 333), (200, 136, 2047), (1536, 512, 131), (1024, 4096, 65), (4104, 4088, 127)],
-}
-CASES = [(o, s) for o in SHAPES for s in SHAPES[o]]
+CASES = [(o, s) for o in REACHED for s in REACHED[o]]  # every kernel (test_linear_plan.py)
 
 
 @pytest.mark.parametrize("order,shape", CASES, ids=lambda v: v if isinstance(v, str) else "x".join(map(str, v)))
@@ -201,7 +195,7 @@ def test_limits_of_the_activations():
 
 def test_workspace_is_used_and_not_overrun():
     require_gpu()
-    M, N, K = 131, 200, 4096
+    M, N, K = 131, 200, 8192
     n = moe.moe_gemm_bf16_workspace_bytes(M, N, K)
     assert n > 0
     A, W, a, w = make("nt", M, N, K, 2)
@@ -216,7 +210,7 @@ def test_workspace_is_used_and_not_overrun():
 
 def test_streams_and_graph():
     require_gpu()
-    M, N, K = 131, 200, 4096
+    M, N, K = 131, 200, 8192
     A, W, _, _ = make("nt", M, N, K, 2)
     B, V, _, _ = make("tn", 512, 264, 300, 3)
     D, E = torch.empty(M, N, device=DEV), torch.empty(512, 264, device=DEV)
