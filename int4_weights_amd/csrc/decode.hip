@@ -84,71 +84,119 @@ __device__ __forceinline__ v4f mma(const v4i x, const v8bf w, const v4f c) {
 
 // ------------------------------------------------------------------ plan --
 struct Plan {
-  int16_t id[kRoutes];      // expert of each route, -1 if none
-  int32_t job[kRoutes];     // expert | row block << 16, experts in order of their first route
-  int njobs;
+  uint32_t* job;    // [R] expert | rows << 10 | (first place in order) << 15
+  uint16_t* order;  // [R] routes grouped by expert
+  int* njobs;
+  static constexpr int bytes(int R) { return 6 * R + 4; }
+  __device__ __forceinline__ Plan(uint8_t* mem, int R) {
+    njobs = (int*)mem;
+    job = (uint32_t*)(mem + 4);
+    order = (uint16_t*)(job + R);
+  }
+  __device__ __forceinline__ static int expert(uint32_t j) { return j & 1023; }
+  __device__ __forceinline__ static int rows(uint32_t j) { return j >> 10 & 31; }
+  __device__ __forceinline__ int route(uint32_t j, int i) const { return order[(j >> 15) + i]; }
 };
 
-// Every thread of the workgroup calls it.  first/count: kMaxExperts ints each, used before anything else in LDS is.
-template <int BR>
-__device__ void plan(Plan& p, int* first, int* count, const int32_t* ids, int R, int E, int32_t* status) {
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    first[e] = 0x7fffffff;
-    count[e] = 0;
+// Sums of v over this lane and the lanes before it, inside the VALU: within rows of 16 lanes, then over the rows.
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast:15 to rows 1, 3
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast:31 to rows 2, 3
+  return v;
+}
+
+constexpr int kFewRoutes = 32;  // so many routes are grouped by one wave, one after another, with one barrier
+
+// Every thread of the workgroup calls it.  count: kMaxExperts ints, used before anything else in LDS is.  A route's place among
+// its expert's is first whatever the atomics make it; SORTED: then the order of the routes, the same in every workgroup, as it has
+// to be where several of them share a job.  (A row's sums do not depend on the rows beside it.)
+template <int BR, int NT, bool SORTED>
+__device__ void plan(const Plan& p, int* count, const DecodeArgs& a, bool report) {
+  const int R = a.T * a.k;
+  if (R <= kFewRoutes) {
+    if (threadIdx.x < kWave) {
+      const int lane = lane_id();
+      int id = lane < R ? a.ids[lane] : -1;
+      if (report && __ballot(id >= a.E) != 0 && lane == 0) atomicOr(a.status, 1);
+      if (id >= a.E) id = -1;
+      int at = 0, jobs = 0;
+      for (int j = 0; j < R; ++j) {
+        const int e = __builtin_amdgcn_readlane(id, j);
+        const uint64_t same = __ballot(id == e);
+        if (e < 0 || (same & ((1ull << j) - 1)) != 0) continue;  // none, or done
+        if (id == e) p.order[at + __popcll(same & lanemask_lt())] = (uint16_t)lane;
+        const int n = __popcll(same);
+        for (int b = 0; b < n; b += BR, ++jobs)
+          if (lane == 0) p.job[jobs] = (uint32_t)e | (uint32_t)min(n - b, BR) << 10 | (uint32_t)(at + b) << 15;
+        at += n;
+      }
+      if (lane == 0) *p.njobs = jobs;
+    }
+    __syncthreads();
+    return;
+  }
+  for (int e = threadIdx.x; e < a.E; e += NT) count[e] = 0;
+  int id[kRoutes / NT], place[kRoutes / NT];
+#pragma unroll
+  for (int q = 0; q < kRoutes / NT; ++q) {
+    const int i = threadIdx.x + NT * q;
+    id[q] = i < R ? a.ids[i] : -1;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < R; i += blockDim.x) {
-    const int id = ids[i];
-    const bool ok = (uint32_t)id < (uint32_t)E;
-    p.id[i] = (int16_t)(ok ? id : -1);
-    if (ok) {
-      atomicMin(first + id, i);  // integers: the order does not matter
-      atomicAdd(count + id, 1);
-    } else if (id >= E && status) {
-      atomicOr(status, 1);       // MOE_DEV_ID_RANGE
+#pragma unroll
+  for (int q = 0; q < kRoutes / NT; ++q) {
+    if (id[q] >= a.E) {
+      if (report) atomicOr(a.status, 1);  // MOE_DEV_ID_RANGE
+      id[q] = -1;
     }
+    if (id[q] >= 0) place[q] = atomicAdd(count + id[q], 1);
   }
   __syncthreads();
   if (threadIdx.x < kWave) {
-    int base = 0;
-    for (int c = 0; c < R; c += kWave) {
-      const int i = c + lane_id();
-      const int id = i < R ? p.id[i] : -1;
-      const int n = id >= 0 && first[id] == i ? (count[id] + BR - 1) / BR : 0;
-      int pre = n;
-#pragma unroll
-      for (int d = 1; d < kWave; d <<= 1) {
-        const int v = __shfl_up(pre, d);
-        if (lane_id() >= d) pre += v;
-      }
-      for (int b = 0; b < n; ++b) p.job[base + pre - n + b] = id | (b << 16);
-      base += __shfl(pre, kWave - 1);
+    uint32_t base = 0;  // routes | jobs << 16
+    for (int c = 0; c < a.E; c += kWave) {
+      const int e = c + lane_id(), n = e < a.E ? count[e] : 0, jobs = (n + BR - 1) / BR;
+      const uint32_t pre = wave_prefix((uint32_t)n | (uint32_t)jobs << 16);
+      const uint32_t mine = base + pre - ((uint32_t)n | (uint32_t)jobs << 16);
+      const int at = mine & 0xffff;
+      if (n > 0) count[e] = at | n << 16;
+      for (int b = 0; b < jobs; ++b)
+        p.job[(mine >> 16) + b] = (uint32_t)e | (uint32_t)min(n - b * BR, BR) << 10 | (uint32_t)(at + b * BR) << 15;
+      base += (uint32_t)__builtin_amdgcn_readlane((int)pre, kWave - 1);
     }
-    if (threadIdx.x == 0) p.njobs = base;
+    if (threadIdx.x == 0) *p.njobs = (int)(base >> 16);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kRoutes / NT; ++q) {
+    const int i = threadIdx.x + NT * q;
+    if (id[q] >= 0) p.order[(count[id[q]] & 0xffff) + place[q]] = (uint16_t)i;
+  }
+  __syncthreads();
+  if (!SORTED) return;
+#pragma unroll
+  for (int q = 0; q < kRoutes / NT; ++q) {
+    if (id[q] < 0) continue;
+    const int at = count[id[q]] & 0xffff, n = count[id[q]] >> 16, i = threadIdx.x + NT * q;
+    place[q] = at;
+    for (int j = 0; j < n; ++j) place[q] += p.order[at + j] < i;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kRoutes / NT; ++q) {
+    const int i = threadIdx.x + NT * q;
+    if (id[q] >= 0) p.order[place[q]] = (uint16_t)i;
   }
   __syncthreads();
 }
 
-// The routes of a job in route order into list[0 .. BR) (wave-private LDS); returns how many.
-template <int BR>
-__device__ __forceinline__ int job_rows(const Plan& p, int job, int R, int* list) {
-  const int e = job & 0xffff, lo = (job >> 16) * BR;
-  int seen = 0;
-  for (int c = 0; c < R; c += kWave) {
-    const int i = c + lane_id();
-    const bool hit = i < R && p.id[i] == e;
-    const uint64_t m = __ballot(hit);
-    const int rank = seen + __popcll(m & lanemask_lt()) - lo;
-    if (hit && rank >= 0 && rank < BR) list[rank] = i;
-    seen += __popcll(m);
-    if (seen >= lo + BR) break;
-  }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  return min(uniform(seen) - lo, BR);
-}
-
 // ---------------------------------------------------------------- stream --
-// One wave's ring: blocks of NCB x 16 weight columns and BR rows, kAhead = S - 1 blocks in flight.
+// One wave's ring: S blocks of NCB x 16 weight columns and BR rows, all of them in flight while a block is multiplied (its
+// fragments go to registers first, so that its slot is filled anew at once).
 template <int F, bool PACKED, int NCB, int BR, int RING>
 struct Stream {
   using T = Fmt<F>;
@@ -197,9 +245,11 @@ struct Stream {
   }
 
   // Blocks kb0 .. kb1 of columns n(cb) = col0 + 16 cb for cb < NCB/2, col1 + 16 (cb - NCB/2) above (NCB 1: col0), for the
-  // rows list[0 .. m) >> shift of x.
-  __device__ __forceinline__ void produce(int e, int col0, int col1, int kb0, int kb1, const int* list, int m, bool tokens,
-                                          int k) {
+  // job's rows of x: its tokens' (TOKENS; per_k = ceil(2^16 / k): route / k in one product, exact for routes below 2^10 and k up to 64)
+  // or its routes'.
+  template <bool TOKENS>
+  __device__ __forceinline__ void produce(const Plan& p, uint32_t job, uint32_t per_k, int col0, int col1, int kb0, int kb1) {
+    const int e = p.expert(job), m = p.rows(job);
     const int64_t rowb = F == kInt4 ? side.K / 2 : F == kFp8 ? side.K : 2 * side.K;
     const uint8_t* we = side.W + (int64_t)e * side.N * rowb;
 #pragma unroll
@@ -211,9 +261,8 @@ struct Stream {
     for (int q = 0; q < XP; ++q) {
       const int row = T::kRowsPerPiece * q + lane / T::kXChunks, c = lane % T::kXChunks;
       const int sw = F == kBf16 ? (row >> 1) & 7 : row & 15;
-      int r = list[min(row, m - 1)];
-      if (tokens) r /= k;
-      xvoff[q] = (uint32_t)r * (uint32_t)side.K * 2u + 16u * (c ^ sw) + (uint32_t)kb0 * T::kXRow;
+      const uint32_t r = (uint32_t)p.route(job, min(row, m - 1));
+      xvoff[q] = (TOKENS ? r * per_k >> 16 : r) * (uint32_t)side.K * 2u + 16u * (c ^ sw) + (uint32_t)kb0 * T::kXRow;
     }
     if constexpr (F == kFp8) {  // lane: the scale of column block lane % NCB
       const int cb = lane % NCB, KB = side.K / 128;
@@ -254,70 +303,82 @@ struct Stream {
     ++pkb;
   }
 
-  // Multiply the oldest block into acc.  kb and col0/col1 are the consumer's (4-bit scales lie in either half of a dword).
-  __device__ __forceinline__ void consume(v4f (&acc)[NCB], int kb, int col0, int col1) {
+  // The oldest block's fragments, in registers.
+  struct Frags {
+    v4i w[NCB][T::kPieces], x[F == kBf16 ? 2 : 4];
+    uint32_t s[NCB];  // FP8: the scale; 4-bit: a dword with the scale in either half
+  };
+  __device__ __forceinline__ void read(Frags& f) {
     const uint8_t* w = ring + cslot * kSlot;
     const uint8_t* xs = w + kWBytes;
     const uint8_t* sc = xs + kXBytes;
     const int row = l16 & (BR - 1);  // the rows past BR repeat; nobody reads their sums
     if constexpr (F == kBf16) {
-      const int fx = (row >> 1) & 7, fw = (l16 >> 1) & 7;
-      v4i xf[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) xf[h] = *(const v4i*)(xs + row * 128 + 16 * ((4 * h + lg) ^ fx));
-#pragma unroll
-      for (int cb = 0; cb < NCB; ++cb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v4i wf = *(const v4i*)(w + cb * 2048 + (PACKED ? 1024 * h + 16 * lane : l16 * 128 + 16 * ((4 * h + lg) ^ fw)));
-          acc[cb] = mma(xf[h], __builtin_bit_cast(v8bf, wf), acc[cb]);
-        }
+      for (int h = 0; h < 2; ++h) f.x[h] = *(const v4i*)(xs + row * 128 + 16 * ((4 * h + lg) ^ ((row >> 1) & 7)));
     } else if constexpr (F == kFp8) {
-      const int fw = (l16 >> 1) & 7;
-      v4i xf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.x[i] = *(const v4i*)(xs + row * 256 + 16 * ((8 * (i >> 1) + 2 * lg + (i & 1)) ^ row));
+    } else {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) f.x[d] = *(const v4i*)(xs + row * 256 + 16 * ((PACKED ? 4 * d + lg : 4 * lg + d) ^ row));
+    }
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) {
+#pragma unroll
+      for (int h = 0; h < T::kPieces; ++h) {
+        const int at = PACKED ? 1024 * h + 16 * lane
+                              : F == kInt4 ? l16 * 64 + 16 * (lg ^ (l16 >> 2)) : l16 * 128 + 16 * ((4 * h + lg) ^ ((l16 >> 1) & 7));
+        f.w[cb][h] = *(const v4i*)(w + cb * T::kPieces * 1024 + at);
+      }
+      if constexpr (F == kFp8) f.s[cb] = *(const uint32_t*)(sc + 4 * cb);
+      if constexpr (F == kInt4) f.s[cb] = *(const uint32_t*)(sc + 4 * (16 * cb + l16));
+    }
+    cslot = cslot + 1 == S ? 0 : cslot + 1;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot may be filled anew
+  }
+  // acc += the block.  kb and col0/col1 are the consumer's (4-bit scales lie in either half of a dword).
+  __device__ __forceinline__ void multiply(const Frags& f, v4f (&acc)[NCB], int kb, int col0, int col1) const {
+    if constexpr (F == kBf16) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) xf[2 * h + i] = *(const v4i*)(xs + row * 256 + 16 * ((8 * h + 2 * lg + i) ^ row));
+        for (int cb = 0; cb < NCB; ++cb) acc[cb] = mma(f.x[h], __builtin_bit_cast(v8bf, f.w[cb][h]), acc[cb]);
+    } else if constexpr (F == kFp8) {
+      v4f s[NCB];
 #pragma unroll
-      for (int cb = 0; cb < NCB; ++cb) {
-        v4f s = {0.f, 0.f, 0.f, 0.f};
+      for (int cb = 0; cb < NCB; ++cb) s[cb] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v4i wf = *(const v4i*)(w + cb * 2048 + (PACKED ? 1024 * h + 16 * lane : l16 * 128 + 16 * ((4 * h + lg) ^ fw)));
-          s = mma(xf[2 * h], widen_fp8(wf[0], wf[1]), s);
-          s = mma(xf[2 * h + 1], widen_fp8(wf[2], wf[3]), s);
-        }
-        const float f = *(const float*)(sc + 4 * cb);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(f, s[i], acc[cb][i]);
-      }
+        for (int cb = 0; cb < NCB; ++cb)
+          s[cb] = mma(f.x[i], widen_fp8(f.w[cb][i >> 1][2 * (i & 1)], f.w[cb][i >> 1][2 * (i & 1) + 1]), s[cb]);
+#pragma unroll
+      for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(__uint_as_float(f.s[cb]), s[cb][i], acc[cb][i]);
     } else {
-      v4i xf[4];
       const v8bf m136 = {(__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f,
                          (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f};
-      v4f fix = {0.f, 0.f, 0.f, 0.f};
+      v4f s[NCB], fix = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int cb = 0; cb < NCB; ++cb) s[cb] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        xf[d] = *(const v4i*)(xs + row * 256 + 16 * ((PACKED ? 4 * d + lg : 4 * lg + d) ^ row));
-        if (!PACKED) xf[d] = nibble_order(xf[d]);
-        fix = mma(xf[d], m136, fix);
+        const v4i x = PACKED ? f.x[d] : nibble_order(f.x[d]);
+        fix = mma(x, m136, fix);
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) s[cb] = mma(x, widen_int4((uint32_t)f.w[cb][0][d]), s[cb]);
       }
 #pragma unroll
       for (int cb = 0; cb < NCB; ++cb) {
-        const v4i wf = *(const v4i*)(w + cb * 1024 + (PACKED ? 16 * lane : l16 * 64 + 16 * (lg ^ (l16 >> 2))));
-        v4f s = fix;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) s = mma(xf[d], widen_int4((uint32_t)wf[d]), s);
         const int n = (NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2)) + l16;
         const int half = PACKED ? ((n & 63) / 16) & 1 : (n * (side.K / 128) + kb) & 1;
-        const uint32_t two = *(const uint32_t*)(sc + 4 * (16 * cb + l16));
-        const float f = (float)__builtin_bit_cast(_Float16, (uint16_t)(half ? two >> 16 : two));
+        const float q = (float)__builtin_bit_cast(_Float16, (uint16_t)(half ? f.s[cb] >> 16 : f.s[cb]));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(f, s[i], acc[cb][i]);
+        for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(q, s[cb][i] + fix[i], acc[cb][i]);
       }
     }
-    cslot = cslot + 1 == S ? 0 : cslot + 1;
   }
 
   // Wait for the oldest block; `full`: S - 1 blocks were issued after it.
@@ -331,122 +392,144 @@ struct Stream {
 // -------------------------------------------------------------------- up --
 constexpr int kUpRing = 17 * 1024;
 
+// LDS: the rings, the waves' sums of a unit (twice where that leaves room for two workgroups on a compute unit: then a unit takes
+// one barrier), the plan.
+template <int F, int BR>
+struct UpCfg {
+  static constexpr int NCB = F == kInt4 ? 4 : 2, kCols = 8 * NCB;  // columns of h per unit
+  static constexpr int kRow = 16 * NCB + 2, kPart = kUpWaves * BR * kRow;
+  static constexpr int kBufs = 8 * kPart <= 10 * 1024 ? 2 : 1;
+  static constexpr int kPlanAt = kUpWaves * kUpRing + kBufs * kPart * 4;
+};
+
 template <int F, bool PACKED, int BR>
 __global__ __launch_bounds__(kUpWaves * 64) void decode_up_kernel(const DecodeArgs a) {
-  constexpr int NCB = F == kInt4 ? 4 : 2, kCols = 8 * NCB;  // columns of h per unit
+  using C = UpCfg<F, BR>;
+  constexpr int NCB = C::NCB, kCols = C::kCols;
   using St = Stream<F, PACKED, NCB, BR, kUpRing>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[kUpWaves * kUpRing];
-  __shared__ float part[2][kUpWaves][BR][16 * NCB + 4];
-  __shared__ Plan p;
-  __shared__ int lists[kUpWaves][2][16];
-  static_assert(sizeof(ring) >= 2 * kMaxExperts * sizeof(int), "the plan's tables lie in the rings");
-  const int R = a.T * a.k;
-  plan<BR>(p, (int*)ring, (int*)ring + kMaxExperts, a.ids, R, a.E, blockIdx.x == 0 ? a.status : nullptr);
+  extern __shared__ __attribute__((aligned(1024))) uint8_t dyn[];
+  uint8_t* ring = dyn;
+  float* part = (float*)(dyn + kUpWaves * kUpRing);
+  const Plan p(dyn + C::kPlanAt, a.T * a.k);
+  static_assert(kUpWaves * kUpRing >= kMaxExperts * (int)sizeof(int), "the plan's table lies in the rings");
+  plan<BR, kUpWaves * 64, true>(p, (int*)ring, a, blockIdx.x == 0 && a.status);
   const int wv = uniform(threadIdx.x >> 6);
   const DecodeSide side{(const uint8_t*)a.W13, (const uint8_t*)a.S13, 2 * a.I, a.H};
   St st(side, (const uint8_t*)a.x, ring + wv * kUpRing);
-  const int ncol = a.I / kCols, units = p.njobs * ncol;
+  const int ncol = a.I / kCols, units = *p.njobs * ncol;
   const int nb = a.H / Fmt<F>::BK, kb0 = wv * nb / kUpWaves, kb1 = (wv + 1) * nb / kUpWaves;
-  int *plist = lists[wv][0], *clist = lists[wv][1];
 
   int pu = blockIdx.x;  // the producer's unit
   auto feed = [&]() {   // one block into the ring, if there is one
     if (st.pkb == st.pend) {
       if (pu >= units || kb0 == kb1) return false;
-      const int job = uniform(p.job[pu / ncol]), col = pu % ncol * kCols;
-      const int m = job_rows<BR>(p, job, R, plist);
-      st.produce(job & 0xffff, col, a.I + col, kb0, kb1, plist, m, true, a.k);
+      const int col = pu % ncol * kCols;
+      st.template produce<true>(p, (uint32_t)uniform((int)p.job[pu / ncol]), a.per_k, col, a.I + col, kb0, kb1);
       pu += gridDim.x;
     }
     st.issue();
     return true;
   };
+  bool full = true;  // S blocks were issued from the oldest on
 #pragma unroll 1
-  for (int i = 0; i < St::S - 1; ++i) feed();
+  for (int i = 0; i < St::S; ++i) full = feed();
   int buf = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
-    const int job = uniform(p.job[u / ncol]), col = u % ncol * kCols;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const uint32_t job = (uint32_t)uniform((int)p.job[u / ncol]);
+    const int col = u % ncol * kCols, m = p.rows(job);
     v4f acc[NCB];
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb) acc[cb] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int kb = kb0; kb < kb1; ++kb) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot that is filled next has been read
-      st.arrive(feed());
-      st.consume(acc, kb, col, a.I + col);
+      typename St::Frags f;
+      st.arrive(full);
+      st.read(f);
+      full = feed();
+      st.multiply(f, acc, kb, col, a.I + col);
     }
+    float* sums = part + buf * C::kPart;
+    float* mine = sums + wv * BR * C::kRow;
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (4 * st.lg + i < BR) part[buf][wv][4 * st.lg + i][16 * cb + st.l16] = acc[cb][i];
-    const int m = job_rows<BR>(p, job, R, clist);
-    barrier_lds();  // one per unit: the other buffer is written before its readers' next barrier
+        if (4 * st.lg + i < BR) mine[(4 * st.lg + i) * C::kRow + 16 * cb + st.l16] = acc[cb][i];
+    barrier_lds();  // with two buffers the only one: the other is written before this one's readers' next barrier
     for (int q = threadIdx.x; q < BR * kCols; q += kUpWaves * 64) {
       const int row = q / kCols, c = q % kCols;
       if (row < m) {
         float g = 0.f, up = 0.f;
 #pragma unroll
         for (int v = 0; v < kUpWaves; ++v) {
-          g += part[buf][v][row][c];
-          up += part[buf][v][row][kCols + c];
+          g += sums[(v * BR + row) * C::kRow + c];
+          up += sums[(v * BR + row) * C::kRow + kCols + c];
         }
-        a.h[(int64_t)clist[row] * a.I + col + c] = (uint16_t)f32_to_bf16_rne(g * sigmoid_f32(g) * up);
+        a.h[(int64_t)p.route(job, row) * a.I + col + c] = (uint16_t)f32_to_bf16_rne(g * sigmoid_f32(g) * up);
       }
     }
+    if (C::kBufs == 1) barrier_lds();
+    else buf ^= 1;
   }
 }
 
 // ------------------------------------------------------------------ down --
 constexpr int kDownRing = 13 * 1024;
-constexpr int kLdsMost = 150 * 1024;  // beside the plan
-static_assert(4 * kDownRing + 64 * kRoutes <= kLdsMost, "any number of routes fits four waves' rings");
+constexpr int kLdsMost = 160 * 1024;
+static_assert(4 * kDownRing + 74 * kRoutes + 4 <= kLdsMost, "any number of routes fits four waves' rings");
 
-// LDS: NW rings, then a line of 16 sums per share of K and route.
+// LDS: NW rings, then a line of 16 sums per share of K and route, then topk_weights and the plan.
 template <int F, bool PACKED, int BR, int NW>
 __global__ __launch_bounds__(NW * 64) void decode_down_kernel(const DecodeArgs a) {
   using St = Stream<F, PACKED, 1, BR, kDownRing>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t dyn[];
-  __shared__ Plan p;
-  __shared__ int lists[NW][2][16];
-  static_assert(NW * kDownRing >= 2 * kMaxExperts * (int)sizeof(int), "the plan's tables lie in the rings");
+  static_assert(NW * kDownRing >= kMaxExperts * (int)sizeof(int), "the plan's table lies in the rings");
   float* y = (float*)(dyn + NW * kDownRing);
   const int R = a.T * a.k, KS = a.ksplit;
-  plan<BR>(p, (int*)dyn, (int*)dyn + kMaxExperts, a.ids, R, a.E, nullptr);
+  float* share = y + 16 * KS * R;  // topk_weights, 0 for skipped slots, whose lines of sums are 0 too
+  for (int i = threadIdx.x; i < R; i += NW * 64) {
+    const bool on = (uint32_t)a.ids[i] < (uint32_t)a.E;
+    share[i] = on ? a.p[i] : 0.f;
+    if (!on)
+      for (int c = 0; c < 16 * KS; ++c) y[(c / 16 * R + i) * 16 + c % 16] = 0.f;
+  }
+  const Plan p((uint8_t*)(share + R), R);
+  plan<BR, NW * 64, false>(p, (int*)dyn, a, false);
   const int wv = uniform(threadIdx.x >> 6);
   const DecodeSide side{(const uint8_t*)a.W2, (const uint8_t*)a.S2, a.H, a.I};
   St st(side, (const uint8_t*)a.h, dyn + wv * kDownRing);
-  const int n0 = blockIdx.x * 16, items = p.njobs * KS, nb = a.I / Fmt<F>::BK;
-  int *plist = lists[wv][0], *clist = lists[wv][1];
+  const int n0 = blockIdx.x * 16, items = *p.njobs * KS, nb = a.I / Fmt<F>::BK;
 
   int pi = wv;
   auto feed = [&]() {
     if (st.pkb == st.pend) {
       if (pi >= items) return false;
-      const int job = uniform(p.job[pi / KS]), ks = pi % KS;
-      const int m = job_rows<BR>(p, job, R, plist);
-      st.produce(job & 0xffff, n0, n0, ks * nb / KS, (ks + 1) * nb / KS, plist, m, false, 1);
+      const int ks = pi % KS;
+      st.template produce<false>(p, (uint32_t)uniform((int)p.job[pi / KS]), 0, n0, n0, ks * nb / KS, (ks + 1) * nb / KS);
       pi += NW;
     }
     st.issue();
     return true;
   };
+  bool full = true;
 #pragma unroll 1
-  for (int i = 0; i < St::S - 1; ++i) feed();
+  for (int i = 0; i < St::S; ++i) full = feed();
   for (int it = wv; it < items; it += NW) {
-    const int job = uniform(p.job[it / KS]), ks = it % KS;
+    const uint32_t job = (uint32_t)uniform((int)p.job[it / KS]);
+    const int ks = it % KS, m = p.rows(job);
     v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
     const int kb1 = (ks + 1) * nb / KS;
 #pragma unroll 1
     for (int kb = ks * nb / KS; kb < kb1; ++kb) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      st.arrive(feed());
-      st.consume(acc, kb, n0, n0);
+      typename St::Frags f;
+      st.arrive(full);
+      st.read(f);
+      full = feed();
+      st.multiply(f, acc, kb, n0, n0);
     }
-    const int m = job_rows<BR>(p, job, R, clist);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (4 * st.lg + i < m) y[(ks * R + clist[4 * st.lg + i]) * 16 + st.l16] = acc[0][i];
+      if (4 * st.lg + i < m) y[(ks * R + p.route(job, 4 * st.lg + i)) * 16 + st.l16] = acc[0][i];
   }
   __syncthreads();
   for (int q = threadIdx.x; q < a.T * 16; q += NW * 64) {
@@ -455,22 +538,24 @@ __global__ __launch_bounds__(NW * 64) void decode_down_kernel(const DecodeArgs a
     float z = 0.f;
     for (int r = 0; r < a.k; ++r) {
       const int i = t * a.k + r;
-      if (p.id[i] < 0) continue;
       float v = y[i * 16 + c];
       for (int s = 1; s < KS; ++s) v += y[(s * R + i) * 16 + c];
-      z = __builtin_fmaf(a.p[i], v, z);
+      z = __builtin_fmaf(share[i], v, z);
     }
     if (a.C) z += bf16_to_f32(a.C[at]);
     a.Z[at] = (uint16_t)f32_to_bf16_rne(z);
   }
 }
 
+// A launch that asks for more than 64 KB of LDS.
+hipError_t allow_lds(const void* kernel) {
+  return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
+}
+
 template <int F, bool PACKED, int BR, int NW>
 hipError_t launch_down(const DecodeArgs& a, hipStream_t s) {
-  const size_t lds = NW * kDownRing + (size_t)a.ksplit * a.T * a.k * 64;
-  // more than 64 KB of LDS asked for at the launch
-  const hipError_t e = hipFuncSetAttribute((const void*)decode_down_kernel<F, PACKED, BR, NW>,
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
+  const size_t lds = NW * kDownRing + a.T * a.k * (64 * a.ksplit + 4) + Plan::bytes(a.T * a.k);
+  const hipError_t e = allow_lds((const void*)decode_down_kernel<F, PACKED, BR, NW>);
   if (e != hipSuccess) return e;
   decode_down_kernel<F, PACKED, BR, NW><<<a.H / 16, NW * 64, lds, s>>>(a);
   return hipGetLastError();
@@ -481,11 +566,15 @@ hipError_t launch_rows(DecodeArgs a, hipStream_t s) {
   const int R = a.T * a.k, nb = a.I / Fmt<F>::BK;
   const int64_t units = (int64_t)R * (a.I / (F == kInt4 ? 32 : 16));
   const int64_t cap = 2 * device_info().cus;
-  decode_up_kernel<F, PACKED, BR><<<(unsigned)(units < cap ? units : cap), kUpWaves * 64, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
+  a.per_k = (65536 + a.k - 1) / a.k;
+  hipError_t e = allow_lds((const void*)decode_up_kernel<F, PACKED, BR>);
+  if (e != hipSuccess) return e;
+  decode_up_kernel<F, PACKED, BR><<<(unsigned)(units < cap ? units : cap), kUpWaves * 64,
+                                    UpCfg<F, BR>::kPlanAt + Plan::bytes(R), s>>>(a);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   // few routes: their K is shared so that every wave has a part
-  const bool wide = a.H / 16 <= 256 && 8 * kDownRing + 64 * R <= kLdsMost;
+  const bool wide = a.H / 16 <= 256 && 8 * kDownRing + 74 * R + 4 <= kLdsMost;
   const int nw = wide ? 8 : 4;
   a.ksplit = 1;
   while (a.ksplit * R < nw && 2 * a.ksplit <= nb) a.ksplit *= 2;

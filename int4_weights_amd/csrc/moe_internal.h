@@ -182,6 +182,7 @@ struct DecodeArgs {
   int32_t* status;       // or nullptr
   int T, k, E, H, I;
   int ksplit;            // shares of I in the down-projection
+  uint32_t per_k;        // ceil(2^16 / k)
 };
 int64_t decode_workspace_bytes(int T, int k, int I);
 hipError_t launch_experts_decode(const DecodeArgs& a, hipStream_t s);
