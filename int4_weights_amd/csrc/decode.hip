@@ -14,7 +14,7 @@
 // rounded to bf16 once (it is the matrix instruction's operand; everything else up to Z stays in fp32).
 //
 // A job is an expert and up to BR of its routes.  Up-projection: a unit is a job and 16 (4-bit: 32) columns of h, whose K the 4
-// waves share; persistent workgroups walk over the units.  Down-projection: a workgroup owns 16 columns of Z and takes every
+// (8) waves share; persistent workgroups walk over the units.  Down-projection: a workgroup owns 16 columns of Z and takes every
 // job, its waves in turn; the rows' sums meet in LDS as one line per route, so the sum over a token's slots runs in slot order
 // whatever wave was first, and no partial result goes through memory.
 #include "linear_act.h"
@@ -27,7 +27,6 @@ namespace {
 
 constexpr int kBf16 = 0, kFp8 = 1, kInt4 = 2;
 constexpr int kRoutes = kDecodeMaxRoutes;
-constexpr int kUpWaves = 4;
 
 template <int F>
 struct Fmt {
@@ -109,7 +108,7 @@ __device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
   return v;
 }
 
-constexpr int kFewRoutes = 32;  // so many routes are grouped by one wave, one after another, with one barrier
+constexpr int kFewRoutes = 64;  // so many routes are grouped by one wave, with one barrier
 
 // Every thread of the workgroup calls it.  count: kMaxExperts ints, used before anything else in LDS is.  A route's place among
 // its expert's is first whatever the atomics make it; SORTED: then the order of the routes, the same in every workgroup, as it has
@@ -117,24 +116,29 @@ constexpr int kFewRoutes = 32;  // so many routes are grouped by one wave, one a
 template <int BR, int NT, bool SORTED>
 __device__ void plan(const Plan& p, int* count, const DecodeArgs& a, bool report) {
   const int R = a.T * a.k;
-  if (R <= kFewRoutes) {
+  if (R <= kFewRoutes) {  // a lane per route: its expert's routes are counted lane by lane
     if (threadIdx.x < kWave) {
       const int lane = lane_id();
       int id = lane < R ? a.ids[lane] : -1;
       if (report && __ballot(id >= a.E) != 0 && lane == 0) atomicOr(a.status, 1);
       if (id >= a.E) id = -1;
-      int at = 0, jobs = 0;
+      int n = 0, before = 0, first = 0;
+#pragma unroll 4
       for (int j = 0; j < R; ++j) {
-        const int e = __builtin_amdgcn_readlane(id, j);
-        const uint64_t same = __ballot(id == e);
-        if (e < 0 || (same & ((1ull << j) - 1)) != 0) continue;  // none, or done
-        if (id == e) p.order[at + __popcll(same & lanemask_lt())] = (uint16_t)lane;
-        const int n = __popcll(same);
-        for (int b = 0; b < n; b += BR, ++jobs)
-          if (lane == 0) p.job[jobs] = (uint32_t)e | (uint32_t)min(n - b, BR) << 10 | (uint32_t)(at + b) << 15;
-        at += n;
+        const bool same = id == __builtin_amdgcn_readlane(id, j);
+        if (same && n == 0) first = j;
+        n += same;
+        before += same && j < lane;
       }
-      if (lane == 0) *p.njobs = jobs;
+      const bool lead = id >= 0 && before == 0;
+      const uint32_t mine = lead ? (uint32_t)n | (uint32_t)((n + BR - 1) / BR) << 16 : 0u, pre = wave_prefix(mine);
+      const uint32_t base = pre - mine;
+      const int at = __shfl((int)(base & 0xffff), first);
+      if (id >= 0) p.order[at + before] = (uint16_t)lane;
+      if (lead)
+        for (int b = 0; b * BR < n; ++b)
+          p.job[(base >> 16) + b] = (uint32_t)id | (uint32_t)min(n - b * BR, BR) << 10 | (uint32_t)(at + b * BR) << 15;
+      if (lane == kWave - 1) *p.njobs = (int)(pre >> 16);
     }
     __syncthreads();
     return;
@@ -394,30 +398,30 @@ constexpr int kUpRing = 17 * 1024;
 
 // LDS: the rings, the waves' sums of a unit (twice where that leaves room for two workgroups on a compute unit: then a unit takes
 // one barrier), the plan.
-template <int F, int BR>
+template <int F, int BR, int NW>
 struct UpCfg {
   static constexpr int NCB = F == kInt4 ? 4 : 2, kCols = 8 * NCB;  // columns of h per unit
-  static constexpr int kRow = 16 * NCB + 2, kPart = kUpWaves * BR * kRow;
-  static constexpr int kBufs = 8 * kPart <= 10 * 1024 ? 2 : 1;
-  static constexpr int kPlanAt = kUpWaves * kUpRing + kBufs * kPart * 4;
+  static constexpr int kRow = 16 * NCB + 2, kPart = NW * BR * kRow;
+  static constexpr int kBufs = 8 * kPart <= (NW == 4 ? 10 : 20) * 1024 ? 2 : 1;
+  static constexpr int kPlanAt = NW * kUpRing + kBufs * kPart * 4;
 };
 
-template <int F, bool PACKED, int BR>
-__global__ __launch_bounds__(kUpWaves * 64) void decode_up_kernel(const DecodeArgs a) {
-  using C = UpCfg<F, BR>;
+template <int F, bool PACKED, int BR, int NW>
+__global__ __launch_bounds__(NW * 64) void decode_up_kernel(const DecodeArgs a) {
+  using C = UpCfg<F, BR, NW>;
   constexpr int NCB = C::NCB, kCols = C::kCols;
   using St = Stream<F, PACKED, NCB, BR, kUpRing>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t dyn[];
   uint8_t* ring = dyn;
-  float* part = (float*)(dyn + kUpWaves * kUpRing);
+  float* part = (float*)(dyn + NW * kUpRing);
   const Plan p(dyn + C::kPlanAt, a.T * a.k);
-  static_assert(kUpWaves * kUpRing >= kMaxExperts * (int)sizeof(int), "the plan's table lies in the rings");
-  plan<BR, kUpWaves * 64, true>(p, (int*)ring, a, blockIdx.x == 0 && a.status);
+  static_assert(NW * kUpRing >= kMaxExperts * (int)sizeof(int), "the plan's table lies in the rings");
+  plan<BR, NW * 64, true>(p, (int*)ring, a, blockIdx.x == 0 && a.status);
   const int wv = uniform(threadIdx.x >> 6);
   const DecodeSide side{(const uint8_t*)a.W13, (const uint8_t*)a.S13, 2 * a.I, a.H};
   St st(side, (const uint8_t*)a.x, ring + wv * kUpRing);
   const int ncol = a.I / kCols, units = *p.njobs * ncol;
-  const int nb = a.H / Fmt<F>::BK, kb0 = wv * nb / kUpWaves, kb1 = (wv + 1) * nb / kUpWaves;
+  const int nb = a.H / Fmt<F>::BK, kb0 = wv * nb / NW, kb1 = (wv + 1) * nb / NW;
 
   int pu = blockIdx.x;  // the producer's unit
   auto feed = [&]() {   // one block into the ring, if there is one
@@ -456,12 +460,12 @@ __global__ __launch_bounds__(kUpWaves * 64) void decode_up_kernel(const DecodeAr
       for (int i = 0; i < 4; ++i)
         if (4 * st.lg + i < BR) mine[(4 * st.lg + i) * C::kRow + 16 * cb + st.l16] = acc[cb][i];
     barrier_lds();  // with two buffers the only one: the other is written before this one's readers' next barrier
-    for (int q = threadIdx.x; q < BR * kCols; q += kUpWaves * 64) {
+    for (int q = threadIdx.x; q < BR * kCols; q += NW * 64) {
       const int row = q / kCols, c = q % kCols;
       if (row < m) {
         float g = 0.f, up = 0.f;
 #pragma unroll
-        for (int v = 0; v < kUpWaves; ++v) {
+        for (int v = 0; v < NW; ++v) {
           g += sums[(v * BR + row) * C::kRow + c];
           up += sums[(v * BR + row) * C::kRow + kCols + c];
         }
@@ -474,30 +478,24 @@ __global__ __launch_bounds__(kUpWaves * 64) void decode_up_kernel(const DecodeAr
 }
 
 // ------------------------------------------------------------------ down --
-constexpr int kDownRing = 13 * 1024;
+constexpr int kDownRing = 13 * 1024, kDownDeep = 19 * 1024;
 constexpr int kLdsMost = 160 * 1024;
 static_assert(4 * kDownRing + 74 * kRoutes + 4 <= kLdsMost, "any number of routes fits four waves' rings");
 
 // LDS: NW rings, then a line of 16 sums per share of K and route, then topk_weights and the plan.
-template <int F, bool PACKED, int BR, int NW>
+template <int F, bool PACKED, int BR, int NW, int RING>
 __global__ __launch_bounds__(NW * 64) void decode_down_kernel(const DecodeArgs a) {
-  using St = Stream<F, PACKED, 1, BR, kDownRing>;
+  using St = Stream<F, PACKED, 1, BR, RING>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t dyn[];
-  static_assert(NW * kDownRing >= kMaxExperts * (int)sizeof(int), "the plan's table lies in the rings");
-  float* y = (float*)(dyn + NW * kDownRing);
+  static_assert(NW * RING >= kMaxExperts * (int)sizeof(int), "the plan's table lies in the rings");
+  float* y = (float*)(dyn + NW * RING);
   const int R = a.T * a.k, KS = a.ksplit;
   float* share = y + 16 * KS * R;  // topk_weights, 0 for skipped slots, whose lines of sums are 0 too
-  for (int i = threadIdx.x; i < R; i += NW * 64) {
-    const bool on = (uint32_t)a.ids[i] < (uint32_t)a.E;
-    share[i] = on ? a.p[i] : 0.f;
-    if (!on)
-      for (int c = 0; c < 16 * KS; ++c) y[(c / 16 * R + i) * 16 + c % 16] = 0.f;
-  }
   const Plan p((uint8_t*)(share + R), R);
   plan<BR, NW * 64, false>(p, (int*)dyn, a, false);
   const int wv = uniform(threadIdx.x >> 6);
   const DecodeSide side{(const uint8_t*)a.W2, (const uint8_t*)a.S2, a.H, a.I};
-  St st(side, (const uint8_t*)a.h, dyn + wv * kDownRing);
+  St st(side, (const uint8_t*)a.h, dyn + wv * RING);
   const int n0 = blockIdx.x * 16, items = *p.njobs * KS, nb = a.I / Fmt<F>::BK;
 
   int pi = wv;
@@ -514,6 +512,12 @@ __global__ __launch_bounds__(NW * 64) void decode_down_kernel(const DecodeArgs a
   bool full = true;
 #pragma unroll 1
   for (int i = 0; i < St::S; ++i) full = feed();
+  for (int i = threadIdx.x; i < R; i += NW * 64) {
+    const bool on = (uint32_t)a.ids[i] < (uint32_t)a.E;
+    share[i] = on ? a.p[i] : 0.f;
+    if (!on)
+      for (int c = 0; c < 16 * KS; ++c) y[(c / 16 * R + i) * 16 + c % 16] = 0.f;
+  }
   for (int it = wv; it < items; it += NW) {
     const uint32_t job = (uint32_t)uniform((int)p.job[it / KS]);
     const int ks = it % KS, m = p.rows(job);
@@ -547,38 +551,41 @@ __global__ __launch_bounds__(NW * 64) void decode_down_kernel(const DecodeArgs a
   }
 }
 
-// A launch that asks for more than 64 KB of LDS.
-hipError_t allow_lds(const void* kernel) {
-  return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
+template <int F, bool PACKED, int BR, int NW, int RING>
+hipError_t launch_down(const DecodeArgs& a, hipStream_t s) {
+  const size_t lds = NW * RING + a.T * a.k * (64 * a.ksplit + 4) + Plan::bytes(a.T * a.k);
+  decode_down_kernel<F, PACKED, BR, NW, RING><<<a.H / 16, NW * 64, lds, s>>>(a);
+  return hipGetLastError();
 }
 
 template <int F, bool PACKED, int BR, int NW>
-hipError_t launch_down(const DecodeArgs& a, hipStream_t s) {
-  const size_t lds = NW * kDownRing + a.T * a.k * (64 * a.ksplit + 4) + Plan::bytes(a.T * a.k);
-  const hipError_t e = allow_lds((const void*)decode_down_kernel<F, PACKED, BR, NW>);
-  if (e != hipSuccess) return e;
-  decode_down_kernel<F, PACKED, BR, NW><<<a.H / 16, NW * 64, lds, s>>>(a);
+hipError_t launch_up(const DecodeArgs& a, int64_t units, int64_t most, hipStream_t s) {
+  decode_up_kernel<F, PACKED, BR, NW><<<(unsigned)(units < most ? units : most), NW * 64,
+                                        UpCfg<F, BR, NW>::kPlanAt + Plan::bytes(a.T * a.k), s>>>(a);
   return hipGetLastError();
 }
 
 template <int F, bool PACKED, int BR>
 hipError_t launch_rows(DecodeArgs a, hipStream_t s) {
-  const int R = a.T * a.k, nb = a.I / Fmt<F>::BK;
-  const int64_t units = (int64_t)R * (a.I / (F == kInt4 ? 32 : 16));
-  const int64_t cap = 2 * device_info().cus;
+  const int R = a.T * a.k, nb = a.I / Fmt<F>::BK, cus = device_info().cus;
   a.per_k = (65536 + a.k - 1) / a.k;
-  hipError_t e = allow_lds((const void*)decode_up_kernel<F, PACKED, BR>);
+  // Up: two workgroups of 4 waves on a compute unit; where there is no more than one unit of work for each, 8 waves share it.
+  const int64_t units = (int64_t)R * (a.I / UpCfg<F, BR, 4>::kCols);
+  hipError_t e;
+  if constexpr (BR < 16) e = units <= cus ? launch_up<F, PACKED, BR, 8>(a, units, cus, s) : launch_up<F, PACKED, BR, 4>(a, units, 2 * cus, s);
+  else e = launch_up<F, PACKED, BR, 4>(a, units, 2 * cus, s);
   if (e != hipSuccess) return e;
-  decode_up_kernel<F, PACKED, BR><<<(unsigned)(units < cap ? units : cap), kUpWaves * 64,
-                                    UpCfg<F, BR>::kPlanAt + Plan::bytes(R), s>>>(a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  // few routes: their K is shared so that every wave has a part
-  const bool wide = a.H / 16 <= 256 && 8 * kDownRing + 74 * R + 4 <= kLdsMost;
+  // Down: up to one workgroup per compute unit has 8 waves, else 4; few routes leave room for deeper rings, and their K is shared
+  // so that every wave has a part.
+  const bool wide = a.H / 16 <= cus && 8 * kDownRing + 74 * R + 4 <= kLdsMost;
   const int nw = wide ? 8 : 4;
   a.ksplit = 1;
   while (a.ksplit * R < nw && 2 * a.ksplit <= nb) a.ksplit *= 2;
-  return wide ? launch_down<F, PACKED, BR, 8>(a, s) : launch_down<F, PACKED, BR, 4>(a, s);
+  if constexpr (BR < 16) {
+    if (wide && 8 * kDownDeep + 74 * R + 4 + 64 * 8 <= kLdsMost) return launch_down<F, PACKED, BR, 8, kDownDeep>(a, s);
+    if (!wide && 2 * (4 * kDownDeep + 74 * R + 4 + 64 * 8) <= kLdsMost) return launch_down<F, PACKED, BR, 4, kDownDeep>(a, s);
+  }
+  return wide ? launch_down<F, PACKED, BR, 8, kDownRing>(a, s) : launch_down<F, PACKED, BR, 4, kDownRing>(a, s);
 }
 
 template <int F, bool PACKED>
