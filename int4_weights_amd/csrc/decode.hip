@@ -478,7 +478,7 @@ __global__ __launch_bounds__(NW * 64) void decode_up_kernel(const DecodeArgs a) 
 }
 
 // ------------------------------------------------------------------ down --
-constexpr int kDownRing = 13 * 1024, kDownDeep = 19 * 1024;
+constexpr int kDownRing = 13 * 1024, kDownDeep = 19 * 1024, kDownShort = 9 * 1024;
 constexpr int kLdsMost = 160 * 1024;
 static_assert(4 * kDownRing + 74 * kRoutes + 4 <= kLdsMost, "any number of routes fits four waves' rings");
 
@@ -581,6 +581,11 @@ hipError_t launch_rows(DecodeArgs a, hipStream_t s) {
   const int nw = wide ? 8 : 4;
   a.ksplit = 1;
   while (a.ksplit * R < nw && 2 * a.ksplit <= nb) a.ksplit *= 2;
+  if constexpr (F == kInt4 && BR == 4)
+    if (a.H / 16 <= cus && 16 * kDownShort + 74 * R + 4 + 64 * 16 <= kLdsMost) {
+      while (a.ksplit * R < 16 && 2 * a.ksplit <= nb) a.ksplit *= 2;
+      return launch_down<F, PACKED, BR, 16, kDownShort>(a, s);
+    }
   if constexpr (BR < 16) {
     if (wide && 8 * kDownDeep + 74 * R + 4 + 64 * 8 <= kLdsMost) return launch_down<F, PACKED, BR, 8, kDownDeep>(a, s);
     if (!wide && 2 * (4 * kDownDeep + 74 * R + 4 + 64 * 8) <= kLdsMost) return launch_down<F, PACKED, BR, 4, kDownDeep>(a, s);
