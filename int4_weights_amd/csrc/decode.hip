@@ -64,10 +64,12 @@ __device__ __forceinline__ v8bf widen_fp8(int lo, int hi) {
   const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-// 128 + q of a dword's 8 nibbles, in the order of nibbles 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ v8bf widen_int4(uint32_t w) {
-  const v4i v = {(int)((w & 0x000f000fu) | 0x43004300u), (int)(((w >> 4) & 0x000f000fu) | 0x43004300u),
-                 (int)(((w >> 8) & 0x000f000fu) | 0x43004300u), (int)(((w >> 12) & 0x000f000fu) | 0x43004300u)};
+// 128 + q of a dword's 8 nibbles, in the order of nibbles 0 4 1 5 2 6 3 7.  magic: 0x43004300 in a vector register, so that mask
+// and exponent take one instruction.
+__device__ __forceinline__ v8bf widen_int4(uint32_t w, uint32_t magic) {
+  constexpr uint32_t m = 0x000f000fu;
+  const v4i v = {(int)((w & m) | magic), (int)(((w >> 4) & m) | magic), (int)(((w >> 8) & m) | magic),
+                 (int)(((w >> 12) & m) | magic)};
   return __builtin_bit_cast(v8bf, v);
 }
 // 8 values in that order.
@@ -364,23 +366,27 @@ struct Stream {
     } else {
       const v8bf m136 = {(__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f,
                          (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f};
+      uint32_t magic = 0x43004300u;
+      asm("" : "+v"(magic));
+      v4i x[4];
       v4f s[NCB], fix = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int cb = 0; cb < NCB; ++cb) s[cb] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
       for (int d = 0; d < 4; ++d) {
-        const v4i x = PACKED ? f.x[d] : nibble_order(f.x[d]);
-        fix = mma(x, m136, fix);
-#pragma unroll
-        for (int cb = 0; cb < NCB; ++cb) s[cb] = mma(x, widen_int4((uint32_t)f.w[cb][0][d]), s[cb]);
+        x[d] = PACKED ? f.x[d] : nibble_order(f.x[d]);
+        fix = mma(x[d], m136, fix);
       }
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) s[cb] = mma(x[d], widen_int4((uint32_t)f.w[cb][0][d], magic), d == 0 ? fix : s[cb]);
 #pragma unroll
       for (int cb = 0; cb < NCB; ++cb) {
         const int n = (NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2)) + l16;
-        const int half = PACKED ? ((n & 63) / 16) & 1 : (n * (side.K / 128) + kb) & 1;
+        // (packed: the column block's parity; NCB / 2 blocks from a multiple of 32 on)
+        const int half = PACKED ? (NCB == 1 ? col0 / 16 : cb) & 1 : (n * (side.K / 128) + kb) & 1;
         const float q = (float)__builtin_bit_cast(_Float16, (uint16_t)(half ? f.s[cb] >> 16 : f.s[cb]));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(q, s[cb][i] + fix[i], acc[cb][i]);
+        for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(q, s[cb][i], acc[cb][i]);
       }
     }
   }
@@ -407,7 +413,7 @@ struct UpCfg {
 };
 
 template <int F, bool PACKED, int BR, int NW>
-__global__ __launch_bounds__(NW * 64) void decode_up_kernel(const DecodeArgs a) {
+__global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_up_kernel(const DecodeArgs a) {
   using C = UpCfg<F, BR, NW>;
   constexpr int NCB = C::NCB, kCols = C::kCols;
   using St = Stream<F, PACKED, NCB, BR, kUpRing>;
@@ -484,7 +490,7 @@ static_assert(4 * kDownRing + 74 * kRoutes + 4 <= kLdsMost, "any number of route
 
 // LDS: NW rings, then a line of 16 sums per share of K and route, then topk_weights and the plan.
 template <int F, bool PACKED, int BR, int NW, int RING>
-__global__ __launch_bounds__(NW * 64) void decode_down_kernel(const DecodeArgs a) {
+__global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_down_kernel(const DecodeArgs a) {
   using St = Stream<F, PACKED, 1, BR, RING>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t dyn[];
   static_assert(NW * RING >= kMaxExperts * (int)sizeof(int), "the plan's table lies in the rings");

@@ -658,7 +658,7 @@ struct LinStreamCfg {
 };
 
 template <bool GATED, int RB, int CB, int KS, int S>
-__global__ __launch_bounds__(KS * 64) void gemm_linear_stream_kernel(const LinearArgs a) {
+__global__ __launch_bounds__(512) void gemm_linear_stream_kernel(const LinearArgs a) {
   using C = LinStreamCfg<RB, CB, KS, S>;
   constexpr int kRows = 16 * RB, kCols = 16 * CB, kOuts = GATED ? kCols / 2 : kCols;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[C::kLds];
