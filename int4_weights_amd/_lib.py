@@ -186,6 +186,33 @@ def _rows(fn, dev, t, name, dtypes, shape) -> int:
     return row_stride if rows > 1 else max(cols, 1)
 
 
+def _mat(fn, dev, t, name, dtypes):
+    """(pointer, rows, columns, row stride in elements) of a 2-D tensor on GPU dev of one of these types whose rows are
+    contiguous.  (One test of each property: these calls are short enough on the GPU for the host's checks to show.)"""
+    shape, dtype = t.shape, t.dtype
+    if len(shape) != 2 or dtype not in dtypes or t.get_device() != dev or dev < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if len(shape) != 2:
+            raise ValueError(f"{name} must have 2 dims, got {len(shape)}")
+        if dtype not in dtypes:
+            raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
+        raise ValueError(f"{fn}: {name} is on {t.device}, the call on cuda:{dev}")
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), rows, cols, ld if rows > 1 else max(cols, 1)
+
+
+def _mat_of(fn, dev, t, name, dtypes, rows, cols):
+    """(pointer, row stride) of such a tensor, which has to be [rows, cols]."""
+    p, r, c, ld = _mat(fn, dev, t, name, dtypes)
+    if r != rows or c != cols:
+        raise ValueError(f"{fn}: {name} is {(r, c)}, needs {(rows, cols)}")
+    return p, ld
+
+
 def _shape2(t, name):
     """(rows, columns, GPU) of a 2-D GPU tensor."""
     dev = t.get_device()
@@ -703,22 +730,32 @@ def moe_gemm_bf16(A, W, D, bias=None, act: str = "none", gated: bool = False, C=
     trans_w=True); weight gradient: moe_gemm_bf16(dP, X, dW, C=dW, trans_a=True, trans_w=True).  workspace:
     moe_gemm_bf16_workspace_bytes(M, N, K) bytes."""
     fn = "moe_gemm_bf16"
-    a0, a1, dev = _shape2(A, "A")
-    w0, w1 = W.shape
-    (M, K), N = ((a1, a0) if trans_a else (a0, a1)), (w1 if trans_w else w0)
-    lda = _rows(fn, dev, A, "A", _BF16S, (a0, a1))
-    ldw = _rows(fn, dev, W, "W", _BF16S, (K, N) if trans_w else (N, K))
-    out = (M, N // 2 if gated else N)
-    ldd = _rows(fn, dev, D, "D", _FLOATS, out)
-    b, btype = (None, 0)
+    dev = A.get_device()
+    ap, a0, a1, lda = _mat(fn, dev, A, "A", _BF16S)
+    wp, w0, w1, ldw = _mat(fn, dev, W, "W", _BF16S)
+    M, K, N, wk = a0, a1, w0, w1
+    if trans_a:
+        M, K = a1, a0
+    if trans_w:
+        N, wk = w1, w0
+    if wk != K:
+        raise ValueError(f"{fn}: A has {K} and W {wk} values to multiply")
+    cols = N // 2 if gated else N
+    dp, ldd = _mat_of(fn, dev, D, "D", _FLOATS, M, cols)
+    b = c = p = None
+    btype = ctype = ldc = ldp = 0
     if bias is not None:
-        b, btype = _whole(fn, dev, bias, "bias", bias.dtype, (N,)), _float_type("bias", bias)
-    c, ctype, ldc = (None, 0, 0) if C is None else (C.data_ptr(), _float_type("C", C), _rows(fn, dev, C, "C", _FLOATS, out))
-    p, ldp = (None, 0) if pre is None else (pre.data_ptr(), _rows(fn, dev, pre, "pre", _BF16S, (M, N)))
+        btype = _float_type("bias", bias)
+        b = _whole(fn, dev, bias, "bias", bias.dtype, (N,))
+    if C is not None:
+        c, ldc = _mat_of(fn, dev, C, "C", _FLOATS, M, cols)
+        ctype = _float_type("C", C)
+    if pre is not None:
+        p, ldp = _mat_of(fn, dev, pre, "pre", _BF16S, M, N)
     ws, ws_bytes = _scratch(fn, dev, workspace)
-    _check(load().moe_gemm_bf16(A.data_ptr(), lda, W.data_ptr(), ldw, (_TRANS_A if trans_a else 0) | (_TRANS_W if trans_w else 0),
-                                D.data_ptr(), _float_type("D", D), ldd, b, btype, _act(fn, act, gated), c, ctype, ldc, p,
-                                ldp, M, N, K, ws, ws_bytes, _queue(fn, dev, stream)), fn)
+    _check(load().moe_gemm_bf16(ap, lda, wp, ldw, (_TRANS_A if trans_a else 0) | (_TRANS_W if trans_w else 0), dp,
+                                _float_type("D", D), ldd, b, btype, _act(fn, act, gated), c, ctype, ldc, p, ldp, M, N, K,
+                                ws, ws_bytes, _queue(fn, dev, stream)), fn)
 
 
 def _float_type(name, t) -> int:
@@ -737,15 +774,15 @@ def moe_act_bwd(dD, pre, dP, dbias=None, act: str = "none", gated: bool = False,
     [M, N] and dbias float32 [N] (added to, if accumulate); either may be None.  pre may be None for act "none" without
     gated.  Rows may be strided.  workspace: moe_act_bwd_workspace_bytes(M, N) bytes (with dbias)."""
     fn = "moe_act_bwd"
-    M, half, dev = _shape2(dD, "dD")
+    dev = dD.get_device()
+    d, M, half, ldd = _mat(fn, dev, dD, "dD", _BF16S)
     N = 2 * half if gated else half
     code = _act(fn, act, gated)
-    ldd = _rows(fn, dev, dD, "dD", _BF16S, (M, half))
-    p, ldp = (None, 0) if pre is None else (pre.data_ptr(), _rows(fn, dev, pre, "pre", _BF16S, (M, N)))
-    o, ldo = (None, 0) if dP is None else (dP.data_ptr(), _rows(fn, dev, dP, "dP", _BF16S, (M, N)))
+    p, ldp = (None, 0) if pre is None else _mat_of(fn, dev, pre, "pre", _BF16S, M, N)
+    o, ldo = (None, 0) if dP is None else _mat_of(fn, dev, dP, "dP", _BF16S, M, N)
     b = None if dbias is None else _whole(fn, dev, dbias, "dbias", torch.float32, (N,))
     ws, ws_bytes = _scratch(fn, dev, workspace)
-    _check(load().moe_act_bwd(dD.data_ptr(), ldd, p, ldp, code, o, ldo, b, int(accumulate), M, N, ws, ws_bytes,
+    _check(load().moe_act_bwd(d, ldd, p, ldp, code, o, ldo, b, int(accumulate), M, N, ws, ws_bytes,
                               _queue(fn, dev, stream)), fn)
 
 
