@@ -288,3 +288,78 @@ class DenseFP8Linear:
             L.moe_quant_act_t(t, q, sf)
             qs += [q, sf]
         return self._gemm(*qs, dw, C=dw if accumulate else None)
+
+
+class MoeDecodeLayer:
+    """The expert layer of a decode step: up-projection, SwiGLU, down-projection and weighted sum in two kernels.
+
+    w13 [E, 2I, H] (gate rows, then up rows) and w2 [E, H, I] in weights "bf16", "fp8" (s13, s2 float32 per 128x128) or
+    "int4" (float16 per 128), packed: in moe_pack_weight_*'s order; the same tensors that the grouped layers above hold.
+    Buffers for up to max_tokens tokens (at most DECODE_MAX_TOKENS, and DECODE_MAX_ROUTES routes): a forward allocates
+    nothing, and calls of one object that overlap in time must not run on two streams."""
+
+    def __init__(self, w13: torch.Tensor, w2: torch.Tensor, topk: int, max_tokens: int, weights: str = "fp8",
+                 s13: torch.Tensor | None = None, s2: torch.Tensor | None = None, packed: bool = False):
+        self.w13, self.w2, self.s13, self.s2 = w13, w2, s13, s2
+        self.weights, self.packed, self.topk, self.max_tokens = weights, packed, topk, max_tokens
+        self.E, self.H, self.I = w13.shape[0], w2.shape[1], w13.shape[1] // 2
+        need = L.moe_experts_decode_workspace_bytes(max_tokens, topk, self.I)
+        if need < 0:
+            raise ValueError(f"a decode step has at most {L.DECODE_MAX_TOKENS} tokens and {L.DECODE_MAX_ROUTES} routes, not "
+                             f"{max_tokens} of {topk}")
+        dev = w13.device
+        self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.Z = torch.empty(max_tokens, self.H, dtype=torch.bfloat16, device=dev)
+
+    def forward(self, x, topk_ids, topk_weights, z=None, residual=None):
+        """x bf16 [T, H], topk_ids int32 and topk_weights float32 [T, topk] -> z bf16 [T, H] (default: this layer's buffer),
+        with residual bf16 [T, H] added (it may be z)."""
+        if x.shape[0] > self.max_tokens:
+            raise ValueError(f"x has {x.shape[0]} tokens, the layer room for {self.max_tokens}")
+        z = self.Z[:x.shape[0]] if z is None else z
+        L.moe_experts_decode(x, topk_ids, topk_weights, self.w13, self.w2, z, weights=self.weights, s13=self.s13, s2=self.s2,
+                             packed=self.packed, residual=residual, dev_status=self.dev_status, workspace=self.workspace)
+        return z
+
+
+class DenseLinear:
+    """y = act(x W^T + bias) + residual in bf16, for a weight that every token uses (a gate projection, a shared expert, a
+    projection), with its gradients.
+
+    w bf16 [N, K], bias float32 or bf16 [N]; gated: w's rows are gates, then what they gate, and y has N/2 columns.  The
+    gradient starts from the pre-activation that forward(..., pre=) keeps: grad_pre gives dP (and the bias's gradient),
+    grad_input and grad_weight take it from there (without activation and bias dP is dy).  Nothing is kept between calls;
+    a product that splits K and grad_pre take their scratch from torch's allocator, which a graph's capture keeps."""
+
+    def __init__(self, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none", gated: bool = False):
+        self.w, self.bias, self.act, self.gated = w, bias, act, gated
+        self.N, self.K = w.shape
+
+    def _product(self, M, N, K, A, W, out, **kw):
+        need = L.moe_gemm_bf16_workspace_bytes(M, N, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=A.device) if need > 0 else None
+        L.moe_gemm_bf16(A, W, out, workspace=ws, **kw)
+        return out
+
+    def forward(self, x, out, residual=None, pre=None):
+        """x bf16 [T, K] -> out bf16 or float32 [T, N] (gated [T, N/2]); residual of out's shape, bf16 or float32 (may be
+        out); pre bf16 [T, N] receives x W^T + bias."""
+        return self._product(x.shape[0], self.N, self.K, x, self.w, out, bias=self.bias, act=self.act, gated=self.gated,
+                             C=residual, pre=pre)
+
+    def grad_pre(self, dy, pre, dp, dbias=None, accumulate=True):
+        """dy bf16 and pre -> dp bf16 [T, N]; dbias float32 [N] (+)= its column sums."""
+        T, N = dy.shape[0], self.N
+        need = L.moe_act_bwd_workspace_bytes(T, N) if dbias is not None else 0
+        ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need > 0 else None
+        L.moe_act_bwd(dy, pre, dp, dbias=dbias, act=self.act, gated=self.gated, accumulate=accumulate, workspace=ws)
+        return dp
+
+    def grad_input(self, dp, dx, residual=None):
+        """dp bf16 [T, N] -> dx bf16 or float32 [T, K] (+ residual: the gradient of another branch; may be dx)."""
+        return self._product(dp.shape[0], self.K, self.N, dp, self.w, dx, C=residual, trans_w=True)
+
+    def grad_weight(self, dp, x, dw, accumulate=True):
+        """dw float32 [N, K] (+)= dp^T x of dp bf16 [T, N] and x bf16 [T, K]."""
+        return self._product(self.N, self.K, x.shape[0], dp, x, dw, C=dw if accumulate else None, trans_a=True, trans_w=True)
