@@ -581,9 +581,9 @@ hipError_t launch_rows(DecodeArgs a, hipStream_t s) {
   if constexpr (BR < 16) e = units <= cus ? launch_up<F, PACKED, BR, 8>(a, units, cus, s) : launch_up<F, PACKED, BR, 4>(a, units, 2 * cus, s);
   else e = launch_up<F, PACKED, BR, 4>(a, units, 2 * cus, s);
   if (e != hipSuccess) return e;
-  // Down: up to one workgroup per compute unit has 8 waves, else 4; few routes leave room for deeper rings, and their K is shared
-  // so that every wave has a part.
-  const bool wide = a.H / 16 <= cus && 8 * kDownRing + 74 * R + 4 <= kLdsMost;
+  // Down: workgroups that have a compute unit to themselves, because there are few or because of the routes' lines, have 8 waves,
+  // else 4; few routes leave room for deeper rings, and their K is shared so that every wave has a part.
+  const bool wide = 8 * kDownRing + 74 * R + 4 <= kLdsMost && (a.H / 16 <= cus || 2 * (4 * kDownRing + 74 * R + 4) > kLdsMost);
   const int nw = wide ? 8 : 4;
   a.ksplit = 1;
   while (a.ksplit * R < nw && 2 * a.ksplit <= nb) a.ksplit *= 2;
