@@ -48,6 +48,7 @@ struct DecodeSide {      // one projection
 __device__ __forceinline__ void copy16(uint32_t voff, const void* base, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(base), "{m0}"(lds) : "memory");
 }
+// Weights, past the caches' replacement: each is read once (61 tokens in bf16: 808 us without, 731 with).
 __device__ __forceinline__ void copy16_once(uint32_t voff, const void* base, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" : : "v"(voff), "s"(base), "{m0}"(lds) : "memory");
 }
@@ -429,7 +430,10 @@ __global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_up_kernel(const
   const int ncol = a.I / kCols, units = *p.njobs * ncol;
   const int nb = a.H / Fmt<F>::BK, kb0 = wv * nb / NW, kb1 = (wv + 1) * nb / NW;
 
-  int pu = blockIdx.x;  // the producer's unit
+  // Workgroup b runs on XCD b % 8: consecutive units, which share their rows, go to one XCD.
+  const int xs = gridDim.x / 8, xr = gridDim.x % 8, xcd = blockIdx.x % 8;
+  const int first = xcd * xs + min(xcd, xr) + blockIdx.x / 8;
+  int pu = first;       // the producer's unit
   auto feed = [&]() {   // one block into the ring, if there is one
     if (st.pkb == st.pend) {
       if (pu >= units || kb0 == kb1) return false;
@@ -444,7 +448,7 @@ __global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_up_kernel(const
 #pragma unroll 1
   for (int i = 0; i < St::S; ++i) full = feed();
   int buf = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int u = first; u < units; u += gridDim.x) {
     const uint32_t job = (uint32_t)uniform((int)p.job[u / ncol]);
     const int col = u % ncol * kCols, m = p.rows(job);
     v4f acc[NCB];

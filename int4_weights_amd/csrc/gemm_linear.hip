@@ -37,6 +37,13 @@ __device__ __forceinline__ void copy16(uint32_t voff, const void* base, uint32_t
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r), "{m0}"(lds) : "memory");
 }
 
+// The same for what one workgroup alone reads.
+__device__ __forceinline__ void copy16_once(uint32_t voff, const void* base, uint32_t lds) {
+  const uint64_t b = (uint64_t)base;
+  const v4i r = {(int)(uint32_t)b, (int)(uint32_t)(b >> 32) & 0xffff, 0x7fffffff, 0x00020000};
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" : : "v"(voff), "s"(r), "{m0}"(lds) : "memory");
+}
+
 __device__ __forceinline__ v4f mma(const v8bf w, const v8bf x, const v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
 }
@@ -648,7 +655,7 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
 // ----------------------------------------------------------------- stream --
 // Few rows (a decode step): every weight byte is used by one wave, so waves need nothing from one another.  A workgroup takes
 // 16 CB columns (gated: blocks of 8 gates and their 8 ups) and all 16 RB rows; its KS waves split K, each with a ring of S blocks
-// of its own in LDS (no barrier in the loop), and meet once at the end, where the partial sums are added in wave order.
+// of its own in LDS (no barrier in the loop; all S in flight while a block is multiplied), and meet once at the end, where the partial sums are added in wave order.
 template <int RB, int CB, int KS, int S>
 struct LinStreamCfg {
   static constexpr int kBlock = (RB + CB) * 2048, kCopies = 2 * (RB + CB), kWave = S * kBlock;
@@ -688,6 +695,9 @@ __global__ __launch_bounds__(512) void gemm_linear_stream_kernel(const LinearArg
       voff[q] = in ? Operand<false, 64>::offset(k, n, a.ldw) : kOut;
     }
   }
+  // Few rows and weights that the caches would not keep until the next step: past their replacement (1 x 4096 x 7168 13.1 -> 12.1
+  // us from HBM; but 16 x 256 x 7168, which they keep, 7.5 -> 11.0, and 32 x 4096 x 7168 from the Infinity Cache 11.7 -> 15.4).
+  const bool once = a.M <= 8 && (int64_t)a.N * a.K >= 8 << 20;
   int slot = 0;
   auto issue = [&](int b) {
     const bool rest = 64 * (kb0 + b) + 64 > a.K;
@@ -695,7 +705,10 @@ __global__ __launch_bounds__(512) void gemm_linear_stream_kernel(const LinearArg
     for (int q = 0; q < C::kCopies; ++q) {
       uint32_t v = voff[q];
       if (rest && 64 * (kb0 + b) + (q & 1 ? ck ^ 32 : ck) >= a.K) v = kOut;
-      copy16(v, 8 * q < kRows ? abase : wbase, (uint32_t)uniform((int)(lds0 + slot * C::kBlock + 1024 * q)));
+      const uint32_t to = (uint32_t)uniform((int)(lds0 + slot * C::kBlock + 1024 * q));
+      if (8 * q < kRows) copy16(v, abase, to);
+      else if (once) copy16_once(v, wbase, to);
+      else copy16(v, wbase, to);
     }
     abase += 128;
     wbase += 128;
@@ -709,36 +722,34 @@ __global__ __launch_bounds__(512) void gemm_linear_stream_kernel(const LinearArg
 #pragma unroll
     for (int j = 0; j < CB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int b = 0; b < S - 1; ++b)
+  for (int b = 0; b < S; ++b)
     if (b < nb) issue(b);
   int cs = 0;
   for (int b = 0; b < nb; ++b) {
-    if (b + S - 1 < nb) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot's last reads are in registers
-      issue(b + S - 1);
-      wait_vmcnt<(S - 1) * C::kCopies>();
-    } else {
-      wait_vmcnt<0>();
-    }
+    if (b + S <= nb) wait_vmcnt<(S - 1) * C::kCopies>();
+    else wait_vmcnt<0>();
     asm volatile("" ::: "memory");
     const uint8_t* blk = ring + cs * C::kBlock;
     cs = cs + 1 == S ? 0 : cs + 1;
+    v8bf x[2][RB], w[2][CB];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      v8bf x[RB];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) x[i] = op.frag(blk, i, h);
+      for (int i = 0; i < RB; ++i) x[h][i] = op.frag(blk, i, h);
 #pragma unroll
-      for (int j = 0; j < CB; ++j) {
-        const v8bf w = op.frag(blk, RB + j, h);
-#pragma unroll
-        for (int i = 0; i < RB; ++i) acc[i][j] = mma(w, x[i], acc[i][j]);
-      }
+      for (int j = 0; j < CB; ++j) w[h][j] = op.frag(blk, RB + j, h);
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the fragments are in registers: the slot is filled anew
+    if (b + S < nb) issue(b + S);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int i = 0; i < RB; ++i) acc[i][j] = mma(w[h][j], x[h][i], acc[i][j]);
   }
   // over the wave's own ring, whose copies have all landed and been read; lane: columns 4 lg .. + 3 of row l16
   float* part = (float*)ring;
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -771,9 +782,9 @@ hipError_t launch_order(LinearArgs a, hipStream_t s) {
   a.splits = p.splits;
   if constexpr (!TA && !TW) {
     const bool many = a.N > 16 * kLinCus;
-    if (p.kind == kLinStream16) return many ? launch_stream<GATED, 1, 2, 4, 5>(a, s) : launch_stream<GATED, 1, 1, 8, 4>(a, s);
-    if (p.kind == kLinStream32) return many ? launch_stream<GATED, 2, 2, 4, 4>(a, s) : launch_stream<GATED, 2, 1, 8, 3>(a, s);
-    if (p.kind == kLinStream64) return many ? launch_stream<GATED, 4, 2, 4, 3>(a, s) : launch_stream<GATED, 4, 1, 4, 3>(a, s);
+    if (p.kind == kLinStream16) return many ? launch_stream<GATED, 1, 2, 4, 6>(a, s) : launch_stream<GATED, 1, 1, 8, 5>(a, s);
+    if (p.kind == kLinStream32) return many ? launch_stream<GATED, 2, 2, 4, 5>(a, s) : launch_stream<GATED, 2, 1, 8, 3>(a, s);
+    if (p.kind == kLinStream64) return many ? launch_stream<GATED, 4, 2, 4, 3>(a, s) : launch_stream<GATED, 4, 1, 4, 4>(a, s);
   }
   switch (p.kind) {
     case kLin64x64: return launch_tile<TA, TW, GATED, 2, 2, 2, 2>(a, s);
