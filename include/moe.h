@@ -742,8 +742,8 @@ moe_status moe_gemm_bf16(const uint16_t* A, int64_t lda, const uint16_t* W, int6
  *   dP or dbias may be NULL, but not both; pre is not read (may be NULL) for
  *   MOE_ACT_NONE without MOE_ACT_GATED.  dP may be dD (not gated, same stride)
  *   or pre (same stride).  ReLU's slope at 0 is 0.
- *   Requires N % 8 == 0 (gated: N % 16 == 0), strides multiples of 8, dD, pre and
- *   dP 16-byte, dbias 4-byte aligned; M, N <= 2^26.  M == 0 writes dbias = 0 (unless
+ *   Any N (gated: even) and strides (16-byte aligned rows are fastest), each array
+ *   aligned to its type; M, N <= 2^26.  M == 0 writes dbias = 0 (unless
  *   accumulate).  workspace: moe_act_bwd_workspace_bytes(M, N) bytes, 16-byte
  *   aligned (NULL when that is 0, or when dbias is); calls that overlap in time
  *   must not share it. */

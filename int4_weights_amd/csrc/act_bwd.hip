@@ -38,6 +38,26 @@ __device__ __forceinline__ v4i pack8(const Eight& e) {
   return w;
 }
 
+// Columns at .. at + 7 of a row, of which cnt are there (rows begin at any element: global memory takes vectors at any address).
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ v4i load8(const uint16_t* p, int cnt) {
+  if (cnt == 8) return *(const v4i_any*)p;
+  v4i w = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < cnt) w[i >> 1] |= (int)((uint32_t)p[i] << 16 * (i & 1));
+  return w;
+}
+__device__ __forceinline__ void store8(uint16_t* p, int cnt, const v4i w) {
+  if (cnt == 8) {
+    *(v4i_any*)p = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < cnt) p[i] = (uint16_t)((uint32_t)w[i >> 1] >> 16 * (i & 1));
+}
+
 // LPR lanes per row: a workgroup of TPB threads owns 8 LPR columns (of each half, if gated) and the rows of chunk blockIdx.y.
 template <int ACT, bool GATED, int LPR, int TPB>
 __global__ __launch_bounds__(TPB) void act_bwd_kernel(const ActBwdArgs a) {
@@ -51,15 +71,16 @@ __global__ __launch_bounds__(TPB) void act_bwd_kernel(const ActBwdArgs a) {
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int h = 0; h < H; ++h) s[h][i] = 0.f;
-  if (n < half) {
+  const int cnt = min(8, half - n);
+  if (cnt > 0) {
     for (int m0 = r0 + threadIdx.x / LPR; m0 < r1; m0 += kRowsAhead * kRows) {
       v4i d[kRowsAhead], g[kRowsAhead], u[kRowsAhead];
 #pragma unroll
       for (int j = 0; j < kRowsAhead; ++j) {
         const int64_t m = min(m0 + j * kRows, r1 - 1);
-        d[j] = *(const v4i*)(a.dD + m * a.ldd + n);
-        if (GATED || ACT != kActNone) g[j] = *(const v4i*)(a.pre + m * a.ldp + n);
-        if (GATED) u[j] = *(const v4i*)(a.pre + m * a.ldp + half + n);
+        d[j] = load8(a.dD + m * a.ldd + n, cnt);
+        if (GATED || ACT != kActNone) g[j] = load8(a.pre + m * a.ldp + n, cnt);
+        if (GATED) u[j] = load8(a.pre + m * a.ldp + half + n, cnt);
       }
 #pragma unroll
       for (int j = 0; j < kRowsAhead; ++j) {
@@ -81,8 +102,8 @@ __global__ __launch_bounds__(TPB) void act_bwd_kernel(const ActBwdArgs a) {
           }
         }
         if (a.dP) {
-          *(v4i*)(a.dP + m * a.ldo + n) = pack8(o);
-          if (GATED) *(v4i*)(a.dP + m * a.ldo + half + n) = pack8(p);
+          store8(a.dP + m * a.ldo + n, cnt, pack8(o));
+          if (GATED) store8(a.dP + m * a.ldo + half + n, cnt, pack8(p));
         }
       }
     }

@@ -979,14 +979,13 @@ moe_status moe_act_bwd(const uint16_t* dD, int64_t ldd, const uint16_t* pre, int
   if (M > (1 << 26) || N > (1 << 26)) return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d x N=%d is too large", fn, M, N);
   if (!act_ok(act)) return fail(MOE_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, act);
   const bool gated = act & MOE_ACT_GATED, reads = act != MOE_ACT_NONE;
-  if (N % (gated ? 16 : 8)) return fail(MOE_ERR_UNSUPPORTED, "%s: N=%d is not a multiple of %d", fn, N, gated ? 16 : 8);
+  if (gated && N % 2) return fail(MOE_ERR_UNSUPPORTED, "%s: a gated activation needs an even N (%d)", fn, N);
   if (!dP && !dbias) return fail(MOE_ERR_NULL, "%s: neither dP nor dbias", fn);
   if (M > 0 && (!dD || (reads && !pre))) return fail(MOE_ERR_NULL, "%s: null pointer", fn);
   if (ldd < (gated ? N / 2 : N) || (reads && ldp < N) || (dP && ldo < N))
     return fail(MOE_ERR_SHAPE, "%s: a row stride is shorter than its row", fn);
-  if (!aligned(dD, 16) || !aligned(dP, 16) || !aligned(dbias, 4) || ldd % 8 || (dP && ldo % 8) ||
-      (reads && (!aligned(pre, 16) || ldp % 8)))
-    return fail(MOE_ERR_ALIGN, "%s: dD, pre and dP (and their strides) must be 16-byte, dbias 4-byte aligned", fn);
+  if (!aligned(dD, 2) || !aligned(dP, 2) || !aligned(dbias, 4) || (reads && !aligned(pre, 2)))
+    return fail(MOE_ERR_ALIGN, "%s: dD, pre, dP and dbias must be aligned to their type", fn);
   if ((dP == dD && dP && (gated || ldo != ldd)) || (reads && dP == pre && dP && ldo != ldp))
     return fail(MOE_ERR_SHAPE, "%s: dP is an input of another shape or stride", fn);
   const int64_t need = dbias ? act_bwd_workspace_bytes(M, N) : 0;

@@ -50,10 +50,10 @@ def test_product_refusals(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(M=(1 << 26) + 1), UNSUPPORTED), (dict(N=1 << 27), UNSUPPORTED), (dict(act=9), UNSUPPORTED),
-    (dict(N=252), UNSUPPORTED), (dict(act=GATED, N=264), UNSUPPORTED), (dict(dP=None, db=None), NULL), (dict(dD=None), NULL),
+    (dict(act=GATED, N=255), UNSUPPORTED), (dict(dP=None, db=None), NULL), (dict(dD=None), NULL),
     (dict(pre=None), NULL), (dict(pre=None, act=GATED), NULL), (dict(ldd=248), SHAPE), (dict(ldp=248), SHAPE), (dict(ldo=248), SHAPE),
-    (dict(act=GATED | 2, ldd=120), SHAPE), (dict(dD=P + 8), ALIGN), (dict(pre=P + 2), ALIGN), (dict(dP=P + 4), ALIGN), (dict(db=P + 2), ALIGN),
-    (dict(ldd=260), ALIGN), (dict(ldp=258), ALIGN), (dict(ldo=257), ALIGN), (dict(dD=P, dP=P, ldo=264), SHAPE),
+    (dict(act=GATED | 2, ldd=120), SHAPE), (dict(dD=P + 1), ALIGN), (dict(pre=P + 1), ALIGN), (dict(dP=P + 1), ALIGN), (dict(db=P + 2), ALIGN),
+    (dict(dD=P, dP=P, ldo=264), SHAPE),
     (dict(dD=P, dP=P, act=GATED | 2), SHAPE), (dict(dP=P + 65536, pre=P + 65536, ldp=264), SHAPE), (dict(M=2000, ws=None), WORKSPACE),
     (dict(M=2000, wsb=16), WORKSPACE), (dict(M=2000, ws=P + 4), WORKSPACE), (dict(M=0, dD=None, pre=None, dP=P, db=None), OK),
     (dict(M=0, dD=None, pre=None, dP=None, db=P, acc=1), OK),

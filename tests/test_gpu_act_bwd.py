@@ -47,7 +47,7 @@ def check(dP, dbias, dD, pre, act, gated, before=0.0):
         assert (np.abs(f64(dbias) - before - ref.sum(0)) <= bound + 1e-37).all()
 
 
-@pytest.mark.parametrize("shape", [(1, 16), (3, 80), (17, 528), (333, 1536), (1000, 1040), (2050, 4096)])
+@pytest.mark.parametrize("shape", [(1, 2), (1, 16), (5, 34), (3, 80), (17, 528), (700, 2344), (333, 1536), (1000, 1042), (1500, 1170), (2050, 4096)])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("gated", [False, True])
 def test_against_the_oracle(shape, act, gated):
@@ -96,7 +96,7 @@ def test_strided_and_in_place(gated):
     dD, pre = inputs(M, N, gated, 4)
     want = run(dD, pre, "gelu", gated)
     h = dD.shape[1]
-    a, b, c = (torch.full((M, w + 8 * i), 5.0, dtype=torch.bfloat16, device=DEV) for i, w in ((1, h), (2, N), (3, N)))
+    a, b, c = (torch.full((M, w + 3 * i), 5.0, dtype=torch.bfloat16, device=DEV) for i, w in ((1, h), (2, N), (3, N)))
     a[:, :h], b[:, :N] = dD, pre
     moe.moe_act_bwd(a[:, :h], b[:, :N], c[:, :N], act="gelu", gated=gated)
     assert torch.equal(c[:, :N], want) and (c[:, N:] == 5).all()
