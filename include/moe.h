@@ -717,7 +717,7 @@ enum {
  *   Requires lda and ldw multiples of 8 and below 2^22, A and W 16-byte aligned,
  *   the others aligned to their type; the contiguous dimension of each operand a
  *   multiple of 8 (K; with MOE_TRANS_A M, with MOE_TRANS_W N), the others any;
- *   gated: N even, N/2 * ldw < 2^30 - 2^28; M and N <= 2^26 and ceil(M/64) * ceil(N/64) <
+ *   gated: N even, (N/2 + 256) * ldw < 2^30; M and N <= 2^26 and ceil(M/64) * ceil(N/64) <
  *   2^24.  M == 0 is a no-op; K == 0 is a product of zeros (A and W are
  *   not looked at).
  *   D and pre must not overlap the inputs (but D = C) or each other.

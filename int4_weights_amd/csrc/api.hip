@@ -925,7 +925,7 @@ moe_status moe_gemm_bf16(const uint16_t* A, int64_t lda, const uint16_t* W, int6
     return fail(MOE_ERR_SHAPE, "%s: a row stride is shorter than its row", fn);
   if (K > 0 && (lda >= (1 << 22) || ldw >= (1 << 22)))
     return fail(MOE_ERR_UNSUPPORTED, "%s: lda and ldw must be below 2^22", fn);
-  if (gated && K > 0 && (int64_t)NO * ldw >= (1 << 30) - (1 << 28))
+  if (gated && K > 0 && ((int64_t)NO + 256) * ldw >= 1 << 30)  // a tile's ups, as 32-bit byte offsets from its gates
     return fail(MOE_ERR_UNSUPPORTED, "%s: a gated product's weight is too large", fn);
   if (M == 0) return MOE_OK;
   if ((K > 0 && (!A || !W)) || !D) return fail(MOE_ERR_NULL, "%s: null pointer", fn);

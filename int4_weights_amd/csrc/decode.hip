@@ -17,6 +17,11 @@
 // (8) waves share; persistent workgroups walk over the units.  Down-projection: a workgroup owns 16 columns of Z and takes every
 // job, its waves in turn; the rows' sums meet in LDS as one line per route, so the sum over a token's slots runs in slot order
 // whatever wave was first, and no partial result goes through memory.
+//
+// Measured (us; TB/s of the active experts' weights): 1 token, 8 of 256 experts, 7168 x 2048, FP8 59.4 (5.9); 61 tokens, 8 of 128,
+// 4096 x 1536, bf16 686 to 720 (6.6 to 6.9), FP8 375 (6.3); 16 tokens, 4096 x 768, 4-bit packed 80 (5.0), row-major 120.  A
+// plain read of memory reaches 7.3 TB/s.  What bounds it: bytes in flight (the rings, 64 to 110 KB a compute unit), the start and
+// the last round of units, and for 4-bit codes the widening beside the stream.
 #include "linear_act.h"
 #include "moe_device.h"
 #include "moe_internal.h"

@@ -13,6 +13,10 @@
 // instruction's A operand (output columns), a its B operand (rows), so a lane holds 4 consecutive columns of one row, and the
 // epilogue sees each value in fp32 once.  Copies are buffer loads into the LDS, whose range check turns what lies outside the
 // matrices (rows, columns, the last K block's rest) into zeros.
+//
+// Measured (us): 4096 x 4096 x 7168 176 (1.36 PFLOP/s; the library's plain product 155 to 160), with GELU, bias and pre 189 to
+// 202; 8192^3 764 (1.44); 4096 x 7168 x 4096 in the gradients' orders 198 (library 200, 221); 1024 x 4096 x 7168 55 (60); 131 x
+// 7168 x 2048 13.4 (19); 1 x 4096 x 7168 12.1 from HBM (4.9 TB/s).
 #include "linear_act.h"
 #include "linear_plan.h"
 #include "moe_device.h"
@@ -505,6 +509,8 @@ __global__ __launch_bounds__(512) void gemm_linear_small_kernel(const LinearArgs
 //  * three slots for rows, two for weights (all of the LDS): a slot of rows is free from that barrier on, so block kb + 3's rows
 //    are copied behind it and have two steps to arrive; weights stay in registers from there on, so block kb + 2's are copied from the
 //    second row block of step kb on (a barrier says that every wave has read block kb's) and have one and a half.
+// 4096 x 4096 x 7168, all tiles at once: 1.48 us a step, of which its matrix instructions are 1.0 at the 2.0 GHz under load; with two
+// slots each and copies one step ahead 2.3 us.  Not the memory: with every tile reading the same operands it takes as long.
 template <bool TA, bool TW, bool GATED, int RB, int CB, int WM, int WN>
 __global__ __launch_bounds__(512) void gemm_linear_big_kernel(const LinearArgs a) {
   using C = LinCfg<RB, CB, WM, WN, 2>;
