@@ -29,7 +29,7 @@ def _p(v):
     (dict(tr=3, lda=63, ldw=256), SHAPE), (dict(ldd=255), SHAPE), (dict(C=P, ldc=255), SHAPE), (dict(pre=P, ldp=255), SHAPE),
     (dict(act=GATED | 2, ldd=127), SHAPE), (dict(lda=1 << 22), UNSUPPORTED), (dict(ldw=1 << 22), UNSUPPORTED),
     (dict(act=GATED, N=1 << 12, ldd=1 << 12, ldw=(1 << 22) - 8), UNSUPPORTED),
-    (dict(act=GATED, N=2, ldd=2, ldw=(1 << 22) - 8), UNSUPPORTED), (dict(EMPTY, act=GATED, N=512, ldd=256, ldw=1 << 21), OK), (dict(A=None), NULL), (dict(W=None), NULL),
+    (dict(act=GATED, N=2, ldd=2, ldw=(1 << 22) - 8), UNSUPPORTED), (dict(EMPTY, act=GATED, N=510, ldd=255, ldw=1 << 21), OK), (dict(A=None), NULL), (dict(W=None), NULL),
     (dict(D=None), NULL), (dict(A=P + 8), ALIGN), (dict(W=P + 2), ALIGN), (dict(lda=132), ALIGN), (dict(ldw=130), ALIGN),
     (dict(D=P + 1), ALIGN), (dict(D=P + 2, out=F32), ALIGN), (dict(bias=P + 2, btype=F32), ALIGN), (dict(bias=P + 1, btype=BF16), ALIGN),
     (dict(C=P + 2, ctype=F32), ALIGN), (dict(pre=P + 1), ALIGN), (dict(C=P + 4096, D=P + 4096, ldc=264), SHAPE),
