@@ -667,15 +667,17 @@ moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx,
  *                         [E, H/128, I/128] fp32, any values (128x128 blocks)
  *       MOE_WEIGHTS_INT4  4-bit codes as moe_grouped_gemm_int4 takes them,
  *                         S13 [E, 2I, H/128] and S2 [E, H, I/128] fp16
+ *       MOE_WEIGHTS_FP4   MXFP4 codes as moe_grouped_gemm_fp8_fp4 takes them,
+ *                         S13 [E, 2I, H/32] and S2 [E, H, I/32] E8M0 bytes
  *     weight_format | MOE_WEIGHTS_PACKED: in the orders written by
- *     moe_pack_weight_bf16 / _fp8 / _int4 (the 4-bit scales too).
+ *     moe_pack_weight_bf16 / _fp8 / _int4 / _fp4 (the scales of the last two too).
  *   1 <= E <= 1024, 1 <= k <= 64, T <= MOE_DECODE_MAX_TOKENS and
  *   T * k <= MOE_DECODE_MAX_ROUTES (more: route, pack and use the grouped
  *   GEMMs); H and I multiples of 128, at most 32768.  x, W13, W2 16-byte, scales
  *   4-byte aligned.  T == 0 is a no-op.
  *   workspace: moe_experts_decode_workspace_bytes(T, k, I) bytes (h), 16-byte
  *   aligned; calls that overlap in time must not share it. */
-enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8 = 1, MOE_WEIGHTS_INT4 = 2 };
+enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8 = 1, MOE_WEIGHTS_INT4 = 2, MOE_WEIGHTS_FP4 = 3 };
 enum { MOE_DECODE_MAX_TOKENS = 128, MOE_DECODE_MAX_ROUTES = 1024 };
 int64_t moe_experts_decode_workspace_bytes(int T, int k, int I);
 moe_status moe_experts_decode(int weight_format, const uint16_t* x, const int32_t* topk_ids,

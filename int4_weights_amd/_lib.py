@@ -24,7 +24,7 @@ F32, BF16 = 0, 1
 SCORES = {"softmax": 0, "sigmoid": 1}
 # weight formats of moe_experts_decode: (number, type, values per element, type of the scales)
 WEIGHT_FORMATS = {"bf16": (0, torch.bfloat16, 1, None), "fp8": (1, torch.uint8, 1, torch.float32),
-                  "int4": (2, torch.uint8, 2, torch.float16)}
+                  "int4": (2, torch.uint8, 2, torch.float16), "fp4": (3, torch.uint8, 2, torch.uint8)}
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _GATED, _TRANS_A, _TRANS_W = 0x10, 1, 2
 _BF16S = (torch.bfloat16,)
@@ -680,7 +680,8 @@ def moe_experts_decode(x, topk_ids, topk_weights, w13, w2, z, weights: str = "fp
     """The expert layer of a few tokens in two kernels: x bf16 [T, H], topk_ids int32 and topk_weights float32 [T, k] ->
     z bf16 [T, H] (+ residual, bf16 [T, H], which may be z).  w13 [E, 2I, H] (gate rows, then up rows) and w2 [E, H, I]:
     weights "bf16"; "fp8", uint8 codes with s13 float32 [E, 2I/128, H/128] and s2 [E, H/128, I/128]; "int4", uint8
-    [..., /2] with s13 float16 [E, 2I, H/128] and s2 [E, H, I/128]; packed: in moe_pack_weight_*'s order.  At most
+    [..., /2] with s13 float16 [E, 2I, H/128] and s2 [E, H, I/128]; "fp4", the same with MXFP4 codes and uint8 scales
+    [E, 2I, H/32], [E, H, I/32]; packed: in moe_pack_weight_*'s order.  At most
     DECODE_MAX_TOKENS tokens and DECODE_MAX_ROUTES routes.  workspace: moe_experts_decode_workspace_bytes(T, k, I) bytes."""
     fn = "moe_experts_decode"
     if weights not in WEIGHT_FORMATS:
@@ -698,9 +699,9 @@ def moe_experts_decode(x, topk_ids, topk_weights, w13, w2, z, weights: str = "fp
     if stype is not None:
         if s13 is None or s2 is None:
             raise ValueError(f"{fn}: {weights} weights need s13 and s2")
-        gran = 128 if per == 1 else 1
-        sa = _whole(fn, dev, s13, "s13", stype, (E, 2 * I // gran, H // 128))
-        sb = _whole(fn, dev, s2, "s2", stype, (E, H // gran, I // 128))
+        gran, block = 128 if per == 1 else 1, 32 if weights == "fp4" else 128
+        sa = _whole(fn, dev, s13, "s13", stype, (E, 2 * I // gran, H // block))
+        sb = _whole(fn, dev, s2, "s2", stype, (E, H // gran, I // block))
     elif s13 is not None or s2 is not None:
         raise ValueError(f"{fn}: bf16 weights have no scales")
     zp = _whole(fn, dev, z, "z", bf16, (T, H))

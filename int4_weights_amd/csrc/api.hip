@@ -842,7 +842,7 @@ moe_status moe_experts_decode(int weight_format, const uint16_t* x, const int32_
   const char* fn = "moe_experts_decode";
   static_assert(MOE_DECODE_MAX_TOKENS == kDecodeMaxTokens && MOE_DECODE_MAX_ROUTES == kDecodeMaxRoutes, "limits");
   const int format = weight_format & ~MOE_WEIGHTS_PACKED;
-  if (format < MOE_WEIGHTS_BF16 || format > MOE_WEIGHTS_INT4)
+  if (format < MOE_WEIGHTS_BF16 || format > MOE_WEIGHTS_FP4)
     return fail(MOE_ERR_UNSUPPORTED, "%s: unknown weight format %d", fn, weight_format);
   if (T < 0 || k < 1 || k > MOE_MAX_TOPK || E < 1 || E > MOE_MAX_EXPERTS || H < 1 || I < 1)
     return fail(MOE_ERR_SHAPE, "%s: T=%d k=%d E=%d H=%d I=%d", fn, T, k, E, H, I);

@@ -30,23 +30,25 @@ namespace moe {
 
 namespace {
 
-constexpr int kBf16 = 0, kFp8 = 1, kInt4 = 2;
+constexpr int kBf16 = 0, kFp8 = 1, kInt4 = 2, kFp4 = 3;
 constexpr int kRoutes = kDecodeMaxRoutes;
 
 template <int F>
 struct Fmt {
   static constexpr int BK = F == kBf16 ? 64 : 128;          // K values of a block
-  static constexpr int kPieces = F == kInt4 ? 1 : 2;        // 1 KB copies per 16 columns and block
-  static constexpr int kRowBytes = F == kInt4 ? 64 : 128;   // of a weight row's block
+  static constexpr bool kHalf = F == kInt4 || F == kFp4;    // two weights a byte
+  static constexpr int kPieces = kHalf ? 1 : 2;             // 1 KB copies per 16 columns and block
+  static constexpr int kRowBytes = kHalf ? 64 : 128;        // of a weight row's block
   static constexpr int kXRow = 2 * BK;                      // bytes of an activation row's block
   static constexpr int kXChunks = kXRow / 16;
   static constexpr int kRowsPerPiece = 1024 / kXRow;
   static constexpr int kScaled = F != kBf16;
+  __device__ static __forceinline__ int row_bytes(int K) { return kHalf ? K / 2 : F == kFp8 ? K : 2 * K; }
 };
 
 struct DecodeSide {      // one projection
   const uint8_t* W;      // [E, N, K] in the format
-  const uint8_t* S;      // scales: fp32 [E, N/128, K/128], fp16 [E, N, K/128], or none
+  const uint8_t* S;      // scales: fp32 [E, N/128, K/128], fp16 [E, N, K/128], E8M0 [E, N, K/32], or none
   int N, K;
 };
 
@@ -68,6 +70,13 @@ __device__ __forceinline__ v8bf widen_fp8(int lo, int hi) {
   const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
   const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
   const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// The bf16 values of 8 E2M1 codes times a power of two (exact; its E8M0 byte is the scale's exponent).
+__device__ __forceinline__ v8bf widen_fp4(uint32_t w, float scale) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 // 128 + q of a dword's 8 nibbles, in the order of nibbles 0 4 1 5 2 6 3 7.  magic: 0x43004300 in a vector register, so that mask
@@ -214,8 +223,10 @@ struct Stream {
   using T = Fmt<F>;
   static constexpr int XP = (BR + T::kRowsPerPiece - 1) / T::kRowsPerPiece;
   static constexpr int kWBytes = NCB * T::kPieces * 1024, kXBytes = XP * 1024;
-  static constexpr int kSlot = kWBytes + kXBytes + (T::kScaled ? 256 : 0);
-  static constexpr int kCopies = NCB * T::kPieces + XP + T::kScaled;
+  // copies of 256 bytes with a block's scales (packed MXFP4: those of 64 columns each)
+  static constexpr int kScales = !T::kScaled ? 0 : F == kFp4 && PACKED && NCB > 1 ? 2 : 1;
+  static constexpr int kSlot = kWBytes + kXBytes + 256 * kScales;
+  static constexpr int kCopies = NCB * T::kPieces + XP + kScales;
   static constexpr int S0 = RING / kSlot, S = S0 > 8 ? 8 : S0;
   static_assert(S >= 2 && (S - 1) * kCopies < 64, "ring; vmcnt's range");
   static_assert(BR == XP * T::kRowsPerPiece && BR <= 16, "rows in whole copies");
@@ -230,7 +241,7 @@ struct Stream {
   // producer: where the next block comes from
   const uint8_t* wbase[NCB];
   const uint8_t* sbase;
-  uint32_t xvoff[XP], svoff, sstep;
+  uint32_t xvoff[XP], svoff[2], sstep;
   int pkb, pend, pslot;
   int cslot;
 
@@ -239,12 +250,12 @@ struct Stream {
     l16 = lane & 15;
     lg = lane >> 4;
     lds0 = (uint32_t)uniform((int)lds_offset(mem));
-    const uint32_t rowb = F == kInt4 ? side.K / 2 : F == kFp8 ? side.K : 2 * side.K;
+    const uint32_t rowb = T::row_bytes(side.K);
 #pragma unroll
     for (int p = 0; p < T::kPieces; ++p) {
       if (PACKED) {
         wvoff[p] = 1024 * p + 16 * lane;
-      } else if (F == kInt4) {
+      } else if (T::kHalf) {
         wvoff[p] = (uint32_t)(lane >> 2) * rowb + 16u * ((lane & 3) ^ ((lane >> 4) & 3));
       } else {
         const int row = 8 * p + (lane >> 3);
@@ -262,7 +273,7 @@ struct Stream {
   template <bool TOKENS>
   __device__ __forceinline__ void produce(const Plan& p, uint32_t job, uint32_t per_k, int col0, int col1, int kb0, int kb1) {
     const int e = p.expert(job), m = p.rows(job);
-    const int64_t rowb = F == kInt4 ? side.K / 2 : F == kFp8 ? side.K : 2 * side.K;
+    const int64_t rowb = T::row_bytes(side.K);
     const uint8_t* we = side.W + (int64_t)e * side.N * rowb;
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb) {
@@ -280,14 +291,26 @@ struct Stream {
       const int cb = lane % NCB, KB = side.K / 128;
       const int n = NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2);
       sbase = side.S + (int64_t)e * (side.N / 128) * KB * 4;
-      svoff = (uint32_t)((n / 128) * KB + kb0) * 4u;
+      svoff[0] = (uint32_t)((n / 128) * KB + kb0) * 4u;
       sstep = 4;
     } else if constexpr (F == kInt4) {  // lane: that of column l16 of column block lg % NCB, and its neighbour in the dword
       const int cb = lg % NCB, KG = side.K / 128;
       const int n = (NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2)) + l16;
       sbase = side.S + (int64_t)e * side.N * KG * 2;
-      svoff = 2u * (uint32_t)(PACKED ? (kb0 * (side.N / 64) + n / 64) * 64 + (n & 15) * 4 + (n & 63) / 16 : n * KG + kb0);
+      svoff[0] = 2u * (uint32_t)(PACKED ? (kb0 * (side.N / 64) + n / 64) * 64 + (n & 15) * 4 + (n & 63) / 16 : n * KG + kb0);
       sstep = PACKED ? 2u * side.N : 2u;
+    } else if constexpr (F == kFp4) {  // a dword: the 4 scales of a column's block, or packed the lane's own of 4 column blocks
+      const int cb = lg % NCB, KG = side.K / 128;
+      sbase = side.S + (int64_t)e * side.N * KG * 4;
+      if (PACKED) {
+        svoff[0] = 4u * (uint32_t)((kb0 * (side.N / 64) + col0 / 64) * 64 + lane);
+        svoff[1] = 4u * (uint32_t)((kb0 * (side.N / 64) + col1 / 64) * 64 + lane);
+        sstep = 4u * side.N;
+      } else {
+        const int n = (NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2)) + l16;
+        svoff[0] = 4u * (uint32_t)(n * KG + kb0);
+        sstep = 4u;
+      }
     }
     pkb = kb0;
     pend = kb1;
@@ -307,9 +330,10 @@ struct Stream {
       copy16(xvoff[q], x, (uint32_t)uniform((int)(to + kWBytes + 1024 * q)));
       xvoff[q] += T::kXRow;
     }
-    if constexpr (T::kScaled) {
-      copy4(svoff & ~3u, sbase, (uint32_t)uniform((int)(to + kWBytes + kXBytes)));
-      svoff += sstep;
+#pragma unroll
+    for (int q = 0; q < kScales; ++q) {
+      copy4(svoff[q] & ~3u, sbase, (uint32_t)uniform((int)(to + kWBytes + kXBytes + 256 * q)));
+      svoff[q] += sstep;
     }
     pslot = pslot + 1 == S ? 0 : pslot + 1;
     ++pkb;
@@ -318,7 +342,7 @@ struct Stream {
   // The oldest block's fragments, in registers.
   struct Frags {
     v4i w[NCB][T::kPieces], x[F == kBf16 ? 2 : 4];
-    uint32_t s[NCB];  // FP8: the scale; 4-bit: a dword with the scale in either half
+    uint32_t s[NCB];  // FP8: the scale; 4-bit: a dword with the scale in either half; MXFP4: with it in one of its bytes
   };
   __device__ __forceinline__ void read(Frags& f) {
     const uint8_t* w = ring + cslot * kSlot;
@@ -333,18 +357,19 @@ struct Stream {
       for (int i = 0; i < 4; ++i) f.x[i] = *(const v4i*)(xs + row * 256 + 16 * ((8 * (i >> 1) + 2 * lg + (i & 1)) ^ row));
     } else {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) f.x[d] = *(const v4i*)(xs + row * 256 + 16 * ((PACKED ? 4 * d + lg : 4 * lg + d) ^ row));
+      for (int d = 0; d < 4; ++d) f.x[d] = *(const v4i*)(xs + row * 256 + 16 * ((PACKED && F == kInt4 ? 4 * d + lg : 4 * lg + d) ^ row));
     }
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb) {
 #pragma unroll
       for (int h = 0; h < T::kPieces; ++h) {
         const int at = PACKED ? 1024 * h + 16 * lane
-                              : F == kInt4 ? l16 * 64 + 16 * (lg ^ (l16 >> 2)) : l16 * 128 + 16 * ((4 * h + lg) ^ ((l16 >> 1) & 7));
+                              : T::kHalf ? l16 * 64 + 16 * (lg ^ (l16 >> 2)) : l16 * 128 + 16 * ((4 * h + lg) ^ ((l16 >> 1) & 7));
         f.w[cb][h] = *(const v4i*)(w + cb * T::kPieces * 1024 + at);
       }
       if constexpr (F == kFp8) f.s[cb] = *(const uint32_t*)(sc + 4 * cb);
-      if constexpr (F == kInt4) f.s[cb] = *(const uint32_t*)(sc + 4 * (16 * cb + l16));
+      if constexpr (F == kInt4 || (F == kFp4 && !PACKED)) f.s[cb] = *(const uint32_t*)(sc + 4 * (16 * cb + l16));
+      if constexpr (F == kFp4 && PACKED) f.s[cb] = *(const uint32_t*)(sc + (NCB > 1 && cb >= NCB / 2 ? 256 : 0) + 4 * lane);
     }
     cslot = cslot + 1 == S ? 0 : cslot + 1;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot may be filled anew
@@ -369,6 +394,16 @@ struct Stream {
       for (int cb = 0; cb < NCB; ++cb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(__uint_as_float(f.s[cb]), s[cb][i], acc[cb][i]);
+    } else if constexpr (F == kFp4) {
+      // E2M1 times a power of two is a bf16 number: widened with its scale, products add up without a block sum of their own
+#pragma unroll
+      for (int cb = 0; cb < NCB; ++cb) {
+        const int n = NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2);
+        const int byte = PACKED ? (n & 63) / 16 : lg;
+        const float scale = __uint_as_float((f.s[cb] >> (8 * byte) & 0xffu) << 23);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[cb] = mma(f.x[d], widen_fp4((uint32_t)f.w[cb][0][d], scale), acc[cb]);
+      }
     } else {
       const v8bf m136 = {(__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f,
                          (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f};
@@ -412,7 +447,7 @@ constexpr int kUpRing = 17 * 1024;
 // one barrier), the plan.
 template <int F, int BR, int NW>
 struct UpCfg {
-  static constexpr int NCB = F == kInt4 ? 4 : 2, kCols = 8 * NCB;  // columns of h per unit
+  static constexpr int NCB = Fmt<F>::kHalf ? 4 : 2, kCols = 8 * NCB;  // columns of h per unit
   static constexpr int kRow = 16 * NCB + 2, kPart = NW * BR * kRow;
   static constexpr int kBufs = 8 * kPart <= (NW == 4 ? 10 : 20) * 1024 ? 2 : 1;
   static constexpr int kPlanAt = NW * kUpRing + kBufs * kPart * 4;
@@ -596,7 +631,7 @@ hipError_t launch_rows(DecodeArgs a, hipStream_t s) {
   const int nw = wide ? 8 : 4;
   a.ksplit = 1;
   while (a.ksplit * R < nw && 2 * a.ksplit <= nb) a.ksplit *= 2;
-  if constexpr (F == kInt4 && BR == 4)
+  if constexpr (Fmt<F>::kHalf && BR == 4)
     if (a.H / 16 <= cus && 16 * kDownShort + 74 * R + 4 + 64 * 16 <= kLdsMost) {
       while (a.ksplit * R < 16 && 2 * a.ksplit <= nb) a.ksplit *= 2;
       return launch_down<F, PACKED, BR, 16, kDownShort>(a, s);
@@ -627,7 +662,8 @@ hipError_t launch_experts_decode(const DecodeArgs& a, hipStream_t s) {
   switch (a.format) {
     case kBf16: return a.packed ? launch_format<kBf16, true>(a, s) : launch_format<kBf16, false>(a, s);
     case kFp8: return a.packed ? launch_format<kFp8, true>(a, s) : launch_format<kFp8, false>(a, s);
-    default: return a.packed ? launch_format<kInt4, true>(a, s) : launch_format<kInt4, false>(a, s);
+    case kInt4: return a.packed ? launch_format<kInt4, true>(a, s) : launch_format<kInt4, false>(a, s);
+    default: return a.packed ? launch_format<kFp4, true>(a, s) : launch_format<kFp4, false>(a, s);
   }
 }
 

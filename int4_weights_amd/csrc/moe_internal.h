@@ -169,7 +169,7 @@ hipError_t launch_gemm_dense(const DenseArgs& a, hipStream_t s);
 
 constexpr int kDecodeMaxTokens = 128, kDecodeMaxRoutes = 1024;
 struct DecodeArgs {
-  int format;            // 0 bf16, 1 FP8, 2 4-bit
+  int format;            // 0 bf16, 1 FP8, 2 4-bit, 3 MXFP4
   int packed;            // weights (and 4-bit scales) in the fragment-packed orders
   const uint16_t* x;     // bf16 [T, H]
   const int32_t* ids;    // [T, k]

@@ -293,8 +293,8 @@ class DenseFP8Linear:
 class MoeDecodeLayer:
     """The expert layer of a decode step: up-projection, SwiGLU, down-projection and weighted sum in two kernels.
 
-    w13 [E, 2I, H] (gate rows, then up rows) and w2 [E, H, I] in weights "bf16", "fp8" (s13, s2 float32 per 128x128) or
-    "int4" (float16 per 128), packed: in moe_pack_weight_*'s order; the same tensors that the grouped layers above hold.
+    w13 [E, 2I, H] (gate rows, then up rows) and w2 [E, H, I] in weights "bf16", "fp8" (s13, s2 float32 per 128x128),
+    "int4" (float16 per 128) or "fp4" (uint8 per 32), packed: in moe_pack_weight_*'s order; the same tensors that the grouped layers above hold.
     Buffers for up to max_tokens tokens (at most DECODE_MAX_TOKENS, and DECODE_MAX_ROUTES routes): a forward allocates
     nothing, and calls of one object that overlap in time must not run on two streams."""
 

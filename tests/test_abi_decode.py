@@ -16,7 +16,7 @@ def _p(v):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(fmt=3), UNSUPPORTED), (dict(fmt=-1), UNSUPPORTED), (dict(fmt=0x20), UNSUPPORTED), (dict(T=-1), SHAPE),
+    (dict(fmt=4), UNSUPPORTED), (dict(fmt=3, s13=None), NULL), (dict(fmt=-1), UNSUPPORTED), (dict(fmt=0x20), UNSUPPORTED), (dict(T=-1), SHAPE),
     (dict(k=0), SHAPE), (dict(k=65), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(H=0), SHAPE), (dict(I=0), SHAPE),
     (dict(T=129, k=1), UNSUPPORTED), (dict(T=128, k=9), UNSUPPORTED), (dict(T=1 << 30, k=64), UNSUPPORTED),
     (dict(H=192), UNSUPPORTED), (dict(I=64), UNSUPPORTED), (dict(H=32768 + 128), UNSUPPORTED), (dict(I=32768 + 128), UNSUPPORTED),
@@ -51,5 +51,5 @@ def test_binding_refuses_cpu_tensors_and_unknown_formats():
     w13, w2 = torch.zeros(1, 256, 128, dtype=torch.bfloat16), torch.zeros(1, 128, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU tensor"):
         moe.moe_experts_decode(t, ids, p, w13, w2, t, weights="bf16")
-    with pytest.raises(ValueError, match="one of bf16, fp8, int4"):
-        moe.moe_experts_decode(t, ids, p, w13, w2, t, weights="fp4")
+    with pytest.raises(ValueError, match="one of bf16, fp8, int4, fp4"):
+        moe.moe_experts_decode(t, ids, p, w13, w2, t, weights="int8")

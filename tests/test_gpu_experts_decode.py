@@ -33,6 +33,15 @@ class Layer:
                 moe.moe_pack_weight_fp8(q, p)
                 big = s.double().repeat_interleave(128, 1).repeat_interleave(128, 2)
                 val = (q.view(torch.float8_e4m3fn).double() * big).cpu().numpy()
+            elif fmt == "fp4":
+                q = torch.empty(E, N, K // 2, dtype=torch.uint8, device=DEV)
+                s = torch.empty(E, N, K // 32, dtype=torch.uint8, device=DEV)
+                w = (w.view(E, N, -1, 32) * torch.exp2(torch.randint(-3, 4, (E, N, K // 32, 1), generator=g)).to(DEV)).view(E, N, K)
+                moe.moe_quant_weight_fp4(w.to(torch.bfloat16), q, s)  # scales that differ from block to block
+                p, sp = torch.empty_like(q), torch.empty_like(s)
+                moe.moe_pack_weight_fp4(q, s, p, sp)
+                codes = torch.stack((q & 15, q >> 4), -1).view(E, N, K).cpu().numpy()
+                val = oracle.e2m1_decode_table()[codes] * np.repeat(np.exp2(s.double().cpu().numpy() - 127), 32, 2)
             else:
                 q = torch.empty(E, N, K // 2, dtype=torch.uint8, device=DEV)
                 s = torch.empty(E, N, K // 128, dtype=torch.float16, device=DEV)
@@ -99,7 +108,7 @@ SHAPES = [  # T, k, E, H, I, dropped, one expert for all
 
 
 @pytest.mark.parametrize("packed", [False, True])
-@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int4", "fp4"])
 @pytest.mark.parametrize("T,k,E,H,I,dropped,one", SHAPES)
 def test_against_the_oracle(fmt, packed, T, k, E, H, I, dropped, one):
     require_gpu()
@@ -110,7 +119,7 @@ def test_against_the_oracle(fmt, packed, T, k, E, H, I, dropped, one):
     check(L, L.run(x, ids, p, packed=packed, residual=res), x, ids, p, res)
 
 
-@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int4", "fp4"])
 def test_orders_agree_and_results_repeat(fmt):
     """Packed weights are the same numbers; nothing depends on timing.  (The orders add a block's products up differently, so
     they agree to the sums' rounding only: at most a step of bf16.)"""
@@ -161,7 +170,7 @@ def test_weights_of_skipped_slots_do_not_count():
     assert torch.equal(z, L.run(x, ids, p))
 
 
-@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int4", "fp4"])
 def test_a_bad_row_stays_alone(fmt):
     """Infinities and NaN of one token reach no other, whatever rows share its matrix instructions."""
     require_gpu()
