@@ -10,17 +10,18 @@
 //
 // Both kernels multiply with v_mfma_f32_16x16x32_bf16, rows (tokens) as its A operand and 16 weight columns as its B operand:
 // a lane holds one column of 4 rows.  FP8 codes are widened to bf16 (exact), 4-bit codes become 128 + q in bf16 (exact), with
-// -136 times the row's sum from an instruction against a constant; a block's sum of 128 products is scaled in fp32.  h is
-// rounded to bf16 once (it is the matrix instruction's operand; everything else up to Z stays in fp32).
+// -136 times the row's sum from an instruction against a constant; a block's sum of 128 products is scaled in fp32.  MXFP4
+// codes are widened together with their power-of-two scale (exact) and need no block sum.  h is rounded to bf16 once (it is
+// the matrix instruction's operand; everything else up to Z stays in fp32).
 //
-// A job is an expert and up to BR of its routes.  Up-projection: a unit is a job and 16 (4-bit: 32) columns of h, whose K the 4
-// (8) waves share; persistent workgroups walk over the units.  Down-projection: a workgroup owns 16 columns of Z and takes every
+// A job is an expert and up to BR of its routes.  Up-projection: a unit is a job and 16 (4-bit and MXFP4: 32) columns of h, whose
+// K the 4 (8) waves share; persistent workgroups walk over the units.  Down-projection: a workgroup owns 16 columns of Z and takes every
 // job, its waves in turn; the rows' sums meet in LDS as one line per route, so the sum over a token's slots runs in slot order
 // whatever wave was first, and no partial result goes through memory.
 //
 // Measured (us; TB/s of the active experts' weights): 1 token, 8 of 256 experts, 7168 x 2048, FP8 59.4 (5.9); 61 tokens, 8 of 128,
-// 4096 x 1536, bf16 686 to 720 (6.6 to 6.9), FP8 375 (6.3); 16 tokens, 4096 x 768, 4-bit packed 80 (5.0), row-major 120.  A
-// plain read of memory reaches 7.3 TB/s.  What bounds it: bytes in flight (the rings, 64 to 110 KB a compute unit), the start and
+// 4096 x 1536, bf16 686 to 720 (6.6 to 6.9), FP8 375 (6.3); 16 tokens, 4096 x 768, 4-bit packed 80 (5.0), row-major 120
+// (copied in pieces of 64 bytes), MXFP4 packed 83.  A plain read of memory reaches 7.3 TB/s.  What bounds it: bytes in flight (the rings, 64 to 110 KB a compute unit), the start and
 // the last round of units, and for 4-bit codes the widening beside the stream.
 #include "linear_act.h"
 #include "moe_device.h"
