@@ -668,7 +668,8 @@ moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx,
  *       MOE_WEIGHTS_INT4  4-bit codes as moe_grouped_gemm_int4 takes them,
  *                         S13 [E, 2I, H/128] and S2 [E, H, I/128] fp16
  *       MOE_WEIGHTS_FP4   MXFP4 codes as moe_grouped_gemm_fp8_fp4 takes them,
- *                         S13 [E, 2I, H/32] and S2 [E, H, I/32] E8M0 bytes
+ *                         S13 [E, 2I, H/32] and S2 [E, H, I/32] E8M0 bytes, any
+ *                         (0 to 254: 2^-127 to 2^127; 255: NaN)
  *     weight_format | MOE_WEIGHTS_PACKED: in the orders written by
  *     moe_pack_weight_bf16 / _fp8 / _int4 / _fp4 (the scales of the last two too).
  *   1 <= E <= 1024, 1 <= k <= 64, T <= MOE_DECODE_MAX_TOKENS and

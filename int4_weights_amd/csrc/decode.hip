@@ -11,7 +11,8 @@
 // Both kernels multiply with v_mfma_f32_16x16x32_bf16, rows (tokens) as its A operand and 16 weight columns as its B operand:
 // a lane holds one column of 4 rows.  FP8 codes are widened to bf16 (exact), 4-bit codes become 128 + q in bf16 (exact), with
 // -136 times the row's sum from an instruction against a constant; a block's sum of 128 products is scaled in fp32.  MXFP4
-// codes are widened together with their power-of-two scale (exact) and need no block sum.  h is rounded to bf16 once (it is
+// codes are widened together with their power-of-two scale (exact) and need no block sum (but beside it for the two largest scales,
+// past bf16's range).  h is rounded to bf16 once (it is
 // the matrix instruction's operand; everything else up to Z stays in fp32).
 //
 // A job is an expert and up to BR of its routes.  Up-projection: a unit is a job and 16 (4-bit and MXFP4: 32) columns of h, whose
@@ -73,13 +74,17 @@ __device__ __forceinline__ v8bf widen_fp8(int lo, int hi) {
   const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-// The bf16 values of 8 E2M1 codes times a power of two (exact; its E8M0 byte is the scale's exponent).
+// The bf16 values of 8 E2M1 codes times a power of two (exact below 2^128; its E8M0 byte is the scale's exponent: byte 0 is 2^-127,
+// 255 NaN, and bf16's subnormals hold the smallest ones).
 __device__ __forceinline__ v8bf widen_fp4(uint32_t w, float scale) {
   typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
   const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
   const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
+// The two scales (2^126 and 2^127) that take codes past the largest bf16 number.  (Looking for them costs 0 to 2%: 1 token, 8 of 256
+// experts, 7168 x 2048 packed 44.9 -> 45.2 us; 16 tokens, 8 of 128, 4096 x 768 81.0 -> 81.8.)
+constexpr uint32_t kFarScale = 253, kNanScale = 255;
 // 128 + q of a dword's 8 nibbles, in the order of nibbles 0 4 1 5 2 6 3 7.  magic: 0x43004300 in a vector register, so that mask
 // and exponent take one instruction.
 __device__ __forceinline__ v8bf widen_int4(uint32_t w, uint32_t magic) {
@@ -97,6 +102,21 @@ __device__ __forceinline__ v4i nibble_order(const v4i x) {
 }
 __device__ __forceinline__ v4f mma(const v4i x, const v8bf w, const v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x), w, c, 0, 0, 0);
+}
+
+// Where some lane's scale is a far one: those lanes' products, with scales 2^8 lower, in a sum of their own, whose 2^8-fold goes
+// to acc; w keeps the other lanes' codes.
+__device__ __forceinline__ void far_fp4(const v4i (&x)[4], v4i& w, uint32_t e8m0, v4f& acc) {
+  const bool far = e8m0 >= kFarScale && e8m0 != kNanScale;
+  const float scale = __uint_as_float((far ? e8m0 - 8 : 0u) << 23);
+  v4f s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < 4; ++d) s = mma(x[d], widen_fp4(far ? (uint32_t)w[d] : 0u, scale), s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[i] = __builtin_fmaf(256.f, s[i], acc[i]);
+    w[i] = far ? 0 : w[i];
+  }
 }
 
 // ------------------------------------------------------------------ plan --
@@ -397,13 +417,25 @@ struct Stream {
         for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(__uint_as_float(f.s[cb]), s[cb][i], acc[cb][i]);
     } else if constexpr (F == kFp4) {
       // E2M1 times a power of two is a bf16 number: widened with its scale, products add up without a block sum of their own
+      uint32_t e8m0[NCB], most = 0;
 #pragma unroll
       for (int cb = 0; cb < NCB; ++cb) {
         const int n = NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2);
-        const int byte = PACKED ? (n & 63) / 16 : lg;
-        const float scale = __uint_as_float((f.s[cb] >> (8 * byte) & 0xffu) << 23);
+        e8m0[cb] = f.s[cb] >> (8 * (PACKED ? (n & 63) / 16 : lg)) & 0xffu;
+        most = max(most, e8m0[cb]);
+      }
+      v4i w[NCB];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) acc[cb] = mma(f.x[d], widen_fp4((uint32_t)f.w[cb][0][d], scale), acc[cb]);
+      for (int cb = 0; cb < NCB; ++cb) w[cb] = f.w[cb][0];
+      if (__builtin_expect(__ballot(most >= kFarScale) != 0, 0)) {
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) far_fp4(f.x, w[cb], e8m0[cb], acc[cb]);
+      }
+#pragma unroll
+      for (int cb = 0; cb < NCB; ++cb) {
+        const float scale = __uint_as_float(e8m0[cb] << 23);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[cb] = mma(f.x[d], widen_fp4((uint32_t)w[cb][d], scale), acc[cb]);
       }
     } else {
       const v8bf m136 = {(__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f,
