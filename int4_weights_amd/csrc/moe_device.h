@@ -65,13 +65,16 @@ __device__ __forceinline__ uint32_t e4m3_encode(float v) {
 // silu(g) = g / (1 + exp(-g)) in fp32: x = -g log2(e) carried as hi + lo (hi the rounded product, lo its
 // error by one fma plus g times the error of the fp32 log2(e)); t = exp2(hi) * (1 + lo ln 2) with the
 // hardware exp2; silu = g * rcp(1 + t) with the hardware reciprocal.  Relative error a few fp32 ulps (about
-// 3e-7); a gate below about -88 makes t infinite and the result -0, never NaN.
+// 3e-7); a gate below about -88 makes t infinite and the result -0, never NaN.  t is 0 and infinite at g = 128
+// and -128 already, so the exponent takes g within them: past 2.3e38 its product with log2(e) would overflow,
+// and from about -4.8e7 down 1 + lo ln 2 can be negative.
 __device__ __forceinline__ float silu_f32(float g) {
   constexpr float kLog2e = 1.44269504088896341f;       // log2(e) rounded to fp32
   constexpr float kLog2eLo = 1.92596299e-08f;            // log2(e) - kLog2e
   constexpr float kLn2 = 0.693147180559945309f;
-  const float hi = -g * kLog2e;
-  const float lo = __builtin_fmaf(-g, kLog2e, -hi) - g * kLog2eLo;
+  const float x = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);
+  const float hi = -x * kLog2e;
+  const float lo = __builtin_fmaf(-x, kLog2e, -hi) - x * kLog2eLo;
   const float t = __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.0f);
   return g * __builtin_amdgcn_rcpf(1.0f + t);
 }
