@@ -24,6 +24,7 @@
 // 4096 x 1536, bf16 686 to 720 (6.6 to 6.9), FP8 375 (6.3); 16 tokens, 4096 x 768, 4-bit packed 80 (5.0), row-major 120
 // (copied in pieces of 64 bytes), MXFP4 packed 83.  A plain read of memory reaches 7.3 TB/s.  What bounds it: bytes in flight (the rings, 64 to 110 KB a compute unit), the start and
 // the last round of units, and for 4-bit codes the widening beside the stream.
+#include "decode_plan.h"
 #include "linear_act.h"
 #include "moe_device.h"
 #include "moe_internal.h"
@@ -32,13 +33,13 @@ namespace moe {
 
 namespace {
 
-constexpr int kBf16 = 0, kFp8 = 1, kInt4 = 2, kFp4 = 3;
+constexpr int kBf16 = kDecBf16, kFp8 = kDecFp8, kInt4 = kDecInt4, kFp4 = kDecFp4;
 constexpr int kRoutes = kDecodeMaxRoutes;
 
 template <int F>
 struct Fmt {
-  static constexpr int BK = F == kBf16 ? 64 : 128;          // K values of a block
-  static constexpr bool kHalf = F == kInt4 || F == kFp4;    // two weights a byte
+  static constexpr int BK = dec_block(F);                   // K values of a block
+  static constexpr bool kHalf = dec_half(F);                // two weights a byte
   static constexpr int kPieces = kHalf ? 1 : 2;             // 1 KB copies per 16 columns and block
   static constexpr int kRowBytes = kHalf ? 64 : 128;        // of a weight row's block
   static constexpr int kXRow = 2 * BK;                      // bytes of an activation row's block
@@ -124,7 +125,6 @@ struct Plan {
   uint32_t* job;    // [R] expert | rows << 10 | (first place in order) << 15
   uint16_t* order;  // [R] routes grouped by expert
   int* njobs;
-  static constexpr int bytes(int R) { return 6 * R + 4; }
   __device__ __forceinline__ Plan(uint8_t* mem, int R) {
     njobs = (int*)mem;
     job = (uint32_t*)(mem + 4);
@@ -474,16 +474,11 @@ struct Stream {
 };
 
 // -------------------------------------------------------------------- up --
-constexpr int kUpRing = 17 * 1024;
-
-// LDS: the rings, the waves' sums of a unit (twice where that leaves room for two workgroups on a compute unit: then a unit takes
-// one barrier), the plan.
 template <int F, int BR, int NW>
 struct UpCfg {
-  static constexpr int NCB = Fmt<F>::kHalf ? 4 : 2, kCols = 8 * NCB;  // columns of h per unit
-  static constexpr int kRow = 16 * NCB + 2, kPart = NW * BR * kRow;
-  static constexpr int kBufs = 8 * kPart <= (NW == 4 ? 10 : 20) * 1024 ? 2 : 1;
-  static constexpr int kPlanAt = NW * kUpRing + kBufs * kPart * 4;
+  static constexpr int NCB = dec_up_blocks(F), kCols = dec_up_cols(F), kRow = dec_up_row(F);
+  static constexpr int kPart = dec_up_part(F, BR, NW), kBufs = dec_up_bufs(F, BR, NW), kPlanAt = dec_up_plan_at(F, BR, NW);
+  static_assert(dec_up_lds(F, BR, NW, kRoutes) <= kLdsMost, "any number of routes");
 };
 
 template <int F, bool PACKED, int BR, int NW>
@@ -561,9 +556,7 @@ __global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_up_kernel(const
 }
 
 // ------------------------------------------------------------------ down --
-constexpr int kDownRing = 13 * 1024, kDownDeep = 19 * 1024, kDownShort = 9 * 1024;
-constexpr int kLdsMost = 160 * 1024;
-static_assert(4 * kDownRing + 74 * kRoutes + 4 <= kLdsMost, "any number of routes fits four waves' rings");
+static_assert(dec_down_lds(4, kDownRing, 1, kRoutes) <= kLdsMost, "any number of routes fits four waves' rings");
 
 // LDS: NW rings, then a line of 16 sums per share of K and route, then topk_weights and the plan.
 template <int F, bool PACKED, int BR, int NW, int RING>
@@ -634,57 +627,44 @@ __global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_down_kernel(con
   }
 }
 
-template <int F, bool PACKED, int BR, int NW, int RING>
-hipError_t launch_down(const DecodeArgs& a, hipStream_t s) {
-  const size_t lds = NW * RING + a.T * a.k * (64 * a.ksplit + 4) + Plan::bytes(a.T * a.k);
-  decode_down_kernel<F, PACKED, BR, NW, RING><<<a.H / 16, NW * 64, lds, s>>>(a);
+template <int F, bool PACKED, int BR, int NW>
+hipError_t launch_up(const DecodeArgs& a, int groups, hipStream_t s) {
+  decode_up_kernel<F, PACKED, BR, NW><<<groups, NW * 64, dec_up_lds(F, BR, NW, a.T * a.k), s>>>(a);
   return hipGetLastError();
 }
 
-template <int F, bool PACKED, int BR, int NW>
-hipError_t launch_up(const DecodeArgs& a, int64_t units, int64_t most, hipStream_t s) {
-  decode_up_kernel<F, PACKED, BR, NW><<<(unsigned)(units < most ? units : most), NW * 64,
-                                        UpCfg<F, BR, NW>::kPlanAt + Plan::bytes(a.T * a.k), s>>>(a);
+template <int F, bool PACKED, int BR, int NW, int RING>
+hipError_t launch_down(const DecodeArgs& a, hipStream_t s) {
+  decode_down_kernel<F, PACKED, BR, NW, RING><<<a.H / 16, NW * 64, dec_down_lds(NW, RING, a.ksplit, a.T * a.k), s>>>(a);
   return hipGetLastError();
 }
 
 template <int F, bool PACKED, int BR>
-hipError_t launch_rows(DecodeArgs a, hipStream_t s) {
-  const int R = a.T * a.k, nb = a.I / Fmt<F>::BK, cus = device_info().cus;
-  a.per_k = (65536 + a.k - 1) / a.k;
-  // Up: two workgroups of 4 waves on a compute unit; where there is no more than one unit of work for each, 8 waves share it.
-  const int64_t units = (int64_t)R * (a.I / UpCfg<F, BR, 4>::kCols);
+hipError_t launch_rows(const DecodeArgs& a, const DecodePlan& p, hipStream_t s) {
   hipError_t e;
-  if constexpr (BR < 16) e = units <= cus ? launch_up<F, PACKED, BR, 8>(a, units, cus, s) : launch_up<F, PACKED, BR, 4>(a, units, 2 * cus, s);
-  else e = launch_up<F, PACKED, BR, 4>(a, units, 2 * cus, s);
+  if constexpr (BR < 16) e = p.up_waves == 8 ? launch_up<F, PACKED, BR, 8>(a, p.up_groups, s) : launch_up<F, PACKED, BR, 4>(a, p.up_groups, s);
+  else e = launch_up<F, PACKED, BR, 4>(a, p.up_groups, s);
   if (e != hipSuccess) return e;
-  // Down: workgroups that have a compute unit to themselves, because there are few or because of the routes' lines, have 8 waves,
-  // else 4; few routes leave room for deeper rings, and their K is shared so that every wave has a part.
-  const bool wide = 8 * kDownRing + 74 * R + 4 <= kLdsMost && (a.H / 16 <= cus || 2 * (4 * kDownRing + 74 * R + 4) > kLdsMost);
-  const int nw = wide ? 8 : 4;
-  a.ksplit = 1;
-  while (a.ksplit * R < nw && 2 * a.ksplit <= nb) a.ksplit *= 2;
   if constexpr (Fmt<F>::kHalf && BR == 4)
-    if (a.H / 16 <= cus && 16 * kDownShort + 74 * R + 4 + 64 * 16 <= kLdsMost) {
-      while (a.ksplit * R < 16 && 2 * a.ksplit <= nb) a.ksplit *= 2;
-      return launch_down<F, PACKED, BR, 16, kDownShort>(a, s);
-    }
+    if (p.down_waves == 16) return launch_down<F, PACKED, BR, 16, kDownShort>(a, s);
   if constexpr (BR < 16) {
-    if (wide && 8 * kDownDeep + 74 * R + 4 + 64 * 8 <= kLdsMost) return launch_down<F, PACKED, BR, 8, kDownDeep>(a, s);
-    if (!wide && 2 * (4 * kDownDeep + 74 * R + 4 + 64 * 8) <= kLdsMost) return launch_down<F, PACKED, BR, 4, kDownDeep>(a, s);
+    if (p.down_ring == kDownDeep) {
+      if constexpr (!(Fmt<F>::kHalf && BR == 4))
+        if (p.down_waves == 8) return launch_down<F, PACKED, BR, 8, kDownDeep>(a, s);
+      return launch_down<F, PACKED, BR, 4, kDownDeep>(a, s);
+    }
   }
-  return wide ? launch_down<F, PACKED, BR, 8, kDownRing>(a, s) : launch_down<F, PACKED, BR, 4, kDownRing>(a, s);
+  return p.down_waves == 8 ? launch_down<F, PACKED, BR, 8, kDownRing>(a, s) : launch_down<F, PACKED, BR, 4, kDownRing>(a, s);
 }
 
 template <int F, bool PACKED>
-hipError_t launch_format(const DecodeArgs& a, hipStream_t s) {
-  // rows of a job: what most experts get, so that their weights are read once
-  const float mean = (float)a.T * (float)a.k / (float)a.E;
-  const int most = a.T;
+hipError_t launch_format(DecodeArgs a, hipStream_t s) {
+  const DecodePlan p = plan_decode(F, a.T, a.k, a.E, a.H, a.I, device_info().cus);
+  a.per_k = (65536 + a.k - 1) / a.k;
+  a.ksplit = p.ksplit;
   if constexpr (F != kBf16)
-    if (mean <= 2.0f || most <= 4) return launch_rows<F, PACKED, 4>(a, s);
-  if (mean <= 5.0f || most <= 8) return launch_rows<F, PACKED, 8>(a, s);
-  return launch_rows<F, PACKED, 16>(a, s);
+    if (p.rows == 4) return launch_rows<F, PACKED, 4>(a, p, s);
+  return p.rows == 8 ? launch_rows<F, PACKED, 8>(a, p, s) : launch_rows<F, PACKED, 16>(a, p, s);
 }
 
 }  // namespace
