@@ -11,8 +11,8 @@
 // Both kernels multiply with v_mfma_f32_16x16x32_bf16, rows (tokens) as its A operand and 16 weight columns as its B operand:
 // a lane holds one column of 4 rows.  FP8 codes are widened to bf16 (exact), 4-bit codes become 128 + q in bf16 (exact), with
 // -136 times the row's sum from an instruction against a constant; a block's sum of 128 products is scaled in fp32.  MXFP4
-// codes are widened together with their power-of-two scale (exact) and need no block sum (but beside it for the two largest scales,
-// past bf16's range).  h is rounded to bf16 once (it is
+// codes are widened together with their power-of-two scale (exact) and need no block sum; a unit with one of the two largest scales,
+// which take codes past bf16's range, is added up a second time.  h is rounded to bf16 once (it is
 // the matrix instruction's operand; everything else up to Z stays in fp32).
 //
 // A job is an expert and up to BR of its routes.  Up-projection: a unit is a job and 16 (4-bit and MXFP4: 32) columns of h, whose
@@ -83,8 +83,7 @@ __device__ __forceinline__ v8bf widen_fp4(uint32_t w, float scale) {
   const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-// The two scales (2^126 and 2^127) that take codes past the largest bf16 number.  (Looking for them costs 0 to 2%: 1 token, 8 of 256
-// experts, 7168 x 2048 packed 44.9 -> 45.2 us; 16 tokens, 8 of 128, 4096 x 768 81.0 -> 81.8.)
+// The two scales (2^126 and 2^127) that take codes past the largest bf16 number.
 constexpr uint32_t kFarScale = 253, kNanScale = 255;
 // 128 + q of a dword's 8 nibbles, in the order of nibbles 0 4 1 5 2 6 3 7.  magic: 0x43004300 in a vector register, so that mask
 // and exponent take one instruction.
@@ -103,21 +102,6 @@ __device__ __forceinline__ v4i nibble_order(const v4i x) {
 }
 __device__ __forceinline__ v4f mma(const v4i x, const v8bf w, const v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x), w, c, 0, 0, 0);
-}
-
-// Where some lane's scale is a far one: those lanes' products, with scales 2^8 lower, in a sum of their own, whose 2^8-fold goes
-// to acc; w keeps the other lanes' codes.
-__device__ __forceinline__ void far_fp4(const v4i (&x)[4], v4i& w, uint32_t e8m0, v4f& acc) {
-  const bool far = e8m0 >= kFarScale && e8m0 != kNanScale;
-  const float scale = __uint_as_float((far ? e8m0 - 8 : 0u) << 23);
-  v4f s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int d = 0; d < 4; ++d) s = mma(x[d], widen_fp4(far ? (uint32_t)w[d] : 0u, scale), s);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc[i] = __builtin_fmaf(256.f, s[i], acc[i]);
-    w[i] = far ? 0 : w[i];
-  }
 }
 
 // ------------------------------------------------------------------ plan --
@@ -265,6 +249,7 @@ struct Stream {
   uint32_t xvoff[XP], svoff[2], sstep;
   int pkb, pend, pslot;
   int cslot;
+  uint32_t top;            // MXFP4: the largest scale byte of this lane's since begin()
 
   __device__ __forceinline__ Stream(const DecodeSide& s, const uint8_t* rows, uint8_t* mem) : side(s), x(rows), ring(mem) {
     lane = lane_id();
@@ -396,7 +381,7 @@ struct Stream {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot may be filled anew
   }
   // acc += the block.  kb and col0/col1 are the consumer's (4-bit scales lie in either half of a dword).
-  __device__ __forceinline__ void multiply(const Frags& f, v4f (&acc)[NCB], int kb, int col0, int col1) const {
+  __device__ __forceinline__ void multiply(const Frags& f, v4f (&acc)[NCB], int kb, int col0, int col1) {
     if constexpr (F == kBf16) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -417,25 +402,13 @@ struct Stream {
         for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(__uint_as_float(f.s[cb]), s[cb][i], acc[cb][i]);
     } else if constexpr (F == kFp4) {
       // E2M1 times a power of two is a bf16 number: widened with its scale, products add up without a block sum of their own
-      uint32_t e8m0[NCB], most = 0;
 #pragma unroll
       for (int cb = 0; cb < NCB; ++cb) {
-        const int n = NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2);
-        e8m0[cb] = f.s[cb] >> (8 * (PACKED ? (n & 63) / 16 : lg)) & 0xffu;
-        most = max(most, e8m0[cb]);
-      }
-      v4i w[NCB];
+        const uint32_t e8m0 = f.s[cb] >> (8 * scale_byte(column(cb, col0, col1))) & 0xffu;
+        const float scale = __uint_as_float(e8m0 << 23);
+        top = max(top, e8m0);
 #pragma unroll
-      for (int cb = 0; cb < NCB; ++cb) w[cb] = f.w[cb][0];
-      if (__builtin_expect(__ballot(most >= kFarScale) != 0, 0)) {
-#pragma unroll
-        for (int cb = 0; cb < NCB; ++cb) far_fp4(f.x, w[cb], e8m0[cb], acc[cb]);
-      }
-#pragma unroll
-      for (int cb = 0; cb < NCB; ++cb) {
-        const float scale = __uint_as_float(e8m0[cb] << 23);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) acc[cb] = mma(f.x[d], widen_fp4((uint32_t)w[cb][d], scale), acc[cb]);
+        for (int d = 0; d < 4; ++d) acc[cb] = mma(f.x[d], widen_fp4((uint32_t)f.w[cb][0][d], scale), acc[cb]);
       }
     } else {
       const v8bf m136 = {(__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f, (__bf16)-136.f,
@@ -461,6 +434,59 @@ struct Stream {
         const float q = (float)__builtin_bit_cast(_Float16, (uint16_t)(half ? f.s[cb] >> 16 : f.s[cb]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(q, s[cb][i], acc[cb][i]);
+      }
+    }
+  }
+
+  // The first weight column of block cb; the byte of a scale dword that is this lane's for it (MXFP4).
+  __device__ __forceinline__ static int column(int cb, int col0, int col1) {
+    return NCB == 1 ? col0 : cb < NCB / 2 ? col0 + 16 * cb : col1 + 16 * (cb - NCB / 2);
+  }
+  __device__ __forceinline__ int scale_byte(int n) const { return PACKED ? (n & 63) / 16 : lg; }
+
+  __device__ __forceinline__ void begin(v4f (&acc)[NCB]) {
+    top = 0;
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) acc[cb] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+  // After blocks kb0 .. kb1 of produce()'s arguments.  MXFP4: if a scale among them was a far one, acc is nothing yet; they are added up
+  // again, out of memory, products under such scales with the scale 2^8 lower and in a sum of their own.  (The stream's copies do not
+  // mind: they only make waits longer.  Keeping `top` costs the stream nothing that shows, where a branch in every block cost up to
+  // 7%: 128 tokens, 8 of 256 experts, 4096 x 1024 packed 354 us, with the branch 378.)
+  template <bool TOKENS>
+  __device__ __forceinline__ void end(v4f (&acc)[NCB], const Plan& p, uint32_t job, uint32_t per_k, int col0, int col1, int kb0, int kb1) {
+    if constexpr (F == kFp4) {
+      if (__builtin_expect(__ballot(top >= kFarScale) == 0, 1)) return;
+      begin(acc);
+      const int64_t rowb = T::row_bytes(side.K), e = p.expert(job);
+      const int KG = side.K / 128;
+      const uint32_t r = (uint32_t)p.route(job, min(l16 & (BR - 1), p.rows(job) - 1));
+      const uint8_t* xr = x + (int64_t)(TOKENS ? r * per_k >> 16 : r) * side.K * 2;
+#pragma unroll 1
+      for (int kb = kb0; kb < kb1; ++kb) {
+        v4i xf[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) xf[d] = *(const v4i*)(xr + kb * T::kXRow + 16 * (4 * lg + d));
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) {
+          const int n = column(cb, col0, col1);
+          const uint8_t* w = side.W + e * side.N * rowb + (PACKED ? (int64_t)(n / 16) * 1024 + (int64_t)kb * wstep + 16 * lane
+                                                                  : (n + l16) * rowb + (int64_t)kb * wstep + 16 * lg);
+          const v4i wf = *(const v4i*)w;
+          const int at = PACKED ? (kb * (side.N / 64) + n / 64) * 64 + lane : (n + l16) * KG + kb;
+          const uint32_t s4 = *(const uint32_t*)(side.S + e * side.N * KG * 4 + 4 * (int64_t)at);
+          const uint32_t e8m0 = s4 >> (8 * scale_byte(n)) & 0xffu;
+          const bool far = e8m0 >= kFarScale && e8m0 != kNanScale;
+          const float scale = __uint_as_float((far ? e8m0 - 8 : e8m0) << 23);
+          v4f s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            s = mma(xf[d], widen_fp4(far ? (uint32_t)wf[d] : 0u, scale), s);
+            acc[cb] = mma(xf[d], widen_fp4(far ? 0u : (uint32_t)wf[d], scale), acc[cb]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[cb][i] = __builtin_fmaf(256.f, s[i], acc[cb][i]);
+        }
       }
     }
   }
@@ -520,8 +546,7 @@ __global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_up_kernel(const
     const uint32_t job = (uint32_t)uniform((int)p.job[u / ncol]);
     const int col = u % ncol * kCols, m = p.rows(job);
     v4f acc[NCB];
-#pragma unroll
-    for (int cb = 0; cb < NCB; ++cb) acc[cb] = v4f{0.f, 0.f, 0.f, 0.f};
+    st.begin(acc);
 #pragma unroll 1
     for (int kb = kb0; kb < kb1; ++kb) {
       typename St::Frags f;
@@ -530,6 +555,7 @@ __global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_up_kernel(const
       full = feed();
       st.multiply(f, acc, kb, col, a.I + col);
     }
+    st.template end<true>(acc, p, job, a.per_k, col, a.I + col, kb0, kb1);
     float* sums = part + buf * C::kPart;
     float* mine = sums + wv * BR * C::kRow;
 #pragma unroll
@@ -597,16 +623,18 @@ __global__ __launch_bounds__(NW < 8 ? 512 : NW * 64) void decode_down_kernel(con
   for (int it = wv; it < items; it += NW) {
     const uint32_t job = (uint32_t)uniform((int)p.job[it / KS]);
     const int ks = it % KS, m = p.rows(job);
-    v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
-    const int kb1 = (ks + 1) * nb / KS;
+    v4f acc[1];
+    const int kb0 = ks * nb / KS, kb1 = (ks + 1) * nb / KS;
+    st.begin(acc);
 #pragma unroll 1
-    for (int kb = ks * nb / KS; kb < kb1; ++kb) {
+    for (int kb = kb0; kb < kb1; ++kb) {
       typename St::Frags f;
       st.arrive(full);
       st.read(f);
       full = feed();
       st.multiply(f, acc, kb, n0, n0);
     }
+    st.template end<false>(acc, p, job, 0, n0, n0, kb0, kb1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (4 * st.lg + i < m) y[(ks * R + p.route(job, 4 * st.lg + i)) * 16 + st.l16] = acc[0][i];
