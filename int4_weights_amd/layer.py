@@ -313,8 +313,9 @@ class MoeDecodeLayer:
         self.Z = torch.empty(max_tokens, self.H, dtype=torch.bfloat16, device=dev)
 
     def forward(self, x, topk_ids, topk_weights, z=None, residual=None):
-        """x bf16 [T, H], topk_ids int32 and topk_weights float32 [T, topk] -> z bf16 [T, H] (default: this layer's buffer),
-        with residual bf16 [T, H] added (it may be z)."""
+        """x bf16 [T, H], topk_ids int32 and topk_weights float32 [T, topk] -> z bf16 [T, H], with residual bf16 [T, H] added
+        (it may be z).  Without z the result lies in this layer's own buffer, where the next such forward overwrites it: whoever
+        keeps it past that (a following step, another layer that shares the object) gives a z."""
         if x.shape[0] > self.max_tokens:
             raise ValueError(f"x has {x.shape[0]} tokens, the layer room for {self.max_tokens}")
         z = self.Z[:x.shape[0]] if z is None else z
@@ -329,7 +330,8 @@ class DenseLinear:
 
     w bf16 [N, K], bias float32 or bf16 [N]; gated: w's rows are gates, then what they gate, and y has N/2 columns.  The
     gradient starts from the pre-activation that forward(..., pre=) keeps: grad_pre gives dP (and the bias's gradient),
-    grad_input and grad_weight take it from there (without activation and bias dP is dy).  Nothing is kept between calls;
+    grad_input and grad_weight take it from there (without activation and bias dP is dy).  K is a multiple of 8, for the two
+    products of the gradient N too (the token count is any).  Nothing is kept between calls;
     a product that splits K and grad_pre take their scratch from torch's allocator, which a graph's capture keeps."""
 
     def __init__(self, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none", gated: bool = False):
