@@ -674,8 +674,11 @@ moe_status moe_quant_act_t(const uint16_t* x, int64_t M, int K, int64_t ldx,
  *     moe_pack_weight_bf16 / _fp8 / _int4 / _fp4 (the scales of the last two too).
  *   1 <= E <= 1024, 1 <= k <= 64, T <= MOE_DECODE_MAX_TOKENS and
  *   T * k <= MOE_DECODE_MAX_ROUTES (more: route, pack and use the grouped
- *   GEMMs); H and I multiples of 128, at most 32768.  x, W13, W2 16-byte, scales
- *   4-byte aligned.  T == 0 is a no-op.
+ *   GEMMs); an expert is read once for every 4, 8 or 16 of its routes (by the mean
+ *   number per expert).  FP8 and 4-bit codes are added up in blocks of 128 before
+ *   their scale is applied: x and h below 2^111 in magnitude.  H and I multiples of
+ *   128, at most 32768.  x, W13, W2 16-byte, scales 4-byte aligned.  T == 0 is a
+ *   no-op.
  *   workspace: moe_experts_decode_workspace_bytes(T, k, I) bytes (h), 16-byte
  *   aligned; calls that overlap in time must not share it. */
 enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8 = 1, MOE_WEIGHTS_INT4 = 2, MOE_WEIGHTS_FP4 = 3 };

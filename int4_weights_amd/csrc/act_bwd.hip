@@ -7,8 +7,9 @@
 // One pass: 8 columns per lane (16-byte loads and stores), kRowsAhead rows' loads in flight per lane; the column sums stay in
 // registers, meet across lanes and waves in a fixed order, and where the rows are cut into several chunks one line of sums per
 // chunk goes to the workspace, where a second launch adds the lines.  A launch costs more than a few hundred rows do, so up to
-// kOneChunk rows are one chunk: narrow strips, 16 waves each, no second launch.  333 x 1536 GELU 5.6 us in a graph (two launches
-// of chunks took 14); 4096 x 2 * 2048 SwiGLU 22 us with the bias, 19 without (84 MB: 4.4 TB/s); 16384 rows 63 us, 5.3 TB/s.
+// kOneChunk rows are one chunk: narrow strips, 16 waves each, no second launch.  333 x 1536 GELU 5.9 us in a graph out of the
+// caches, 7.3 out of HBM (two launches of chunks took 14); 4096 x 2 * 2048 SwiGLU 22 us with the bias, 19 without (84 MB: 4.4 TB/s);
+// 16384 rows 63 us, 5.3 TB/s.
 #include "linear_act.h"
 #include "moe_internal.h"
 

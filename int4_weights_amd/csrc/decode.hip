@@ -21,9 +21,13 @@
 // whatever wave was first, and no partial result goes through memory.
 //
 // Measured (us; TB/s of the active experts' weights): 1 token, 8 of 256 experts, 7168 x 2048, FP8 59.4 (5.9); 61 tokens, 8 of 128,
-// 4096 x 1536, bf16 686 to 720 (6.6 to 6.9), FP8 375 (6.3); 16 tokens, 4096 x 768, 4-bit packed 80 (5.0), row-major 120
-// (copied in pieces of 64 bytes), MXFP4 packed 83.  A plain read of memory reaches 7.3 TB/s.  What bounds it: bytes in flight (the rings, 64 to 110 KB a compute unit), the start and
-// the last round of units, and for 4-bit codes the widening beside the stream.
+// 4096 x 1536, bf16 679 to 694 (6.8 to 7.0), FP8 368 (6.4); 16 tokens, 4096 x 768, 4-bit packed 80 (5.0), row-major 120
+// (copied in pieces of 64 bytes), MXFP4 packed 80, row-major 124.  A plain read of memory reaches 7.3 TB/s.  What bounds it: bytes
+// in flight (the rings, 64 to 110 KB a compute unit), the start and the last round of units, and for 4-bit codes the widening beside
+// the stream.  Two things cost more than the active experts' bytes: an expert with more than BR routes is read once for each of its jobs
+// (Zipf routing of 61 tokens, 8 of 256, 4096 x 1024, FP8: 206 jobs of 149 experts, 4.8 TB/s of the active bytes where uniform
+// routing has 6.1), and from about 600 routes on the routes' tables and lines leave room for fewer rings (128 tokens, 8 of 128, 4096 x
+// 1536: FP8 445, 5.4 TB/s).
 #include "decode_plan.h"
 #include "linear_act.h"
 #include "moe_device.h"
